@@ -295,7 +295,7 @@ def _quantize(x, block_rows):
     amax = _block_max(x, block_rows)
     part, power = torch.frexp(amax / E4M3_MAX)
     power = torch.where(part == 0.5, power - 1, power)
-    scale = torch.where(amax == 0, 1.0, torch.ldexp(torch.ones_like(amax), power.clamp(min=-126)))
+    scale = torch.where(amax == 0, 1.0, ((power.clamp(min=-126) + 127) << 23).view(torch.float32))
     return (x / _spread(scale, *x.shape, block_rows)).to(torch.float8_e4m3fn), scale
 
 
