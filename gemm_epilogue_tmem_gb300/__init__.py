@@ -30,6 +30,10 @@ __all__ = [
     "gf_noalloc_status",
     "gf_swiglu_plan", "gf_swiglu_execute", "gf_dswiglu_plan", "gf_dswiglu_execute",
     "GF_NOALLOC_MAX_PARTIALS",
+    "GF_FP8_EPILOG_NONE", "GF_FP8_EPILOG_SWIGLU_QUANT",
+    "gf_moe_plan", "gf_moe_dispatch_execute", "gf_moe_dispatch_fp8_execute",
+    "gf_moe_dispatch_grad_execute", "gf_moe_combine_execute", "gf_moe_combine_grad_execute",
+    "gf_fp8_quantize", "gf_fp8_matmul_plan", "gf_fp8_matmul_execute",
 ]
 
 # gf_status
@@ -49,6 +53,8 @@ GF_BGRAD_TWO_PASS, GF_BGRAD_ATOMIC = 0, 1
 GF_OPT_BGRAD_MODE, GF_OPT_WAIT_LIMIT_US, GF_OPT_TILE_N, GF_OPT_FAULT_DROP_LOAD = 0, 1, 2, 3
 GF_OPT_KERNEL, GF_OPT_GROUP_M, GF_OPT_L2_HINTS, GF_OPT_SCHEDULE = 4, 5, 6, 7
 GF_OPT_SPLIT_K, GF_OPT_PDL, GF_OPT_RASTER = 8, 9, 10
+# gf_fp8_epilog
+GF_FP8_EPILOG_NONE, GF_FP8_EPILOG_SWIGLU_QUANT = 0, 1
 # fp32 partial sums the allocation-free DRELU_BGRAD entry point can hold
 GF_NOALLOC_MAX_PARTIALS = 2097152
 
@@ -110,6 +116,24 @@ def lib(path: str | None = None):
         L.gf_drelu_bgrad_noalloc.argtypes = [_I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P]
         L.gf_noalloc_status.restype = _I32
         L.gf_noalloc_status.argtypes = [_P]
+        L.gf_moe_plan.restype = _P
+        L.gf_moe_plan.argtypes = [_I64, _I64, _I64, _I64, _I32]
+        L.gf_moe_dispatch_execute.restype = _I32
+        L.gf_moe_dispatch_execute.argtypes = [_P] * 8
+        L.gf_moe_dispatch_fp8_execute.restype = _I32
+        L.gf_moe_dispatch_fp8_execute.argtypes = [_P] * 9
+        L.gf_moe_dispatch_grad_execute.restype = _I32
+        L.gf_moe_dispatch_grad_execute.argtypes = [_P] * 5
+        L.gf_moe_combine_execute.restype = _I32
+        L.gf_moe_combine_execute.argtypes = [_P] * 6
+        L.gf_moe_combine_grad_execute.restype = _I32
+        L.gf_moe_combine_grad_execute.argtypes = [_P] * 9
+        L.gf_fp8_quantize.restype = _I32
+        L.gf_fp8_quantize.argtypes = [_I64, _I64, _I32, _I32, _P, _P, _P, _P]
+        L.gf_fp8_matmul_plan.restype = _P
+        L.gf_fp8_matmul_plan.argtypes = [_I64, _I64, _I64, _I64, _I32, _I32]
+        L.gf_fp8_matmul_execute.restype = _I32
+        L.gf_fp8_matmul_execute.argtypes = [_P] * 11
         _lib = L
     return _lib
 
@@ -275,3 +299,148 @@ def gf_noalloc_status(stream=None) -> int:
     """Synchronise the stream and return the status of the most recent
     gf_drelu_bgrad_noalloc on this device (GF_OK, GF_ERR_DEVICE_TIMEOUT ...)."""
     return int(lib().gf_noalloc_status(_stream(stream)))
+
+
+# ------------------------------------------------------- expert routing, e4m3
+# Tensors of the calls below are checked against the plan: element size and
+# kind, number of elements, contiguous, on a GPU. Raw addresses are not.
+_TENSOR_KINDS = {
+    "i32": ("torch.int32",), "f32": ("torch.float32",),
+    "e4m3": ("torch.float8_e4m3fn", "torch.uint8"),
+    GF_F16: ("torch.float16",), GF_BF16: ("torch.bfloat16",),
+}
+_kinds = {}  # kind -> its torch dtypes
+
+
+def _arg(x, kind, count: int, what: str) -> int | None:
+    """Device address of x, a tensor of `count` elements of `kind` (or an address, or None)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not _kinds:
+        import torch
+        _kinds.update({k: tuple(getattr(torch, n.split(".")[1]) for n in v)
+                       for k, v in _TENSOR_KINDS.items()})
+    if x.dtype not in _kinds[kind] or x.numel() != count or not x.is_contiguous() or not x.is_cuda:
+        raise GfError(GF_ERR_INVALID_VALUE,
+                      f"{what}: a contiguous CUDA tensor of {count} elements of "
+                      f"{' or '.join(_TENSOR_KINDS[kind])} is needed, not {x.dtype} "
+                      f"{tuple(x.shape)}")
+    return x.data_ptr()
+
+
+def _check(rc: int, what: str) -> None:
+    if rc != GF_OK:
+        raise GfError(rc, what)
+
+
+def gf_moe_plan(tokens: int, topk: int, experts: int, hidden: int, dtype: int) -> Plan:
+    """Expert-routing plan: `tokens` rows of `hidden` elements, `topk` of `experts` each."""
+    h = lib().gf_moe_plan(tokens, topk, experts, hidden, dtype)
+    if not h:
+        raise GfError(gf_last_error(), "gf_moe_plan")
+    plan = Plan(h, tokens, experts, hidden, dtype, -3, GF_BIAS_COL, GF_B_KN)
+    plan.topk, plan.slots = topk, tokens * topk
+    return plan
+
+
+def _moe(plan: Plan, what: str) -> None:
+    if not hasattr(plan, "slots"):
+        raise GfError(GF_ERR_INVALID_VALUE, f"{what}: not a plan of gf_moe_plan")
+
+
+def gf_moe_dispatch_execute(plan: Plan, expert, x, offsets, row_of, slot_of, rows,
+                            stream=None) -> None:
+    """Sort the slots by expert and copy the tokens' rows to their places
+    (x and rows None: the sort alone); see include/gf.h."""
+    what = "gf_moe_dispatch_execute"
+    _moe(plan, what)
+    _check(lib().gf_moe_dispatch_execute(
+        plan.handle, _arg(expert, "i32", plan.slots, what), _arg(x, plan.dtype, plan.m * plan.k, what),
+        _arg(offsets, "i32", plan.n + 1, what), _arg(row_of, "i32", plan.slots, what),
+        _arg(slot_of, "i32", plan.slots, what), _arg(rows, plan.dtype, plan.slots * plan.k, what),
+        _stream(stream)), what)
+
+
+def gf_moe_dispatch_fp8_execute(plan: Plan, expert, x, offsets, row_of, slot_of, rows, scale,
+                                stream=None) -> None:
+    """Dispatch with rows quantised to e4m3, one fp32 scale per 128 elements."""
+    what = "gf_moe_dispatch_fp8_execute"
+    _moe(plan, what)
+    _check(lib().gf_moe_dispatch_fp8_execute(
+        plan.handle, _arg(expert, "i32", plan.slots, what), _arg(x, plan.dtype, plan.m * plan.k, what),
+        _arg(offsets, "i32", plan.n + 1, what), _arg(row_of, "i32", plan.slots, what),
+        _arg(slot_of, "i32", plan.slots, what), _arg(rows, "e4m3", plan.slots * plan.k, what),
+        _arg(scale, "f32", plan.slots * -(-plan.k // 128), what), _stream(stream)), what)
+
+
+def gf_moe_dispatch_grad_execute(plan: Plan, row_of, d_rows, d_x, stream=None) -> None:
+    """d_x[t] = sum of its slots' d_rows."""
+    what = "gf_moe_dispatch_grad_execute"
+    _moe(plan, what)
+    _check(lib().gf_moe_dispatch_grad_execute(
+        plan.handle, _arg(row_of, "i32", plan.slots, what),
+        _arg(d_rows, plan.dtype, plan.slots * plan.k, what),
+        _arg(d_x, plan.dtype, plan.m * plan.k, what), _stream(stream)), what)
+
+
+def gf_moe_combine_execute(plan: Plan, row_of, weight, rows, out, stream=None) -> None:
+    """out[t] = sum of its slots' rows, weighted."""
+    what = "gf_moe_combine_execute"
+    _moe(plan, what)
+    _check(lib().gf_moe_combine_execute(
+        plan.handle, _arg(row_of, "i32", plan.slots, what), _arg(weight, "f32", plan.slots, what),
+        _arg(rows, plan.dtype, plan.slots * plan.k, what),
+        _arg(out, plan.dtype, plan.m * plan.k, what), _stream(stream)), what)
+
+
+def gf_moe_combine_grad_execute(plan: Plan, offsets, row_of, weight, rows, d_out, d_rows, d_weight,
+                                stream=None) -> None:
+    """Gradients of combine: d_rows and d_weight."""
+    what = "gf_moe_combine_grad_execute"
+    _moe(plan, what)
+    _check(lib().gf_moe_combine_grad_execute(
+        plan.handle, _arg(offsets, "i32", plan.n + 1, what), _arg(row_of, "i32", plan.slots, what),
+        _arg(weight, "f32", plan.slots, what), _arg(rows, plan.dtype, plan.slots * plan.k, what),
+        _arg(d_out, plan.dtype, plan.m * plan.k, what),
+        _arg(d_rows, plan.dtype, plan.slots * plan.k, what),
+        _arg(d_weight, "f32", plan.slots, what), _stream(stream)), what)
+
+
+def gf_fp8_quantize(m: int, k: int, dtype: int, block_rows: int, x, q, scale, stream=None) -> None:
+    """e4m3 values and one power-of-two scale per block of block_rows x 128."""
+    what = "gf_fp8_quantize"
+    if dtype not in (GF_F16, GF_BF16) or block_rows < 1:
+        raise GfError(GF_ERR_INVALID_VALUE, what)
+    blocks = -(-m // block_rows) * -(-k // 128)
+    _check(lib().gf_fp8_quantize(m, k, dtype, block_rows, _arg(x, dtype, m * k, what),
+                                 _arg(q, "e4m3", m * k, what), _arg(scale, "f32", blocks, what),
+                                 _stream(stream)), what)
+
+
+def gf_fp8_matmul_plan(m: int, n: int, k: int, groups: int, dtype: int,
+                       epilog: int = GF_FP8_EPILOG_NONE) -> Plan:
+    """Block-scaled e4m3 product plan: m rows in `groups` groups, each with a B [n, k] of its own."""
+    h = lib().gf_fp8_matmul_plan(m, n, k, groups, dtype, epilog)
+    if not h:
+        raise GfError(gf_last_error(), "gf_fp8_matmul_plan")
+    plan = Plan(h, m, n, k, dtype, -4, GF_BIAS_COL, GF_B_NK)
+    plan.groups, plan.quant = groups, epilog == GF_FP8_EPILOG_SWIGLU_QUANT
+    plan.kb, plan.nb = -(-k // 128), -(-n // 128)
+    return plan
+
+
+def gf_fp8_matmul_execute(plan: Plan, A, a_scale, B, b_scale, B2=None, b2_scale=None, offsets=None,
+                          out=None, out_scale=None, stream=None) -> None:
+    """Enqueue the planned product; B2 and out_scale for GF_FP8_EPILOG_SWIGLU_QUANT."""
+    what = "gf_fp8_matmul_execute"
+    if not hasattr(plan, "groups"):
+        raise GfError(GF_ERR_INVALID_VALUE, f"{what}: not a plan of gf_fp8_matmul_plan")
+    m, n, k, groups = plan.m, plan.n, plan.k, plan.groups
+    scales = groups * plan.nb * plan.kb
+    _check(lib().gf_fp8_matmul_execute(
+        plan.handle, _arg(A, "e4m3", m * k, what), _arg(a_scale, "f32", m * plan.kb, what),
+        _arg(B, "e4m3", groups * n * k, what), _arg(b_scale, "f32", scales, what),
+        _arg(B2, "e4m3", groups * n * k, what), _arg(b2_scale, "f32", scales, what),
+        _arg(offsets, "i32", groups + 1, what),
+        _arg(out, "e4m3" if plan.quant else plan.dtype, m * n, what),
+        _arg(out_scale, "f32", m * plan.nb, what), _stream(stream)), what)

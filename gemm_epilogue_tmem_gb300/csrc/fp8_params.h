@@ -1,0 +1,45 @@
+// Parameter block and launchers of the block-scaled e4m3 products.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gf {
+
+constexpr int kFp8MaxGroups = 1024;
+
+struct Fp8Params {
+  int32_t M, N, K;          // rows of all groups, columns of one B, inner length
+  int32_t groups;
+  int32_t num_k_blocks;     // blocks of 128
+  int32_t num_n_blocks;     // scale blocks of 128 columns
+  const int32_t* offsets;   // [groups + 1], NULL: one group of all rows
+  const float* a_scale;     // [M][num_k_blocks]
+  const float* b_scale;     // [groups][num_n_blocks][num_k_blocks]
+  const float* b2_scale;
+  void* out;                // 16-bit [M][N], or e4m3 bytes
+  float* out_scale;         // [M][num_n_blocks]
+  int32_t* status;
+  uint64_t wait_limit_ns;
+  int32_t drop_load;        // test hook: 1-based index of a stage load to skip (0: none)
+};
+
+struct Fp8LaunchArgs {
+  const CUtensorMap* tmA;   // the rows
+  const CUtensorMap* tmB;   // B, and B2 (else = tmB)
+  const CUtensorMap* tmB2;
+  const Fp8Params* params;
+  int grid;
+  int bf16;
+  int dual;                 // SwiGLU: two products, e4m3 out
+  int tile_rows;            // token rows of a tile of the narrow kernel
+  int pdl;
+  cudaStream_t stream;
+};
+
+// the narrow kernel: 128 columns of B x tile_rows rows per tile
+cudaError_t launch_fp8_narrow(const Fp8LaunchArgs& a);
+int fp8_narrow_stages(int tile_rows, int dual);
+
+}  // namespace gf

@@ -1,0 +1,57 @@
+// Host-side view of the expert-routing and quantising kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gf {
+
+struct MoeParams {
+  int32_t tokens, topk, experts;
+  int64_t hidden;
+  int32_t slots;         // tokens * topk
+  int32_t chunk_tokens;  // tokens per CTA of the sort
+  int32_t num_chunks;
+  int32_t one_pass;      // 1: every CTA counts all slots; 0: counts from `counts`
+  int32_t segments;      // CTAs that share the copies of one chunk (along hidden)
+  int32_t* counts;       // [num_chunks][experts], written by the count kernel
+  const int32_t* expert;
+  int32_t* offsets;
+  int32_t* row_of;
+  int32_t* slot_of;
+  const void* x;
+  void* rows;
+  float* scale;
+};
+
+enum MoeCopy : int { MOE_SORT_ONLY = 0, MOE_COPY = 1, MOE_COPY_FP8 = 2 };
+
+// most tokens of a chunk: its slots' rows are held in shared memory
+int moe_max_chunk_slots();
+cudaError_t launch_moe_count(const MoeParams& p, cudaStream_t stream, int pdl);
+cudaError_t launch_moe_dispatch(const MoeParams& p, int copy, int bf16, cudaStream_t stream,
+                                int pdl);
+
+struct GatherParams {
+  int32_t tokens, topk;
+  int64_t hidden;
+  int32_t slots;
+  const int32_t* offsets;  // gradient: its entry `experts` bounds the rows with a slot
+  int32_t experts;
+  const int32_t* row_of;
+  const float* weight;     // NULL: ones
+  const void* rows;
+  const void* d_out;
+  void* out;               // forward: [tokens, hidden]; gradient: d_rows
+  float* d_weight;
+};
+
+cudaError_t launch_moe_gather(const GatherParams& p, int bf16, int sms, cudaStream_t stream,
+                              int pdl);
+cudaError_t launch_moe_combine_grad(const GatherParams& p, int bf16, cudaStream_t stream,
+                                    int pdl);
+
+cudaError_t launch_fp8_quantize(int64_t m, int64_t k, int bf16, int block_rows, const void* x,
+                                void* q, float* scale, int sms, cudaStream_t stream, int pdl);
+
+}  // namespace gf

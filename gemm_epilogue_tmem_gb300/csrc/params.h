@@ -23,7 +23,14 @@ enum Epi : int {
   EPI_SWIGLU = 8,       // h = silu(x Wg^T) * (x Wu^T): two B operands, two accumulators
   EPI_SWIGLU_SAVE = 9,  // ... and g, u saved for the backward
   EPI_DSWIGLU = 10,     // d_gate, d_up of h = silu(g) * u from dh = dout Wd
+  // plans of the other operators (the codes above are the 16-bit GEMM plans)
+  EPI_FP8 = 11,               // block-scaled e4m3 product, 16-bit out
+  EPI_FP8_SWIGLU_QUANT = 12,  // ... gate+up SwiGLU, e4m3 out
+  EPI_MOE = 13,               // expert routing
 };
+
+// a plan of gf_fp8_matmul_plan
+GF_HD constexpr bool epi_fp8(int epi) { return epi == EPI_FP8 || epi == EPI_FP8_SWIGLU_QUANT; }
 
 // Shared-memory budget of one CTA (227 KB) and the ring depth that fills it:
 // 1 KB of alignment slack, 256 B of barriers, the bias-gradient scratch, then

@@ -21,61 +21,8 @@
 #include "gf.h"
 #include "launch.h"
 #include "params.h"
+#include "plan.h"
 #include "runtime_internal.h"
-
-struct gf_plan {
-  int64_t m, n, k;
-  gf_dtype dtype;
-  int epi;               // gf::Epi code (the public gf_epilog values, plus SwiGLU forms)
-  gf_bias_axis bias_axis;
-  gf_b_layout b_layout;
-  int device;
-  int num_sms;
-  int tile_n;
-  int forced_tile_n;
-  int forced_kernel;     // 0 auto, 1 single CTA, 2 CTA pair, 3 CTA pair with 256 x 512 tiles
-  int forced_group_m;    // 0 auto, else row (or column) blocks per raster group
-  int forced_raster;     // 0 auto, 1 groups of row blocks, 2 groups of column blocks
-  int raster_n;          // 1: raster groups of column blocks (B panels stay in L2)
-  int l2_hint_a, l2_hint_b;  // L2 eviction policy of the A / B loads (0 none, 1 first, 2 last)
-  int one_tile_per_cta;  // 1: grid of one tile per CTA (pair); the hardware orders the tiles
-  int static_schedule;   // 1: persistent CTA pairs walk every gridDim-th tile (default: counter)
-  int pair;              // the plan uses the CTA-pair kernel
-  int wide;              // ... with 256 x 512 tiles
-  int max_pair_clusters; // resident CTA pairs (0: the pair kernel cannot run)
-  int stages;
-  int grid;
-  int num_m_blocks, num_n_blocks, num_k_blocks, num_tiles, group_m;
-  gf_bgrad_mode bgrad_mode;
-  uint64_t wait_limit_ns;
-  int drop_load;
-  int32_t* d_status;     // device status word (bounded-wait time-outs)
-  float* d_partials;     // [num_m_blocks][n] fp32, DRELU_BGRAD two-pass only
-  size_t partial_bytes;
-  int forced_split;      // 0 the plan's choice, 1 no split, else k-splits per tile
-  int split_from;        // CTA-pair split k: the first tile split into k-split units
-  int k_splits;          // single-CTA kernel: CTAs sharing the k-blocks of one tile
-  int kb_per_split;
-  void* d_splitk;        // split-k partial sums, then the per-tile counters
-  size_t splitk_bytes;   // capacity of d_splitk
-  size_t splitk_cnt_offset;
-  int pdl;               // 1: launches overlap their set-up with the previous kernel
-  // Tensor maps of the last execute, reused while the operand pointers and
-  // the plan's tiling are unchanged (encoding them is host work on every
-  // call otherwise). `gen` counts tiling changes; the cache is valid for
-  // cache_gen == gen.
-  uint64_t gen;
-  uint64_t cache_gen;
-  bool cache_valid;
-  const void* cache_A;
-  const void* cache_B;
-  const void* cache_B2;
-  const void* cache_out;
-  const void* cache_aux;
-  bool cache_b_mn_3d;
-  CUtensorMap cache_tmA, cache_tmB, cache_tmB2, cache_tmOut, cache_tmAux;
-  std::mutex cache_mu;
-};
 
 namespace {
 
@@ -747,6 +694,80 @@ bool runtime_encode_2d(CUtensorMap* map, const void* ptr, gf_dtype dt, uint64_t 
   return g_encode != nullptr && encode_2d(map, ptr, dt, inner, outer, box_inner, box_outer);
 }
 
+bool runtime_encode_2d_u8(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer,
+                          uint32_t box_inner, uint32_t box_outer) {
+  load_driver_entry_points();
+  if (!g_encode) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+gf_status runtime_device(int* dev, int* sms) {
+  const gf_status st = current_device(dev);
+  if (st != GF_OK) return st;
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) {
+    cudaGetLastError();
+    return GF_ERR_CUDA;
+  }
+  return major == 10 && minor == 3 ? GF_OK : GF_ERR_UNSUPPORTED;
+}
+
+gf_plan* runtime_new_plan(int epi, gf_dtype dtype, size_t work_bytes) {
+  g_last = GF_OK;
+  int dev = 0, sms = 0;
+  const gf_status st = runtime_device(&dev, &sms);
+  if (st != GF_OK) {
+    fail(st);
+    return nullptr;
+  }
+  if (cudaSetDevice(dev) != cudaSuccess) {
+    fail(GF_ERR_CUDA);
+    return nullptr;
+  }
+  gf_plan* p = new (std::nothrow) gf_plan();
+  if (!p) {
+    fail(GF_ERR_OUT_OF_MEMORY);
+    return nullptr;
+  }
+  p->epi = epi;
+  p->dtype = dtype;
+  p->device = dev;
+  p->num_sms = sms;
+  p->pdl = 1;
+  p->k_splits = 1;
+  p->wait_limit_ns = 2000000000ull;
+  const char* env_wait = getenv("GF_WAIT_LIMIT_US");
+  if (env_wait) {
+    const long long us = atoll(env_wait);
+    if (us >= 1000 && us <= 600000000) p->wait_limit_ns = static_cast<uint64_t>(us) * 1000ull;
+  }
+  gf_status got = GF_OK;
+  if (cudaMalloc(&p->d_status, 256) != cudaSuccess ||
+      (work_bytes > 0 && cudaMalloc(&p->d_work, work_bytes) != cudaSuccess)) {
+    got = GF_ERR_OUT_OF_MEMORY;
+  } else if (cudaMemset(p->d_status, 0, 256) != cudaSuccess ||
+             (work_bytes > 0 && cudaMemset(p->d_work, 0, work_bytes) != cudaSuccess)) {
+    got = GF_ERR_CUDA;
+  }
+  if (got != GF_OK) {
+    cudaGetLastError();
+    gf_plan_free(p);
+    fail(got);
+    return nullptr;
+  }
+  p->work_bytes = work_bytes;
+  return p;
+}
+
 }  // namespace gf
 
 extern "C" {
@@ -795,8 +816,26 @@ GF_API gf_plan* gf_matmul_plan(int64_t m, int64_t n, int64_t k, gf_dtype dtype, 
   return gf_matmul_plan_ex(m, n, k, dtype, epilog, bias_axis, GF_B_KN);
 }
 
+// which options a plan of another operator than the 16-bit GEMM takes
+static gf_status epi_option_check(const gf_plan* p, gf_option option) {
+  if (option == GF_OPT_PDL) return GF_OK;
+  if (gf::epi_fp8(p->epi) && (option == GF_OPT_KERNEL || option == GF_OPT_WAIT_LIMIT_US ||
+                              option == GF_OPT_FAULT_DROP_LOAD))
+    return GF_OK;
+  return option >= GF_OPT_BGRAD_MODE && option <= GF_OPT_RASTER ? GF_ERR_UNSUPPORTED
+                                                                : GF_ERR_INVALID_VALUE;
+}
+
 GF_API gf_status gf_plan_set_option(gf_plan* p, gf_option option, int64_t value) {
   if (!p) return fail(GF_ERR_INVALID_VALUE);
+  if (p->epi >= gf::EPI_FP8) {
+    const gf_status st = epi_option_check(p, option);
+    if (st != GF_OK) return fail(st);
+    if (option == GF_OPT_KERNEL) {
+      const gf_status k = gf::runtime_fp8_set_kernel(p, value);
+      return k == GF_OK ? GF_OK : fail(k);
+    }
+  }
   switch (option) {
     case GF_OPT_BGRAD_MODE:
       if (value != GF_BGRAD_TWO_PASS && value != GF_BGRAD_ATOMIC) return fail(GF_ERR_INVALID_VALUE);
@@ -929,6 +968,14 @@ GF_API gf_status gf_matmul_autotune(gf_plan* p, const void* A, const void* B, co
 GF_API gf_status gf_plan_describe(const gf_plan* p, int32_t* tile_m, int32_t* tile_n,
                                   int32_t* stages, int32_t* grid, int64_t* workspace_bytes) {
   if (!p) return fail(GF_ERR_INVALID_VALUE);
+  if (p->epi >= gf::EPI_FP8) {
+    if (tile_m) *tile_m = p->epi == gf::EPI_MOE ? p->chunk_tokens : p->tile_rows;
+    if (tile_n) *tile_n = p->tile_n;
+    if (stages) *stages = p->stages;
+    if (grid) *grid = p->grid;
+    if (workspace_bytes) *workspace_bytes = static_cast<int64_t>(p->work_bytes) + 256;
+    return GF_OK;
+  }
   if (tile_m) *tile_m = p->pair ? 2 * kBM : kBM;
   if (tile_n) *tile_n = p->tile_n;
   if (stages) *stages = p->stages;
@@ -940,6 +987,10 @@ GF_API gf_status gf_plan_describe(const gf_plan* p, int32_t* tile_m, int32_t* ti
 
 GF_API gf_status gf_plan_launches(const gf_plan* p, int32_t* launches) {
   if (!p || !launches) return fail(GF_ERR_INVALID_VALUE);
+  if (p->epi == gf::EPI_MOE) {
+    *launches = p->one_pass ? 1 : 2;
+    return GF_OK;
+  }
   const bool finalize = has_bgrad(p->epi) && p->bgrad_mode != GF_BGRAD_ATOMIC;
   *launches = p->m == 0 || p->n == 0 ? 0 : 1 + (finalize ? 1 : 0);
   return GF_OK;
@@ -1007,6 +1058,7 @@ GF_API void gf_plan_free(gf_plan* p) {
   cudaSetDevice(p->device);
   if (p->d_partials) cudaFree(p->d_partials);
   if (p->d_splitk) cudaFree(p->d_splitk);
+  if (p->d_work) cudaFree(p->d_work);
   if (p->d_status) cudaFree(p->d_status);
   delete p;
 }

@@ -1,0 +1,135 @@
+// Host entry points of the block-scaled e4m3 products: checks of the
+// arguments, the plan's tiles, tensor maps and launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "fp8_params.h"
+#include "gf.h"
+#include "params.h"
+#include "plan.h"
+#include "runtime_internal.h"
+
+namespace {
+
+using gf::runtime_fail;
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+
+bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Tiles of the plan: 16 rows when the groups have few rows on average, else 64.
+void plan_tiles(gf_plan* p) {
+  const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
+  const int64_t rows_per_group = p->m / p->groups;
+  const int kernel = p->forced_kernel != 0 ? p->forced_kernel : rows_per_group <= 16 ? 1 : 2;
+  p->tile_rows = kernel == 1 ? 16 : 64;
+  p->tile_n = 128;
+  p->stages = gf::fp8_narrow_stages(p->tile_rows, dual);
+  p->grid = p->num_sms;
+}
+
+}  // namespace
+
+namespace gf {
+
+gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value) {
+  if (value < 0 || value > 2) return GF_ERR_INVALID_VALUE;
+  p->forced_kernel = static_cast<int>(value);
+  plan_tiles(p);
+  return GF_OK;
+}
+
+}  // namespace gf
+
+extern "C" {
+
+GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t groups,
+                                   gf_dtype dtype, gf_fp8_epilog epilog) {
+  if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim || groups < 1 ||
+      groups > gf::kFp8MaxGroups || (dtype != GF_F16 && dtype != GF_BF16) ||
+      (epilog != GF_FP8_EPILOG_NONE && epilog != GF_FP8_EPILOG_SWIGLU_QUANT)) {
+    runtime_fail(GF_ERR_INVALID_VALUE);
+    return nullptr;
+  }
+  const bool dual = epilog == GF_FP8_EPILOG_SWIGLU_QUANT;
+  // rows of B over all groups and the tiles of 16 rows x 128 columns are int32
+  // in the kernels
+  if (k % 16 != 0 || n % (dual ? 16 : 8) != 0 || groups * n > kMaxDim ||
+      (m / 16 + groups + 1) * ((n + 127) / 128) > kMaxDim) {
+    runtime_fail(GF_ERR_UNSUPPORTED);
+    return nullptr;
+  }
+  gf_plan* p = gf::runtime_new_plan(dual ? gf::EPI_FP8_SWIGLU_QUANT : gf::EPI_FP8, dtype, 0);
+  if (!p) return nullptr;
+  p->m = m;
+  p->n = n;
+  p->k = k;
+  p->groups = groups;
+  plan_tiles(p);
+  return p;
+}
+
+GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const float* a_scale,
+                                       const void* B, const float* b_scale, const void* B2,
+                                       const float* b2_scale, const int32_t* offsets, void* out,
+                                       float* out_scale, struct CUstream_st* stream) {
+  if (!p || !gf::epi_fp8(p->epi)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  const bool dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT;
+  const bool empty = p->m == 0 || p->n == 0;
+  if (!empty) {
+    if (!given(out) || (dual && !given(out_scale))) return runtime_fail(GF_ERR_INVALID_VALUE);
+    if (p->k > 0 && (!given(A) || !given(a_scale) || !given(B) || !given(b_scale)))
+      return runtime_fail(GF_ERR_INVALID_VALUE);
+    if (p->k > 0 && dual && (!given(B2) || !given(b2_scale)))
+      return runtime_fail(GF_ERR_INVALID_VALUE);
+    if (offsets == nullptr ? p->groups != 1 : !given(offsets))
+      return runtime_fail(GF_ERR_INVALID_VALUE);
+  }
+  if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  if (empty) return GF_OK;
+
+  CUtensorMap tmA, tmB, tmB2;
+  memset(&tmA, 0, sizeof tmA);
+  memset(&tmB, 0, sizeof tmB);
+  memset(&tmB2, 0, sizeof tmB2);
+  if (p->k > 0) {
+    const uint64_t b_rows = static_cast<uint64_t>(p->groups) * p->n;
+    if (!gf::runtime_encode_2d_u8(&tmA, A, p->k, p->m, 128, p->tile_rows) ||
+        !gf::runtime_encode_2d_u8(&tmB, B, p->k, b_rows, 128, 128) ||
+        (dual && !gf::runtime_encode_2d_u8(&tmB2, B2, p->k, b_rows, 128, 128)))
+      return runtime_fail(GF_ERR_INVALID_VALUE);
+  }
+  gf::Fp8Params prm = {};
+  prm.M = static_cast<int32_t>(p->m);
+  prm.N = static_cast<int32_t>(p->n);
+  prm.K = static_cast<int32_t>(p->k);
+  prm.groups = static_cast<int32_t>(p->groups);
+  prm.num_k_blocks = static_cast<int32_t>((p->k + 127) / 128);
+  prm.num_n_blocks = static_cast<int32_t>((p->n + 127) / 128);
+  prm.offsets = offsets;
+  prm.a_scale = a_scale;
+  prm.b_scale = b_scale;
+  prm.b2_scale = b2_scale;
+  prm.out = out;
+  prm.out_scale = out_scale;
+  prm.status = p->d_status;
+  prm.wait_limit_ns = p->wait_limit_ns;
+  prm.drop_load = p->drop_load;
+
+  gf::Fp8LaunchArgs la = {};
+  la.tmA = &tmA;
+  la.tmB = &tmB;
+  la.tmB2 = dual ? &tmB2 : &tmB;
+  la.params = &prm;
+  la.grid = p->grid;
+  la.bf16 = p->dtype == GF_BF16 ? 1 : 0;
+  la.dual = dual ? 1 : 0;
+  la.tile_rows = p->tile_rows;
+  la.pdl = p->pdl;
+  la.stream = reinterpret_cast<cudaStream_t>(stream);
+  return gf::launch_fp8_narrow(la) == cudaSuccess ? GF_OK : runtime_fail(GF_ERR_CUDA);
+}
+
+}  // extern "C"

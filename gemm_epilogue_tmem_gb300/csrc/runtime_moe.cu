@@ -1,0 +1,216 @@
+// Host entry points of expert routing and of the e4m3 quantiser: checks of the
+// arguments, the plan's chunks, launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gf.h"
+#include "moe.h"
+#include "params.h"
+#include "plan.h"
+#include "runtime_internal.h"
+
+namespace {
+
+using gf::runtime_fail;
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+
+bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Slots up to which every CTA counts all of them itself, without the count
+// kernel.
+constexpr int64_t kOnePassSlots = 4096;
+
+bool is_moe(const gf_plan* p) { return p != nullptr && p->epi == gf::EPI_MOE; }
+
+gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32_t* offsets,
+                   int32_t* row_of, int32_t* slot_of, void* rows, float* scale, int copy,
+                   cudaStream_t st) {
+  const bool some = p->m > 0;
+  if (!given(offsets)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (some && (!given(expert) || !given(row_of) || !given(slot_of)))
+    return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (some && copy != gf::MOE_SORT_ONLY && (!given(x) || !given(rows)))
+    return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (some && copy == gf::MOE_COPY_FP8 && !given(scale)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  gf::MoeParams prm = {};
+  prm.tokens = static_cast<int32_t>(p->m);
+  prm.topk = static_cast<int32_t>(p->topk);
+  prm.experts = static_cast<int32_t>(p->experts);
+  prm.hidden = p->k;
+  prm.slots = static_cast<int32_t>(p->m * p->topk);
+  prm.chunk_tokens = p->chunk_tokens;
+  prm.num_chunks = p->num_chunks;
+  prm.one_pass = p->one_pass;
+  prm.counts = static_cast<int32_t*>(p->d_work);
+  prm.expert = expert;
+  prm.offsets = offsets;
+  prm.row_of = row_of;
+  prm.slot_of = slot_of;
+  prm.x = x;
+  prm.rows = rows;
+  prm.scale = scale;
+  // CTAs that share a chunk's copies: as many as have work for their 16 warps
+  // (512 elements of a row at a time), while the grid has fewer than two CTAs
+  // per SM
+  const int64_t items = p->chunk_tokens * ((p->k + 511) / 512);
+  int64_t seg = (items + 15) / 16;
+  const int64_t room = 2 * p->num_sms / p->num_chunks;
+  seg = seg > room ? room : seg;
+  prm.segments = static_cast<int32_t>(seg < 1 ? 1 : seg);
+  const int bf16 = p->dtype == GF_BF16 ? 1 : 0;
+  if (!p->one_pass && gf::launch_moe_count(prm, st, p->pdl) != cudaSuccess)
+    return runtime_fail(GF_ERR_CUDA);
+  if (gf::launch_moe_dispatch(prm, copy, bf16, st, p->pdl) != cudaSuccess)
+    return runtime_fail(GF_ERR_CUDA);
+  return GF_OK;
+}
+
+gf::GatherParams gather_params(const gf_plan* p, const int32_t* row_of, const float* weight,
+                               const void* rows, void* out) {
+  gf::GatherParams g = {};
+  g.tokens = static_cast<int32_t>(p->m);
+  g.topk = static_cast<int32_t>(p->topk);
+  g.hidden = p->k;
+  g.slots = static_cast<int32_t>(p->m * p->topk);
+  g.experts = static_cast<int32_t>(p->experts);
+  g.row_of = row_of;
+  g.weight = weight;
+  g.rows = rows;
+  g.out = out;
+  return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
+                            gf_dtype dtype) {
+  if (tokens < 0 || tokens > kMaxDim || topk < 1 || topk > 64 || experts < 1 || experts > 1024 ||
+      hidden < 1 || hidden > kMaxDim || tokens * topk > kMaxDim ||
+      (dtype != GF_F16 && dtype != GF_BF16)) {
+    runtime_fail(GF_ERR_INVALID_VALUE);
+    return nullptr;
+  }
+  int dev = 0, sms = 0;
+  const gf_status st = gf::runtime_device(&dev, &sms);
+  if (st != GF_OK) {
+    runtime_fail(st);
+    return nullptr;
+  }
+  // one chunk of tokens per SM, as far as its slots fit the kernel's table
+  int64_t chunk = (tokens + sms - 1) / sms;
+  const int64_t most = gf::moe_max_chunk_slots() / topk;
+  chunk = chunk > most ? most : chunk < 1 ? 1 : chunk;
+  const int64_t chunks = tokens == 0 ? 1 : (tokens + chunk - 1) / chunk;
+  const bool one_pass = tokens * topk <= kOnePassSlots;
+  gf_plan* p = gf::runtime_new_plan(gf::EPI_MOE, dtype,
+                                    one_pass ? 0 : static_cast<size_t>(chunks * experts) * 4);
+  if (!p) return nullptr;
+  p->m = tokens;
+  p->k = hidden;
+  p->n = experts;
+  p->topk = topk;
+  p->experts = experts;
+  p->chunk_tokens = static_cast<int>(chunk);
+  p->num_chunks = static_cast<int>(chunks);
+  p->one_pass = one_pass ? 1 : 0;
+  p->grid = static_cast<int>(chunks);
+  return p;
+}
+
+GF_API gf_status gf_moe_dispatch_execute(const gf_plan* p, const int32_t* expert, const void* x,
+                                         int32_t* offsets, int32_t* row_of, int32_t* slot_of,
+                                         void* rows, struct CUstream_st* stream) {
+  if (!is_moe(p)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  const int copy = x == nullptr && rows == nullptr ? gf::MOE_SORT_ONLY : gf::MOE_COPY;
+  return dispatch(p, expert, x, offsets, row_of, slot_of, rows, nullptr, copy,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+GF_API gf_status gf_moe_dispatch_fp8_execute(const gf_plan* p, const int32_t* expert,
+                                             const void* x, int32_t* offsets, int32_t* row_of,
+                                             int32_t* slot_of, void* rows, float* scale,
+                                             struct CUstream_st* stream) {
+  if (!is_moe(p)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (p->k % 16 != 0) return runtime_fail(GF_ERR_UNSUPPORTED);
+  return dispatch(p, expert, x, offsets, row_of, slot_of, rows, scale, gf::MOE_COPY_FP8,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+GF_API gf_status gf_moe_dispatch_grad_execute(const gf_plan* p, const int32_t* row_of,
+                                              const void* d_rows, void* d_x,
+                                              struct CUstream_st* stream) {
+  if (!is_moe(p)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (p->m == 0) return GF_OK;
+  if (!given(row_of) || !given(d_rows) || !given(d_x)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  const gf::GatherParams g = gather_params(p, row_of, nullptr, d_rows, d_x);
+  return gf::launch_moe_gather(g, p->dtype == GF_BF16, p->num_sms,
+                               reinterpret_cast<cudaStream_t>(stream), p->pdl) == cudaSuccess
+             ? GF_OK
+             : runtime_fail(GF_ERR_CUDA);
+}
+
+GF_API gf_status gf_moe_combine_execute(const gf_plan* p, const int32_t* row_of,
+                                        const float* weight, const void* rows, void* out,
+                                        struct CUstream_st* stream) {
+  if (!is_moe(p)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (p->m == 0) return GF_OK;
+  if (!given(row_of) || !given(weight) || !given(rows) || !given(out))
+    return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  const gf::GatherParams g = gather_params(p, row_of, weight, rows, out);
+  return gf::launch_moe_gather(g, p->dtype == GF_BF16, p->num_sms,
+                               reinterpret_cast<cudaStream_t>(stream), p->pdl) == cudaSuccess
+             ? GF_OK
+             : runtime_fail(GF_ERR_CUDA);
+}
+
+GF_API gf_status gf_moe_combine_grad_execute(const gf_plan* p, const int32_t* offsets,
+                                             const int32_t* row_of, const float* weight,
+                                             const void* rows, const void* d_out, void* d_rows,
+                                             float* d_weight, struct CUstream_st* stream) {
+  if (!is_moe(p)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (p->m == 0) return GF_OK;
+  if (!given(offsets) || !given(row_of) || !given(weight) || !given(rows) || !given(d_out) ||
+      !given(d_rows) || !given(d_weight))
+    return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  gf::GatherParams g = gather_params(p, row_of, weight, rows, d_rows);
+  g.offsets = offsets;
+  g.d_out = d_out;
+  g.d_weight = d_weight;
+  return gf::launch_moe_combine_grad(g, p->dtype == GF_BF16,
+                                     reinterpret_cast<cudaStream_t>(stream),
+                                     p->pdl) == cudaSuccess
+             ? GF_OK
+             : runtime_fail(GF_ERR_CUDA);
+}
+
+GF_API gf_status gf_fp8_quantize(int64_t m, int64_t k, gf_dtype dtype, int32_t block_rows,
+                                 const void* x, void* q, float* scale,
+                                 struct CUstream_st* stream) {
+  if (m < 0 || k < 0 || m > kMaxDim || k > kMaxDim || (dtype != GF_F16 && dtype != GF_BF16) ||
+      (block_rows != 1 && block_rows != 128))
+    return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (k % 16 != 0) return runtime_fail(GF_ERR_UNSUPPORTED);
+  // one CTA per 128 x 128 block
+  if (((m + 127) / 128) * ((k + 127) / 128) > kMaxDim) return runtime_fail(GF_ERR_UNSUPPORTED);
+  const bool empty = m == 0 || k == 0;
+  if (!empty && (!given(x) || !given(q) || !given(scale)))
+    return runtime_fail(GF_ERR_INVALID_VALUE);
+  int dev = 0, sms = 0;
+  const gf_status st = gf::runtime_device(&dev, &sms);
+  if (st != GF_OK) return runtime_fail(st);
+  if (empty) return GF_OK;
+  if (cudaSetDevice(dev) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  return gf::launch_fp8_quantize(m, k, dtype == GF_BF16, block_rows, x, q, scale, sms,
+                                 reinterpret_cast<cudaStream_t>(stream), 1) == cudaSuccess
+             ? GF_OK
+             : runtime_fail(GF_ERR_CUDA);
+}
+
+}  // extern "C"

@@ -213,6 +213,141 @@ GF_API gf_status gf_dswiglu_execute(const gf_plan* plan, const void* dout, const
                                     struct CUstream_st* stream);
 
 /*
+ * Mixture-of-experts routing: the rows of a token batch, sorted by expert and
+ * back.
+ *
+ * A router gives each of `tokens` tokens `topk` experts, expert[t][s], and
+ * weights, weight[t][s]. Slot i = t * topk + s is kept when 0 <= expert < experts,
+ * and dropped otherwise (-1: past an expert's capacity). The kept slots,
+ * ordered by expert and within one expert by i (a stable sort), are the rows:
+ *   offsets[e]  = the first row of expert e; offsets[experts] = kept slots
+ *   row_of[t][s] = the slot's row, -1 when dropped
+ *   slot_of[r]  = the slot of row r, -1 for rows >= offsets[experts]
+ *   dispatch      rows[row_of[t][s]] = x[t]            (rows without a slot: 0)
+ *   its gradient  d_x[t] = sum_s d_rows[row_of[t][s]]
+ *   combine       out[t] = sum_s weight[t][s] rows[row_of[t][s]]
+ *   its gradient  d_rows[row_of[t][s]] = weight[t][s] d_out[t]  (without a slot: 0)
+ *                 d_weight[t][s] = <d_out[t], rows[row_of[t][s]]>  (dropped: 0)
+ * Sums run in fp32 in slot order, so results do not vary from run to run. A
+ * token whose slots are all dropped gets zeros.
+ *
+ * tokens >= 0, 1 <= topk <= 64, 1 <= experts <= 1024, 1 <= hidden,
+ * tokens * topk < 2^31. The plan owns the sort's workspace. GF_OPT_PDL is its
+ * one option; gf_plan_status, gf_plan_describe (tile_m: tokens per CTA of the
+ * sort), gf_plan_launches (of gf_moe_dispatch_execute) and gf_plan_free take
+ * it as any other plan.
+ */
+GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
+                            gf_dtype dtype);
+
+/*
+ * Sort and copy. expert: device int32 [tokens, topk]; x: device [tokens,
+ * hidden] of dtype; offsets: device int32 [experts + 1]; row_of: device int32
+ * [tokens, topk]; slot_of: device int32 [tokens * topk]; rows: device [tokens *
+ * topk, hidden] of dtype. x and rows may both be NULL: the sort alone. Arrays
+ * must not overlap. Asynchronous on stream; pointers 16-byte aligned
+ * (GF_ERR_INVALID_VALUE otherwise, as for a plan of another kind). So for the
+ * three calls below.
+ */
+GF_API gf_status gf_moe_dispatch_execute(const gf_plan* plan, const int32_t* expert, const void* x,
+                                         int32_t* offsets, int32_t* row_of, int32_t* slot_of,
+                                         void* rows, struct CUstream_st* stream);
+
+/* gf_moe_dispatch_execute whose rows are quantised on the way, each token once,
+ * as gf_fp8_quantize with block_rows 1 would: rows: device e4m3 bytes [tokens *
+ * topk, hidden], scale: device fp32 [tokens * topk, ceil(hidden / 128)] (rows
+ * without a slot: zeros with scale 1). hidden % 16 == 0, else
+ * GF_ERR_UNSUPPORTED. All pointers required. */
+GF_API gf_status gf_moe_dispatch_fp8_execute(const gf_plan* plan, const int32_t* expert,
+                                             const void* x, int32_t* offsets, int32_t* row_of,
+                                             int32_t* slot_of, void* rows, float* scale,
+                                             struct CUstream_st* stream);
+
+/* The gradient of dispatch: d_x: device [tokens, hidden], d_rows: device
+ * [tokens * topk, hidden], both of dtype. An entry of row_of outside [0, tokens *
+ * topk) counts as dropped, here and in the two calls below. */
+GF_API gf_status gf_moe_dispatch_grad_execute(const gf_plan* plan, const int32_t* row_of,
+                                              const void* d_rows, void* d_x,
+                                              struct CUstream_st* stream);
+
+/* Back to the tokens, weighted: weight: device fp32 [tokens, topk]; rows: device
+ * [tokens * topk, hidden] and out: device [tokens, hidden], both of dtype. The
+ * weight of a dropped slot is not used (it may be NaN). */
+GF_API gf_status gf_moe_combine_execute(const gf_plan* plan, const int32_t* row_of,
+                                        const float* weight, const void* rows, void* out,
+                                        struct CUstream_st* stream);
+
+/* The gradient of combine: offsets (its last entry bounds the rows that hold a
+ * slot), row_of, weight and rows as in the forward, d_out: device [tokens,
+ * hidden]; d_rows: device [tokens * topk, hidden] of dtype, d_weight: device
+ * fp32 [tokens, topk], both written in full. */
+GF_API gf_status gf_moe_combine_grad_execute(const gf_plan* plan, const int32_t* offsets,
+                                             const int32_t* row_of, const float* weight,
+                                             const void* rows, const void* d_out, void* d_rows,
+                                             float* d_weight, struct CUstream_st* stream);
+
+/*
+ * 8-bit floating point with a scale for each block of 128: x is held as e4m3
+ * values q (OCP 8-bit floating point: 4 exponent bits, 3 mantissa bits, largest
+ * 448, no infinity) times one fp32 scale per block of block_rows x 128
+ * elements, block_rows 1 (activations) or 128 (weights).
+ *   scale = the smallest power of two with max|x| / scale <= 448 over the
+ *           block's finite elements, at least 2^-126; 1 for a block without a
+ *           finite non-zero element
+ *   q     = x / scale rounded to nearest even; infinities and NaN become NaN
+ * A power of two makes the division exact, so the rounding to e4m3 is the only
+ * one; it costs at most one bit of e4m3's exponent range. x: device [m, k] of
+ * dtype; q: device bytes [m, k]; scale: device fp32 [ceil(m / block_rows),
+ * ceil(k / 128)]. 0 <= m, k < 2^31, k % 16 == 0 (else GF_ERR_UNSUPPORTED).
+ * Asynchronous on stream; needs no plan and no workspace.
+ */
+GF_API gf_status gf_fp8_quantize(int64_t m, int64_t k, gf_dtype dtype, int32_t block_rows,
+                                 const void* x, void* q, float* scale,
+                                 struct CUstream_st* stream);
+
+typedef enum gf_fp8_epilog {
+  GF_FP8_EPILOG_NONE = 0,         /* out = the product, of dtype                           */
+  GF_FP8_EPILOG_SWIGLU_QUANT = 1  /* out = e4m3 of silu(gate) * up, out_scale its scales    */
+} gf_fp8_epilog;
+
+/*
+ * Plan out = A . B^T with e4m3 operands and a scale for each block of 128,
+ * over `groups` groups of rows that each have a B of their own (the experts):
+ *   out[i][j] = sum_b a_scale[i][b] b_scale[g][j / 128][b]
+ *                     sum_{l in block b} A[i][l] B[g][j][l]      b = l / 128
+ * with g the group of row i. Each block's sum of up to 128 products and the
+ * sum over the blocks are fp32. GF_FP8_EPILOG_SWIGLU_QUANT forms two products,
+ * gate = A . B^T and up = A . B2^T, and writes h = silu(gate) * up quantised
+ * as by gf_fp8_quantize with block_rows 1 from the fp32 h: the next product's A.
+ *
+ * m rows, n columns, k; groups >= 1. 0 <= m, n, k < 2^31, 1 <= groups <= 1024.
+ * k % 16 == 0 (16-byte rows for the tensor maps), n % 8 == 0, or n % 16 == 0
+ * for SWIGLU_QUANT, else GF_ERR_UNSUPPORTED. dtype: the element type of out
+ * (NONE). Options: GF_OPT_KERNEL, GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US,
+ * GF_OPT_FAULT_DROP_LOAD; others give GF_ERR_UNSUPPORTED.
+ */
+GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t groups,
+                                   gf_dtype dtype, gf_fp8_epilog epilog);
+
+/*
+ * A: device e4m3 [m, k]; a_scale: device fp32 [m, ceil(k / 128)]. B, B2: device
+ * e4m3 [groups, n, k]; b_scale, b2_scale: device fp32 [groups, ceil(n / 128),
+ * ceil(k / 128)]; B2 and b2_scale: SWIGLU_QUANT only. Scales are any fp32 values.
+ * offsets: device int32 [groups + 1], group g is rows offsets[g] ..
+ * offsets[g + 1] - 1 (offsets[0] is taken as 0 and each other one bounded to
+ * [the one before, m] by the kernel); NULL with groups == 1: all rows. Rows of
+ * no group get zeros (and scale 1).
+ * out: device [m, n] of dtype (NONE), or e4m3 bytes [m, n] with out_scale:
+ * device fp32 [m, ceil(n / 128)] (SWIGLU_QUANT). 16-byte aligned;
+ * asynchronous on stream, one kernel launch; the host never reads offsets.
+ * The plan's workspace is shared by its calls: one stream at a time.
+ */
+GF_API gf_status gf_fp8_matmul_execute(const gf_plan* plan, const void* A, const float* a_scale,
+                                       const void* B, const float* b_scale, const void* B2,
+                                       const float* b2_scale, const int32_t* offsets, void* out,
+                                       float* out_scale, struct CUstream_st* stream);
+
+/*
  * Synchronise `stream`, then read and clear the plan's device status word.
  * Returns GF_ERR_DEVICE_TIMEOUT if a bounded wait in a kernel of this plan
  * gave up since the last call (the kernel then skipped the rest of its work
