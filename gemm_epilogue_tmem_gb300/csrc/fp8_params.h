@@ -41,5 +41,10 @@ struct Fp8LaunchArgs {
 // the narrow kernel: 128 columns of B x tile_rows rows per tile
 cudaError_t launch_fp8_narrow(const Fp8LaunchArgs& a);
 int fp8_narrow_stages(int tile_rows, int dual);
+// the CTA-pair kernel: 256 rows x 256 columns (SwiGLU: 128) per tile
+cudaError_t launch_fp8_wide(const Fp8LaunchArgs& a);
+int fp8_wide_stages();
+// resident CTA pairs (0 if the kernel cannot launch)
+int fp8_wide_max_clusters();
 
 }  // namespace gf

@@ -19,11 +19,22 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Tiles of the plan: 16 rows when the groups have few rows on average, else 64.
+// Kernel and tiles of the plan. The average number of rows a group decides:
+// the counts themselves are on the device.
 void plan_tiles(gf_plan* p) {
   const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
   const int64_t rows_per_group = p->m / p->groups;
-  const int kernel = p->forced_kernel != 0 ? p->forced_kernel : rows_per_group <= 16 ? 1 : 2;
+  int kernel = p->forced_kernel;
+  if (kernel == 0) kernel = rows_per_group <= 16 ? 1 : rows_per_group <= 64 ? 2 : 3;
+  if (kernel == 3 && p->max_pair_clusters == 0) kernel = 2;
+  p->wide = kernel == 3 ? 1 : 0;
+  if (p->wide) {
+    p->tile_rows = 256;
+    p->tile_n = dual ? 128 : 256;
+    p->stages = gf::fp8_wide_stages();
+    p->grid = 2 * p->max_pair_clusters;
+    return;
+  }
   p->tile_rows = kernel == 1 ? 16 : 64;
   p->tile_n = 128;
   p->stages = gf::fp8_narrow_stages(p->tile_rows, dual);
@@ -35,7 +46,8 @@ void plan_tiles(gf_plan* p) {
 namespace gf {
 
 gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value) {
-  if (value < 0 || value > 2) return GF_ERR_INVALID_VALUE;
+  if (value < 0 || value > 3) return GF_ERR_INVALID_VALUE;
+  if (value == 3 && p->max_pair_clusters == 0) return GF_ERR_UNSUPPORTED;
   p->forced_kernel = static_cast<int>(value);
   plan_tiles(p);
   return GF_OK;
@@ -67,6 +79,8 @@ GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t grou
   p->n = n;
   p->k = k;
   p->groups = groups;
+  p->max_pair_clusters = gf::fp8_wide_max_clusters();
+  cudaGetLastError();
   plan_tiles(p);
   return p;
 }
@@ -96,7 +110,7 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   memset(&tmB2, 0, sizeof tmB2);
   if (p->k > 0) {
     const uint64_t b_rows = static_cast<uint64_t>(p->groups) * p->n;
-    if (!gf::runtime_encode_2d_u8(&tmA, A, p->k, p->m, 128, p->tile_rows) ||
+    if (!gf::runtime_encode_2d_u8(&tmA, A, p->k, p->m, 128, p->wide ? 128 : p->tile_rows) ||
         !gf::runtime_encode_2d_u8(&tmB, B, p->k, b_rows, 128, 128) ||
         (dual && !gf::runtime_encode_2d_u8(&tmB2, B2, p->k, b_rows, 128, 128)))
       return runtime_fail(GF_ERR_INVALID_VALUE);
@@ -129,7 +143,8 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   la.tile_rows = p->tile_rows;
   la.pdl = p->pdl;
   la.stream = reinterpret_cast<cudaStream_t>(stream);
-  return gf::launch_fp8_narrow(la) == cudaSuccess ? GF_OK : runtime_fail(GF_ERR_CUDA);
+  const cudaError_t err = p->wide ? gf::launch_fp8_wide(la) : gf::launch_fp8_narrow(la);
+  return err == cudaSuccess ? GF_OK : runtime_fail(GF_ERR_CUDA);
 }
 
 }  // extern "C"

@@ -323,7 +323,9 @@ typedef enum gf_fp8_epilog {
  * m rows, n columns, k; groups >= 1. 0 <= m, n, k < 2^31, 1 <= groups <= 1024.
  * k % 16 == 0 (16-byte rows for the tensor maps), n % 8 == 0, or n % 16 == 0
  * for SWIGLU_QUANT, else GF_ERR_UNSUPPORTED. dtype: the element type of out
- * (NONE). Options: GF_OPT_KERNEL, GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US,
+ * (NONE). Options: GF_OPT_KERNEL (0 the plan's choice by the average number of
+ * rows a group; 1 and 2 the single-CTA kernel with tiles of 16 and 64 rows; 3
+ * the CTA-pair kernel with tiles of 256 rows), GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US,
  * GF_OPT_FAULT_DROP_LOAD; others give GF_ERR_UNSUPPORTED.
  */
 GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t groups,
