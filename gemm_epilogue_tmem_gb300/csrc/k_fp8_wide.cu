@@ -255,6 +255,16 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
           const int nkb = t < table.tile0[p.groups] ? KB : 0;
           for (int kb = 0; kb < nkb; ++kb) {
+            if (!mbar_wait_bounded(full0 + 8u * stage, phase, abort_flag, p.wait_limit_ns)) {
+              fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_SMEM);
+              aborted = true;
+              ok = false;
+              break;
+            }
+            const uint64_t adesc = sdesc_sw128(base + stage * kStageBytes, 16, 1024);
+            const uint64_t bdesc = sdesc_sw128(base + stage * kStageBytes + kPartBytes, 16, 1024);
+            const uint32_t d = tmem_base + 256u * static_cast<uint32_t>(buf);
+            // the accumulator last: its release is what the pace hangs on
             if (!mbar_wait_bounded_cluster(tempty0 + 8u * buf, bphase ^ 1u, abort_flag,
                                            p.wait_limit_ns)) {
               fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_TMEM);
@@ -262,19 +272,11 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
               ok = false;
               break;
             }
-            if (!mbar_wait_bounded(full0 + 8u * stage, phase, abort_flag, p.wait_limit_ns)) {
-              fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_SMEM);
-              aborted = true;
-              ok = false;
-              break;
-            }
             tc_fence_after();
-            const uint32_t sA = base + stage * kStageBytes;
-            const uint32_t d = tmem_base + 256u * static_cast<uint32_t>(buf);
+            // (a descriptor's address field counts 16 bytes)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_f8_pair(d, sdesc_sw128(sA + kk * 32, 16, 1024),
-                           sdesc_sw128(sA + kPartBytes + kk * 32, 16, 1024), idesc, kk != 0);
+              umma_f8_pair(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0);
             umma_commit_pair(empty0 + 8u * stage, 0x3);
             umma_commit_pair(tfull0 + 8u * buf, 0x3);
             if (++stage == S) {
@@ -370,20 +372,16 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                                256u * static_cast<uint32_t>(buf);
-        uint32_t v[2][16];
-        tmem_ld_32x32b_x16(taddr + col_a, v[0]);
-        tmem_ld_wait_tied(v[0]);
+        // 64 columns at a time: two loads in flight, and the accumulator is
+        // released as soon as the second pair is in registers
+        uint32_t v[2][32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          // the next 16 columns arrive while these are added
-          if (c < 7)
-            tmem_ld_32x32b_x16(taddr + (c + 1 < 4 ? col_a : col_b) + 16u * ((c + 1) & 3),
-                               v[(c + 1) & 1]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            fma2(acc[8 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], c < 4 ? s_a : s_b);
-          if (c < 7) tmem_ld_wait_tied(v[(c + 1) & 1]);
-          if (c == 6) {  // all columns are in registers, and so are the scales
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b), v[0]);
+          tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b) + 32u, v[1]);
+          tmem_ld_wait_tied(v[0]);
+          tmem_tie(v[1]);
+          if (c == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -391,6 +389,10 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
               mbar_arrive(sempty0 + 8u * slot);
             }
           }
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            fma2(acc[32 * c + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1],
+                 c == 0 ? s_a : s_b);
         }
         buf ^= 1;
         bphase ^= buf == 0 ? 1u : 0u;
