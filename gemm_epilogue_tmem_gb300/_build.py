@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgf.so")
 
 SOURCES = ["runtime.cu", "k_none_bias.cu", "k_relu.cu", "k_drelu.cu", "k_gelu.cu", "k_swiglu.cu", "noalloc.cu",
-           "k_moe.cu", "runtime_moe.cu", "k_fp8_narrow.cu", "k_fp8_wide.cu", "runtime_fp8.cu"]
+           "k_moe.cu", "runtime_moe.cu", "k_fp8_narrow.cu",
+           "k_fp8_single.cu", "k_fp8_wide.cu", "runtime_fp8.cu"]
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "gemm_kernel_2sm.cuh", "dispatch.cuh", "launch.h",
            "params.h", "runtime_internal.h", "plan.h", "moe.h", "fp8.cuh", "fp8_common.cuh",
            "fp8_params.h"]

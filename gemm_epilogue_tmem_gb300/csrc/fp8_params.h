@@ -20,6 +20,10 @@ struct Fp8Params {
   const float* b2_scale;
   void* out;                // 16-bit [M][N], or e4m3 bytes
   float* out_scale;         // [M][num_n_blocks]
+  // narrow kernel: partial sums of the tiles that several CTAs share, two
+  // slots per CTA, and a counter per CTA (zero between launches)
+  float* partials;
+  int32_t* counters;
   int32_t* status;
   uint64_t wait_limit_ns;
   int32_t drop_load;        // test hook: 1-based index of a stage load to skip (0: none)
@@ -33,14 +37,18 @@ struct Fp8LaunchArgs {
   int grid;
   int bf16;
   int dual;                 // SwiGLU: two products, e4m3 out
-  int tile_rows;            // token rows of a tile of the narrow kernel
+  int tile_rows;            // rows of a tile of the narrow kernel
   int pdl;
   cudaStream_t stream;
 };
 
-// the narrow kernel: 128 columns of B x tile_rows rows per tile
+// the narrow kernel: 128 columns of B x tile_rows (16 or 64) rows per tile
 cudaError_t launch_fp8_narrow(const Fp8LaunchArgs& a);
 int fp8_narrow_stages(int tile_rows, int dual);
+size_t fp8_narrow_partial_bytes(int tile_rows, int dual, int grid);
+// the single-CTA kernel: 128 rows x 256 columns (SwiGLU: 128) per tile
+cudaError_t launch_fp8_single(const Fp8LaunchArgs& a);
+int fp8_single_stages();
 // the CTA-pair kernel: 256 rows x 256 columns (SwiGLU: 128) per tile
 cudaError_t launch_fp8_wide(const Fp8LaunchArgs& a);
 int fp8_wide_stages();

@@ -55,48 +55,6 @@ constexpr int kSmemWide = kSmemAlignSlack + kStagesWide * kStageBytes + kSmemCtr
                           kStagingBytes + kTableBytes + kMagBytes + kScaleBytes;
 constexpr int kRasterRows = 8;  // row tiles visited together, column by column
 
-// the pair form of umma_f8
-__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// acc += v * s, two columns at a time
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
-}
-
-__device__ __forceinline__ uint64_t both(float s) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(v) : "f"(s));
-  return v;
-}
-
-__device__ __forceinline__ float2 split2(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-
-// asynchronous 4-byte copy to shared memory (zero where !in), and an arrival
-// on `bar` when this thread's copies so far have landed
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(in ? 4 : 0)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // bulk copy of `bytes` (a multiple of 16) from shared to global memory
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
@@ -198,96 +156,98 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
     setmaxnreg_dec<kCtlRegs>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      if (lane == 0) {
-        int stage = 0;
-        uint32_t phase = 0;
-        int loads = 0;
-        bool ok = true;
-        uint32_t issued = 0, issued_phase = 0;  // bit s: a load of stage s, and its phase
-        for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-          int g, row, row_end, nt;
-          tile_at(t, g, row, row_end, nt);
-          const int nkb = g < p.groups ? KB : 0;
-          const int a_row = row + 128 * static_cast<int>(rank);
-          const int b_row = g * p.N + (DUAL ? nt * 128 : nt * 256 + 128 * static_cast<int>(rank));
-          const CUtensorMap* mb = DUAL && rank == 1 ? &tmB2 : &tmB;
-          for (int kb = 0; kb < nkb; ++kb) {
-            if (!mbar_wait_bounded(empty0 + 8u * stage, phase ^ 1u, abort_flag,
-                                   p.wait_limit_ns)) {
-              fp8_raise(p, abort_flag, ST_TIMEOUT_PRODUCER);
-              aborted = true;
-              ok = false;
-              break;
-            }
-            ++loads;
-            if (loads != p.drop_load) {
-              const uint32_t fb_local = full0 + 8u * stage;
-              const uint32_t fb = mapa_shared(fb_local, 0);  // the leader's barrier
-              const uint32_t dst = base + stage * kStageBytes;
-              if (leader) mbar_arrive_expect_tx(fb_local, 2u * kStageBytes);
-              tma_load_2d_pair(dst, &tmA, fb, kb * 128, a_row);
-              tma_load_2d_pair(dst + kPartBytes, mb, fb, kb * 128, b_row);
-              issued |= 1u << stage;
-              issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-            }
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
-            }
+      const uint32_t e = elect_one();
+      int stage = 0;
+      uint32_t phase = 0;
+      int loads = 0;
+      bool ok = true;
+      uint32_t issued = 0, issued_phase = 0;  // bit s: a load of stage s, and its phase
+      const uint32_t leader_full = mapa_shared(full0, 0);
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+        int g, row, row_end, nt;
+        tile_at(t, g, row, row_end, nt);
+        const int nkb = g < p.groups ? KB : 0;
+        const int a_row = row + 128 * static_cast<int>(rank);
+        const int b_row = g * p.N + (DUAL ? nt * 128 : nt * 256 + 128 * static_cast<int>(rank));
+        const CUtensorMap* mb = DUAL && rank == 1 ? &tmB2 : &tmB;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty0 + 8u * stage, phase ^ 1u,
+                                                         abort_flag, p.wait_limit_ns))) {
+            fp8_raise(p, abort_flag, ST_TIMEOUT_PRODUCER);
+            aborted = true;
+            ok = false;
+            break;
+          }
+          ++loads;
+          if (loads != p.drop_load) {
+            const uint32_t fb = leader_full + 8u * stage;
+            const uint32_t dst = base + stage * kStageBytes;
+            if (leader && e) mbar_arrive_expect_tx(full0 + 8u * stage, 2u * kStageBytes);
+            __syncwarp();
+            tma_load_f8<true>(dst, &tmA, fb, kb * 128, a_row, e);
+            tma_load_f8<true>(dst + kPartBytes, mb, fb, kb * 128, b_row, e);
+            issued |= 1u << stage;
+            issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          }
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        // the leader's full barriers count both CTAs' bytes: when they have
-        // completed, every load of the pair has landed
-        if (leader)
-          for (int s = 0; s < S; ++s)
-            if ((issued >> s & 1u) && !mbar_wait_bounded(full0 + 8u * s, issued_phase >> s & 1u,
-                                                         nullptr, p.wait_limit_ns))
-              fp8_raise(p, abort_flag, ST_TIMEOUT_DRAIN);
       }
+      // the leader's full barriers count both CTAs' bytes: when they have
+      // completed, every load of the pair has landed
+      if (leader)
+        for (int s = 0; s < S; ++s)
+          if ((issued >> s & 1u) && !mbar_wait_bounded(full0 + 8u * s, issued_phase >> s & 1u,
+                                                       nullptr, p.wait_limit_ns))
+            fp8_raise(p, abort_flag, ST_TIMEOUT_DRAIN);
       __syncwarp();
     } else if (warp == 1) {
       // ----------------------------------------------------- MMA (leader)
-      if (lane == 0 && leader) {
+      if (leader) {
         constexpr uint32_t idesc = idesc_e4m3(256, 256);
+        const uint32_t e = elect_one();
+        const uint64_t desc0 = sdesc_sw128(base, 16, 1024);
         int stage = 0, buf = 0;
         uint32_t phase = 0, bphase = 0;
         bool ok = true;
-        for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-          const int nkb = t < table.tile0[p.groups] ? KB : 0;
-          for (int kb = 0; kb < nkb; ++kb) {
-            if (!mbar_wait_bounded(full0 + 8u * stage, phase, abort_flag, p.wait_limit_ns)) {
-              fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_SMEM);
-              aborted = true;
-              ok = false;
-              break;
-            }
-            const uint64_t adesc = sdesc_sw128(base + stage * kStageBytes, 16, 1024);
-            const uint64_t bdesc = sdesc_sw128(base + stage * kStageBytes + kPartBytes, 16, 1024);
-            const uint32_t d = tmem_base + 256u * static_cast<uint32_t>(buf);
-            // the accumulator last: its release is what the pace hangs on
-            if (!mbar_wait_bounded_cluster(tempty0 + 8u * buf, bphase ^ 1u, abort_flag,
-                                           p.wait_limit_ns)) {
-              fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_TMEM);
-              aborted = true;
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            // (a descriptor's address field counts 16 bytes)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f8_pair(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0);
-            umma_commit_pair(empty0 + 8u * stage, 0x3);
-            umma_commit_pair(tfull0 + 8u * buf, 0x3);
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
-            }
-            buf ^= 1;
-            bphase ^= buf == 0 ? 1u : 0u;
+        // all tiles of products have KB blocks
+        const int tiles = table.tile0[p.groups];
+        const int mine = tiles > cluster_id ? (tiles - cluster_id - 1) / num_clusters + 1 : 0;
+        for (int64_t i = static_cast<int64_t>(mine) * KB; i > 0; --i) {
+          ok = mbar_wait_bounded(full0 + 8u * stage, phase, abort_flag, p.wait_limit_ns);
+          if (!__all_sync(0xFFFFFFFFu, ok)) {
+            fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_SMEM);
+            aborted = true;
+            break;
           }
+          // the accumulator last: its release is what the pace hangs on
+          ok = mbar_wait_bounded_cluster(tempty0 + 8u * buf, bphase ^ 1u, abort_flag,
+                                         p.wait_limit_ns);
+          if (!__all_sync(0xFFFFFFFFu, ok)) {
+            fp8_raise(p, abort_flag, ST_TIMEOUT_MMA_TMEM);
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          // (a descriptor's address field counts 16 bytes)
+          const uint64_t adesc = desc0 + static_cast<uint64_t>(stage * (kStageBytes / 16));
+          const uint64_t bdesc = adesc + kPartBytes / 16;
+          const uint32_t d = tmem_base + 256u * static_cast<uint32_t>(buf);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f8<true>(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, kk != 0, e);
+          umma_commit_f8<true>(empty0 + 8u * stage, e);
+          umma_commit_f8<true>(tfull0 + 8u * buf, e);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          buf ^= 1;
+          bphase ^= buf == 0 ? 1u : 0u;
         }
-        umma_commit_pair(done_bar, 0x1);
+        if (e) umma_commit_pair(done_bar, 0x1);
         if (!mbar_wait_bounded(done_bar, 0, nullptr, p.wait_limit_ns))
           fp8_raise(p, abort_flag, ST_TIMEOUT_DRAIN);
       }

@@ -62,6 +62,7 @@ struct gf_plan {
   std::mutex cache_mu;
   // gf_fp8_matmul_plan (m, n, k above): groups of rows with a B each
   int64_t groups;
+  int kernel;            // 1, 2 narrow, 3 single CTA, 4 CTA pair
   int tile_rows;         // rows of a tile
   // gf_moe_plan: m = tokens, k = hidden
   int64_t topk, experts;

@@ -1041,6 +1041,9 @@ GF_API gf_status gf_plan_status(const gf_plan* p, struct CUstream_st* stream) {
     // the status word, and the dynamic schedule's tile counters that a launch
     // which gave up may leave part-way
     if (cudaMemset(p->d_status, 0, 256) != cudaSuccess) return fail(GF_ERR_CUDA);
+    if (gf::epi_fp8(p->epi) &&
+        gf::runtime_fp8_clear_counters(const_cast<gf_plan*>(p)) != GF_OK)
+      return fail(GF_ERR_CUDA);
     // a launch that gave up may leave split-k counters part-way
     const size_t counters = p->pair ? 2 * static_cast<size_t>(p->num_tiles - p->split_from)
                                     : static_cast<size_t>(p->num_tiles);

@@ -19,26 +19,64 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// GF_OPT_KERNEL
+enum : int { kNarrow16 = 1, kNarrow64 = 2, kSingle = 3, kPair = 4 };
+
 // Kernel and tiles of the plan. The average number of rows a group decides:
-// the counts themselves are on the device.
+// the counts themselves are on the device. Measured, in us (m rows, n, k; "64 x"
+// is 64 groups of m rows with 0.5 GB of weights):
+//                       16-row  64-row  single  pair
+//   1, 17408, 5120        14      20      28     33   up to 16 rows: the 16-row tiles
+//   64, 17408, 5120       41      18      27     25   68 tiles do not fill the SMs
+//   64 x 64, 4096, 2048    -      94      94    134   tiles that do: each weight read
+//   64 x 128, 4096, 2048   -     158     119    137     once by one SM
+//   128, 17408, 5120       -      30      28     25   68 pair tiles on 76 pairs
+//   128, 5120, 17408       -      34      75     63   20 pair tiles: k is split
 void plan_tiles(gf_plan* p) {
   const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
-  const int64_t rows_per_group = p->m / p->groups;
+  const int64_t rows = p->m / p->groups;
+  const int tile_n = dual ? 128 : 256;  // of the single-CTA and the pair kernel
   int kernel = p->forced_kernel;
-  if (kernel == 0) kernel = rows_per_group <= 16 ? 1 : rows_per_group <= 64 ? 2 : 3;
-  if (kernel == 3 && p->max_pair_clusters == 0) kernel = 2;
-  p->wide = kernel == 3 ? 1 : 0;
-  if (p->wide) {
-    p->tile_rows = 256;
-    p->tile_n = dual ? 128 : 256;
-    p->stages = gf::fp8_wide_stages();
-    p->grid = 2 * p->max_pair_clusters;
-    return;
+  if (kernel == 0) {
+    const int64_t tiles = p->groups * ((p->n + tile_n - 1) / tile_n);
+    const bool fills = 10 * tiles >= 6 * ((tiles + p->num_sms - 1) / p->num_sms) * p->num_sms;
+    if (rows <= 16)
+      kernel = kNarrow16;
+    else if (rows <= 128 && fills)
+      kernel = kSingle;
+    else
+      kernel = rows <= 64 || (rows <= 128 && 2 * tiles < p->max_pair_clusters) ? kNarrow64 : kPair;
   }
-  p->tile_rows = kernel == 1 ? 16 : 64;
-  p->tile_n = 128;
-  p->stages = gf::fp8_narrow_stages(p->tile_rows, dual);
-  p->grid = p->num_sms;
+  if (kernel == kPair && p->max_pair_clusters == 0) kernel = kSingle;
+  p->kernel = kernel;
+  p->tile_n = kernel <= kNarrow64 ? 128 : tile_n;
+  p->grid = kernel == kPair ? 2 * p->max_pair_clusters : p->num_sms;
+  p->tile_rows = kernel == kNarrow16 ? 16 : kernel == kNarrow64 ? 64 : kernel == kSingle ? 128 : 256;
+  p->stages = kernel == kPair     ? gf::fp8_wide_stages()
+              : kernel == kSingle ? gf::fp8_single_stages()
+                                  : gf::fp8_narrow_stages(p->tile_rows, dual);
+}
+
+// The workspace of the plan's tiling: the narrow kernel's counters (zeroed),
+// then its partial sums. Grown when too small.
+size_t counter_bytes(const gf_plan* p) { return (static_cast<size_t>(p->grid) * 4 + 255) / 256 * 256; }
+
+gf_status ensure_work(gf_plan* p) {
+  if (p->kernel > kNarrow64) return GF_OK;
+  const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
+  const size_t need =
+      counter_bytes(p) + gf::fp8_narrow_partial_bytes(p->tile_rows, dual, p->grid);
+  if (need > p->work_bytes) {
+    void* grown = nullptr;
+    if (cudaMalloc(&grown, need) != cudaSuccess) {  // the plan keeps what it has
+      cudaGetLastError();
+      return GF_ERR_OUT_OF_MEMORY;
+    }
+    if (p->d_work) cudaFree(p->d_work);
+    p->d_work = grown;
+    p->work_bytes = need;
+  }
+  return cudaMemset(p->d_work, 0, counter_bytes(p)) == cudaSuccess ? GF_OK : GF_ERR_CUDA;
 }
 
 }  // namespace
@@ -46,11 +84,23 @@ void plan_tiles(gf_plan* p) {
 namespace gf {
 
 gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value) {
-  if (value < 0 || value > 3) return GF_ERR_INVALID_VALUE;
-  if (value == 3 && p->max_pair_clusters == 0) return GF_ERR_UNSUPPORTED;
+  if (value < 0 || value > 4) return GF_ERR_INVALID_VALUE;
+  if (value == 4 && p->max_pair_clusters == 0) return GF_ERR_UNSUPPORTED;
+  if (cudaSetDevice(p->device) != cudaSuccess) return GF_ERR_CUDA;
+  const int before = p->forced_kernel;
   p->forced_kernel = static_cast<int>(value);
   plan_tiles(p);
-  return GF_OK;
+  const gf_status st = ensure_work(p);
+  if (st != GF_OK) {  // back to the kernel whose workspace the plan has
+    p->forced_kernel = before;
+    plan_tiles(p);
+  }
+  return st;
+}
+
+gf_status runtime_fp8_clear_counters(gf_plan* p) {
+  if (p->kernel > kNarrow64) return GF_OK;
+  return cudaMemset(p->d_work, 0, counter_bytes(p)) == cudaSuccess ? GF_OK : GF_ERR_CUDA;
 }
 
 }  // namespace gf
@@ -82,6 +132,12 @@ GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t grou
   p->max_pair_clusters = gf::fp8_wide_max_clusters();
   cudaGetLastError();
   plan_tiles(p);
+  const gf_status st = ensure_work(p);
+  if (st != GF_OK) {
+    gf_plan_free(p);
+    runtime_fail(st);
+    return nullptr;
+  }
   return p;
 }
 
@@ -110,7 +166,8 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   memset(&tmB2, 0, sizeof tmB2);
   if (p->k > 0) {
     const uint64_t b_rows = static_cast<uint64_t>(p->groups) * p->n;
-    if (!gf::runtime_encode_2d_u8(&tmA, A, p->k, p->m, 128, p->wide ? 128 : p->tile_rows) ||
+    if (!gf::runtime_encode_2d_u8(&tmA, A, p->k, p->m, 128,
+                                  p->tile_rows < 128 ? p->tile_rows : 128) ||
         !gf::runtime_encode_2d_u8(&tmB, B, p->k, b_rows, 128, 128) ||
         (dual && !gf::runtime_encode_2d_u8(&tmB2, B2, p->k, b_rows, 128, 128)))
       return runtime_fail(GF_ERR_INVALID_VALUE);
@@ -128,6 +185,11 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   prm.b2_scale = b2_scale;
   prm.out = out;
   prm.out_scale = out_scale;
+  if (p->kernel <= kNarrow64) {
+    prm.counters = static_cast<int32_t*>(p->d_work);
+    prm.partials =
+        reinterpret_cast<float*>(static_cast<char*>(p->d_work) + counter_bytes(p));
+  }
   prm.status = p->d_status;
   prm.wait_limit_ns = p->wait_limit_ns;
   prm.drop_load = p->drop_load;
@@ -143,7 +205,9 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   la.tile_rows = p->tile_rows;
   la.pdl = p->pdl;
   la.stream = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = p->wide ? gf::launch_fp8_wide(la) : gf::launch_fp8_narrow(la);
+  const cudaError_t err = p->kernel == kPair     ? gf::launch_fp8_wide(la)
+                          : p->kernel == kSingle ? gf::launch_fp8_single(la)
+                                                 : gf::launch_fp8_narrow(la);
   return err == cudaSuccess ? GF_OK : runtime_fail(GF_ERR_CUDA);
 }
 

@@ -36,6 +36,9 @@ gf_plan* runtime_new_plan(int epi, gf_dtype dtype, size_t work_bytes);
 // GF_OPT_KERNEL of an e4m3 product's plan.
 gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value);
 
+// After a launch of such a plan that gave up: its counters back to zero.
+gf_status runtime_fp8_clear_counters(gf_plan* p);
+
 // The number of SMs of the calling thread's device, checked as above.
 gf_status runtime_device(int* dev, int* sms);
 

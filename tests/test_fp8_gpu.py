@@ -13,7 +13,7 @@ from fp8_reference import quantize_reference  # noqa: E402
 
 TDT = {gf.GF_F16: torch.float16, gf.GF_BF16: torch.bfloat16}
 ROUND = {gf.GF_F16: (2.0 ** -11, 2.0 ** -25), gf.GF_BF16: (2.0 ** -8, 0.0)}
-KERNELS = [0, 1, 2, 3]  # GF_OPT_KERNEL
+KERNELS = [0, 1, 2, 3, 4]  # GF_OPT_KERNEL
 
 
 def gen(seed):
