@@ -147,10 +147,27 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_current_stream = None  # () -> the address of the current device's current stream
+
+
+def _bind_current_stream():
+    """torch's own getter of the raw stream where it has one (it makes no
+    Stream object: 0.1 against 2.9 us a call), else the public one."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        torch.cuda.init()
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_current_stream or _bind_current_stream())()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -304,9 +321,10 @@ def gf_noalloc_status(stream=None) -> int:
 # ------------------------------------------------------- expert routing, e4m3
 # Tensors of the calls below are checked against the plan: element size and
 # kind, number of elements, contiguous, on a GPU. Raw addresses are not.
+_I32_KIND, _F32_KIND, _E4M3_KIND = "i32", "f32", "e4m3"
 _TENSOR_KINDS = {
-    "i32": ("torch.int32",), "f32": ("torch.float32",),
-    "e4m3": ("torch.float8_e4m3fn", "torch.uint8"),
+    _I32_KIND: ("torch.int32",), _F32_KIND: ("torch.float32",),
+    _E4M3_KIND: ("torch.float8_e4m3fn", "torch.uint8"),
     GF_F16: ("torch.float16",), GF_BF16: ("torch.bfloat16",),
 }
 _kinds = {}  # kind -> its torch dtypes
@@ -314,18 +332,19 @@ _kinds = {}  # kind -> its torch dtypes
 
 def _arg(x, kind, count: int, what: str) -> int | None:
     """Device address of x, a tensor of `count` elements of `kind` (or an address, or None)."""
-    if x is None or isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    if not _kinds:
+    try:
+        if x.dtype in _kinds[kind] and x.numel() == count and x.is_cuda and x.is_contiguous():
+            return x.data_ptr()
+    except KeyError:  # the first tensor
         import torch
         _kinds.update({k: tuple(getattr(torch, n.split(".")[1]) for n in v)
                        for k, v in _TENSOR_KINDS.items()})
-    if x.dtype not in _kinds[kind] or x.numel() != count or not x.is_contiguous() or not x.is_cuda:
-        raise GfError(GF_ERR_INVALID_VALUE,
-                      f"{what}: a contiguous CUDA tensor of {count} elements of "
-                      f"{' or '.join(_TENSOR_KINDS[kind])} is needed, not {x.dtype} "
-                      f"{tuple(x.shape)}")
-    return x.data_ptr()
+        return _arg(x, kind, count, what)
+    raise GfError(GF_ERR_INVALID_VALUE,
+                  f"{what}: a contiguous CUDA tensor of {count} elements of "
+                  f"{' or '.join(_TENSOR_KINDS[kind])} is needed, not {x.dtype} {tuple(x.shape)}")
 
 
 def _check(rc: int, what: str) -> None:
@@ -355,9 +374,9 @@ def gf_moe_dispatch_execute(plan: Plan, expert, x, offsets, row_of, slot_of, row
     what = "gf_moe_dispatch_execute"
     _moe(plan, what)
     _check(lib().gf_moe_dispatch_execute(
-        plan.handle, _arg(expert, "i32", plan.slots, what), _arg(x, plan.dtype, plan.m * plan.k, what),
-        _arg(offsets, "i32", plan.n + 1, what), _arg(row_of, "i32", plan.slots, what),
-        _arg(slot_of, "i32", plan.slots, what), _arg(rows, plan.dtype, plan.slots * plan.k, what),
+        plan.handle, _arg(expert, _I32_KIND, plan.slots, what), _arg(x, plan.dtype, plan.m * plan.k, what),
+        _arg(offsets, _I32_KIND, plan.n + 1, what), _arg(row_of, _I32_KIND, plan.slots, what),
+        _arg(slot_of, _I32_KIND, plan.slots, what), _arg(rows, plan.dtype, plan.slots * plan.k, what),
         _stream(stream)), what)
 
 
@@ -367,10 +386,10 @@ def gf_moe_dispatch_fp8_execute(plan: Plan, expert, x, offsets, row_of, slot_of,
     what = "gf_moe_dispatch_fp8_execute"
     _moe(plan, what)
     _check(lib().gf_moe_dispatch_fp8_execute(
-        plan.handle, _arg(expert, "i32", plan.slots, what), _arg(x, plan.dtype, plan.m * plan.k, what),
-        _arg(offsets, "i32", plan.n + 1, what), _arg(row_of, "i32", plan.slots, what),
-        _arg(slot_of, "i32", plan.slots, what), _arg(rows, "e4m3", plan.slots * plan.k, what),
-        _arg(scale, "f32", plan.slots * -(-plan.k // 128), what), _stream(stream)), what)
+        plan.handle, _arg(expert, _I32_KIND, plan.slots, what), _arg(x, plan.dtype, plan.m * plan.k, what),
+        _arg(offsets, _I32_KIND, plan.n + 1, what), _arg(row_of, _I32_KIND, plan.slots, what),
+        _arg(slot_of, _I32_KIND, plan.slots, what), _arg(rows, _E4M3_KIND, plan.slots * plan.k, what),
+        _arg(scale, _F32_KIND, plan.slots * -(-plan.k // 128), what), _stream(stream)), what)
 
 
 def gf_moe_dispatch_grad_execute(plan: Plan, row_of, d_rows, d_x, stream=None) -> None:
@@ -378,7 +397,7 @@ def gf_moe_dispatch_grad_execute(plan: Plan, row_of, d_rows, d_x, stream=None) -
     what = "gf_moe_dispatch_grad_execute"
     _moe(plan, what)
     _check(lib().gf_moe_dispatch_grad_execute(
-        plan.handle, _arg(row_of, "i32", plan.slots, what),
+        plan.handle, _arg(row_of, _I32_KIND, plan.slots, what),
         _arg(d_rows, plan.dtype, plan.slots * plan.k, what),
         _arg(d_x, plan.dtype, plan.m * plan.k, what), _stream(stream)), what)
 
@@ -388,7 +407,7 @@ def gf_moe_combine_execute(plan: Plan, row_of, weight, rows, out, stream=None) -
     what = "gf_moe_combine_execute"
     _moe(plan, what)
     _check(lib().gf_moe_combine_execute(
-        plan.handle, _arg(row_of, "i32", plan.slots, what), _arg(weight, "f32", plan.slots, what),
+        plan.handle, _arg(row_of, _I32_KIND, plan.slots, what), _arg(weight, _F32_KIND, plan.slots, what),
         _arg(rows, plan.dtype, plan.slots * plan.k, what),
         _arg(out, plan.dtype, plan.m * plan.k, what), _stream(stream)), what)
 
@@ -399,11 +418,11 @@ def gf_moe_combine_grad_execute(plan: Plan, offsets, row_of, weight, rows, d_out
     what = "gf_moe_combine_grad_execute"
     _moe(plan, what)
     _check(lib().gf_moe_combine_grad_execute(
-        plan.handle, _arg(offsets, "i32", plan.n + 1, what), _arg(row_of, "i32", plan.slots, what),
-        _arg(weight, "f32", plan.slots, what), _arg(rows, plan.dtype, plan.slots * plan.k, what),
+        plan.handle, _arg(offsets, _I32_KIND, plan.n + 1, what), _arg(row_of, _I32_KIND, plan.slots, what),
+        _arg(weight, _F32_KIND, plan.slots, what), _arg(rows, plan.dtype, plan.slots * plan.k, what),
         _arg(d_out, plan.dtype, plan.m * plan.k, what),
         _arg(d_rows, plan.dtype, plan.slots * plan.k, what),
-        _arg(d_weight, "f32", plan.slots, what), _stream(stream)), what)
+        _arg(d_weight, _F32_KIND, plan.slots, what), _stream(stream)), what)
 
 
 def gf_fp8_quantize(m: int, k: int, dtype: int, block_rows: int, x, q, scale, stream=None) -> None:
@@ -413,7 +432,7 @@ def gf_fp8_quantize(m: int, k: int, dtype: int, block_rows: int, x, q, scale, st
         raise GfError(GF_ERR_INVALID_VALUE, what)
     blocks = -(-m // block_rows) * -(-k // 128)
     _check(lib().gf_fp8_quantize(m, k, dtype, block_rows, _arg(x, dtype, m * k, what),
-                                 _arg(q, "e4m3", m * k, what), _arg(scale, "f32", blocks, what),
+                                 _arg(q, _E4M3_KIND, m * k, what), _arg(scale, _F32_KIND, blocks, what),
                                  _stream(stream)), what)
 
 
@@ -438,9 +457,9 @@ def gf_fp8_matmul_execute(plan: Plan, A, a_scale, B, b_scale, B2=None, b2_scale=
     m, n, k, groups = plan.m, plan.n, plan.k, plan.groups
     scales = groups * plan.nb * plan.kb
     _check(lib().gf_fp8_matmul_execute(
-        plan.handle, _arg(A, "e4m3", m * k, what), _arg(a_scale, "f32", m * plan.kb, what),
-        _arg(B, "e4m3", groups * n * k, what), _arg(b_scale, "f32", scales, what),
-        _arg(B2, "e4m3", groups * n * k, what), _arg(b2_scale, "f32", scales, what),
-        _arg(offsets, "i32", groups + 1, what),
-        _arg(out, "e4m3" if plan.quant else plan.dtype, m * n, what),
-        _arg(out_scale, "f32", m * plan.nb, what), _stream(stream)), what)
+        plan.handle, _arg(A, _E4M3_KIND, m * k, what), _arg(a_scale, _F32_KIND, m * plan.kb, what),
+        _arg(B, _E4M3_KIND, groups * n * k, what), _arg(b_scale, _F32_KIND, scales, what),
+        _arg(B2, _E4M3_KIND, groups * n * k, what), _arg(b2_scale, _F32_KIND, scales, what),
+        _arg(offsets, _I32_KIND, groups + 1, what),
+        _arg(out, _E4M3_KIND if plan.quant else plan.dtype, m * n, what),
+        _arg(out_scale, _F32_KIND, m * plan.nb, what), _stream(stream)), what)

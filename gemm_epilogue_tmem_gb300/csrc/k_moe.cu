@@ -5,6 +5,13 @@
 // element. Each kernel is token-driven, so that the one row that all of a
 // token's slots share (x, out, d_out) passes through the chip once and only
 // the topk rows per token that differ are read or written.
+//
+// Rows whose length is not a multiple of 16 bytes (ANY below) start at every
+// even byte. Their accesses are 16 bytes all the same: stores go by the
+// aligned words of the row that is written (its first and last word element by
+// element), and what they need of another row is shifted out of the two
+// aligned words that hold it (5003 tokens, 6 slots, 2047 columns of fp16: the
+// gradient of dispatch took 87 us with 2-byte accesses).
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -14,7 +21,7 @@
 namespace gf {
 namespace {
 
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kRankWarps = 8;        // warps that rank the slots of a chunk
 constexpr int kMaxChunkSlots = 4096;
 
@@ -58,17 +65,258 @@ __global__ void __launch_bounds__(kSortThreads) moe_count_kernel(const MoeParams
     p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
 }
 
-// one 16-byte or 2-byte element of a row
-template <int VEC>
-struct Elem {
-  using type = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
-};
+// --------------------------------------------------------- rows of any length
+// The aligned 16-byte word at byte `at` of an array of `total` bytes; bytes
+// outside it are zero and are not read.
+__device__ __forceinline__ uint4 word_at(const uint8_t* array, int64_t at, int64_t total) {
+  if (at >= 0 && at + 16 <= total) return *reinterpret_cast<const uint4*>(array + at);
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (at >= 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at + 2 * i < total)
+        w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(array + at + 2 * i))
+                    << (16 * (i & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-// VEC: elements per access, 8 where rows are multiples of 16 bytes, else 1.
-template <typename T, int COPY, int VEC>
+// the 16 bytes that begin `shift` (even, below 16) bytes into a and end in b
+__device__ __forceinline__ uint4 shift_out(const uint4& a, const uint4& b, uint32_t shift) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (shift & 8u) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (shift & 4u) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t r = 8u * (shift & 2u);
+  return make_uint4(__funnelshift_r(w[0], w[1], r), __funnelshift_r(w[1], w[2], r),
+                    __funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r));
+}
+
+// The 16 bytes from byte `at` (even) on, out of the two aligned words around
+// them; bytes outside the array are zero and are not read.
+__device__ __forceinline__ uint4 bytes_at(const uint8_t* array, int64_t at, int64_t total) {
+  const uint32_t shift = static_cast<uint32_t>(at) & 15u;
+  return shift_out(word_at(array, at - shift, total), word_at(array, at - shift + 16, total),
+                   shift);
+}
+
+// whether both aligned words around byte `at` lie in the array: their loads need
+// no checks, so that those of several rows can be in flight together
+__device__ __forceinline__ bool pair_inside(int64_t at, int64_t total) {
+  return at >= 0 && (at & ~int64_t(15)) + 32 <= total;
+}
+
+// How a row of H 16-bit elements is cut into words of 8. Aligned: column 8 v.
+// ANY: by the aligned words of the array, the first and last of which may
+// hold neighbours' elements too.
+template <bool ANY>
+struct RowWords {
+  int64_t H, start;  // elements; first element of the row in its array
+  int lead;          // elements before the row in its first word
+  __device__ __forceinline__ RowWords(int64_t h, int64_t row)
+      : H(h), start(row * h), lead(ANY ? static_cast<int>((row * h) & 7) : 0) {}
+  // column of word v's first element (below 0 in a first word with a lead)
+  __device__ __forceinline__ int64_t column(int64_t v) const { return 8 * v - lead; }
+};
+template <bool ANY>
+__device__ __forceinline__ int64_t words_of_row(int64_t H) {
+  return ANY ? (H + 14) / 8 : H / 8;  // the most that a row touches
+}
+
+// elements `col` .. `col` + 7 of an aligned row
+__device__ __forceinline__ uint4 load_words(const void* array, int64_t row, int64_t H,
+                                            int64_t col) {
+  return __ldcs(
+      reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(array) + row * H + col));
+}
+
+// the word at column `col` of the row that the words were cut by
+template <bool ANY>
+__device__ __forceinline__ void store_words(void* array, const RowWords<ANY>& r, int64_t col,
+                                            const uint4& w) {
+  uint16_t* dst = static_cast<uint16_t*>(array) + r.start + col;
+  if (!ANY || (col >= 0 && col + 8 <= r.H)) {
+    __stcs(reinterpret_cast<uint4*>(dst), w);
+  } else {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i >= 0 && col + i < r.H)
+        dst[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = Pair16<T>::unpack(u[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(Pair16<T>::pack(f[0], f[1]), Pair16<T>::pack(f[2], f[3]),
+                    Pair16<T>::pack(f[4], f[5]), Pair16<T>::pack(f[6], f[7]));
+}
+
+// ------------------------------------------------------------------ the copies
+// Row x[token] to the places of its slots, by one warp: words [32 U part,
+// 32 U (part + 1)) of it. `place`: the token's topk rows (below 0: dropped).
+constexpr int kCopyWords = 4;  // words a lane holds (U)
+
+template <bool ANY>
+__device__ __forceinline__ void copy_item(const MoeParams& p, int64_t token, int part,
+                                          const int32_t* place) {
+  constexpr int U = kCopyWords;
+  const int64_t H = p.hidden;
+  const int64_t v0 = static_cast<int64_t>(part) * (32 * U) + lane_id();
+  if constexpr (!ANY) {
+    const int64_t nv = H / 8;
+    const uint4* src = static_cast<const uint4*>(p.x) + token * nv;
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + 32 * u < nv) v[u] = __ldcs(src + v0 + 32 * u);
+    for (int s = 0; s < p.topk; ++s) {
+      const int row = place[s];
+      if (row < 0) continue;
+      uint4* dst = static_cast<uint4*>(p.rows) + static_cast<int64_t>(row) * nv;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < nv) __stcs(dst + v0 + 32 * u, v[u]);
+    }
+  } else {
+    const int64_t total = 2 * static_cast<int64_t>(p.tokens) * H;
+    const uint8_t* x = static_cast<const uint8_t*>(p.x);
+    for (int s = 0; s < p.topk; ++s) {
+      const int row = place[s];
+      if (row < 0) continue;
+      const RowWords<true> r(H, row);
+      // (the row's alignment, and so the shift, is the same for all its words)
+      const int64_t at0 = 2 * (token * H + r.column(v0));
+      const uint32_t shift = static_cast<uint32_t>(at0) & 15u;
+      uint4 a[U], b[U];
+      if (pair_inside(at0, total) && pair_inside(at0 + 512 * (U - 1), total)) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + at0 - shift);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          a[u] = __ldg(src + 32 * u);
+          b[u] = __ldg(src + 32 * u + 1);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          a[u] = word_at(x, at0 - shift + 512 * u, total);
+          b[u] = word_at(x, at0 - shift + 512 * u + 16, total);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t col = r.column(v0 + 32 * u);
+        if (col < H) store_words<true>(p.rows, r, col, shift_out(a[u], b[u], shift));
+      }
+    }
+  }
+}
+
+// The same, quantised: 16 elements a lane, 8 lanes a block of 128, 512
+// elements a warp.
+template <typename T>
+__device__ __forceinline__ void quant_item(const MoeParams& p, int64_t token, int part,
+                                           const int32_t* place) {
+  const int64_t nv = p.hidden / 16;
+  const int blocks = static_cast<int>((p.hidden + 127) / 128);
+  const uint32_t lane = lane_id();
+  const int64_t v = static_cast<int64_t>(part) * 32 + lane;
+  const bool in = v < nv;
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (in) {
+    const uint4* src = static_cast<const uint4*>(p.x) + (token * nv + v) * 2;
+    a = __ldcs(src);
+    b = __ldcs(src + 1);
+  }
+  float f[16];
+  uint32_t mag = unpack16<T>(a, b, f);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d));
+  float inv;
+  const float sc = e4m3_scale(mag, inv);
+  const uint4 q = quant16(f, inv);
+  uint4* rows = static_cast<uint4*>(p.rows);
+  for (int s = 0; s < p.topk; ++s) {
+    const int row = place[s];
+    if (row < 0 || !in) continue;
+    __stcs(rows + static_cast<int64_t>(row) * nv + v, q);
+    if ((lane & 7u) == 0) p.scale[static_cast<int64_t>(row) * blocks + (v >> 3)] = sc;
+  }
+}
+
+template <int COPY, bool ANY>
+__device__ __forceinline__ int copy_parts(int64_t H) {
+  return COPY == MOE_COPY_FP8
+             ? static_cast<int>((H / 16 + 31) / 32)
+             : static_cast<int>((words_of_row<ANY>(H) + 32 * kCopyWords - 1) / (32 * kCopyWords));
+}
+
+// rows [kept, slots) of the output: zeros (e4m3: with scale 1), by thread
+// `first` of `threads`
+template <int COPY>
+__device__ __forceinline__ void clear_tail(const MoeParams& p, int kept, int64_t first,
+                                           int64_t threads) {
+  const int64_t tail = p.slots - kept;
+  if (tail <= 0) return;
+  if constexpr (COPY == MOE_COPY_FP8) {
+    const int64_t nv = p.hidden / 16, blocks = (p.hidden + 127) / 128;
+    uint4* zero = static_cast<uint4*>(p.rows) + kept * nv;
+    for (int64_t i = first; i < tail * nv; i += threads) zero[i] = make_uint4(0, 0, 0, 0);
+    float* ones = p.scale + kept * blocks;
+    for (int64_t i = first; i < tail * blocks; i += threads) ones[i] = 1.0f;
+  } else {
+    // 16-bit zeros from element `begin` on; the array's aligned words between
+    uint16_t* rows = static_cast<uint16_t*>(p.rows);
+    const int64_t begin = kept * p.hidden, end = static_cast<int64_t>(p.slots) * p.hidden;
+    const int64_t w0 = (begin + 7) / 8, w1 = end / 8;
+    for (int64_t i = w0 + first; i < w1; i += threads)
+      reinterpret_cast<uint4*>(rows)[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = begin + first; i < min(8 * w0, end); i += threads) rows[i] = 0;
+    for (int64_t i = max(8 * w1, begin) + first; i < end; i += threads) rows[i] = 0;
+  }
+}
+
+// The copies on their own, after the sort of many slots: a warp per item, a CTA
+// per 8 items, so that the hardware balances them over the SMs.
+template <typename T, int COPY, bool ANY>
+__global__ void __launch_bounds__(256) moe_copy_kernel(const MoeParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int parts = copy_parts<COPY, ANY>(p.hidden);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (item < static_cast<int64_t>(p.tokens) * parts) {
+    const int64_t token = item / parts;
+    const int part = static_cast<int>(item - token * parts);
+    if constexpr (COPY == MOE_COPY_FP8)
+      quant_item<T>(p, token, part, p.row_of + token * p.topk);
+    else
+      copy_item<ANY>(p, token, part, p.row_of + token * p.topk);
+  }
+  clear_tail<COPY>(p, p.offsets[p.experts], static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x,
+                   static_cast<int64_t>(gridDim.x) * 256);
+}
+
+// The sort, and with few slots (fused) the copies of the chunk's tokens too.
+template <typename T, int COPY, bool ANY>
 __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoeParams p) {
   extern __shared__ int32_t smem[];
-  int32_t* total = smem;                                // [experts]
+  int32_t* total = smem;                                // [experts], less `before`
   int32_t* before = total + p.experts;                  // [experts]
   int32_t* rank = before + p.experts;                   // [kRankWarps][experts]
   int32_t* place = rank + kRankWarps * p.experts;       // [chunk slots]
@@ -88,26 +336,50 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
 
   // the slots of every expert: in all chunks, and in the chunks before this
   if (p.one_pass) {
-    for (int i = tid; i < p.slots; i += kSortThreads) {
-      const uint32_t e = static_cast<uint32_t>(p.expert[i]);
-      if (e < static_cast<uint32_t>(experts)) {
-        atomicAdd(&total[e], 1);
-        if (i < first) atomicAdd(&before[e], 1);
+    // `before` counts what lies before the chunk, `total` the rest
+    const int lead = first & ~3;
+    for (int i = 4 * tid; i < p.slots; i += 4 * kSortThreads) {
+      int e[4];
+      if (i + 4 <= p.slots) {
+        const int4 v = *reinterpret_cast<const int4*>(p.expert + i);
+        e[0] = v.x, e[1] = v.y, e[2] = v.z, e[3] = v.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = i + j < p.slots ? p.expert[i + j] : -1;
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (static_cast<uint32_t>(e[j]) < static_cast<uint32_t>(experts))
+          atomicAdd(i < lead || i + j < first ? &before[e[j]] : &total[e[j]], 1);
     }
   } else {
-    // a warp's 32 lanes take 32 experts, the warps different chunks
-    for (int e0 = 0; e0 < experts; e0 += 32) {
-      const int e = e0 + static_cast<int>(lane);
-      if (e >= experts) continue;
-      int all = 0, prior = 0;
-      for (int c = warp; c < p.num_chunks; c += kSortThreads / 32) {
-        const int v = p.counts[static_cast<int64_t>(c) * experts + e];
-        all += v;
-        prior += c < static_cast<int>(blockIdx.x) ? v : 0;
+    // a warp's 32 lanes take 32 experts; the warps of the same experts share
+    // the chunks, kBatch loads at a time
+    constexpr int kBatch = 16, kWarps = kSortThreads / 32;
+    const int sets = (experts + 31) / 32;
+    const int sharing = sets < kWarps ? kWarps / sets : 1;  // warps per set of experts
+    for (int set = warp % (sets < kWarps ? sets : kWarps); set < sets && warp / sets < sharing;
+         set += kWarps) {
+      const int e = 32 * set + static_cast<int>(lane);
+      int rest = 0, prior = 0;
+      const int part = sets < kWarps ? warp / sets : 0;
+      for (int c0 = part; c0 < p.num_chunks; c0 += sharing * kBatch) {
+        int v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int c = c0 + j * sharing;
+          v[j] = c < p.num_chunks && e < experts
+                     ? p.counts[static_cast<int64_t>(c) * experts + e]
+                     : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          (c0 + j * sharing < static_cast<int>(blockIdx.x) ? prior : rest) += v[j];
       }
-      atomicAdd(&total[e], all);
-      atomicAdd(&before[e], prior);
+      if (e < experts) {
+        atomicAdd(&total[e], rest);
+        atomicAdd(&before[e], prior);
+      }
     }
   }
   // this chunk's slots of every expert, for each ranking warp's run of slots
@@ -126,7 +398,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   int sum = 0;
   for (int j = 0; j < per; ++j) {
     const int e = per * tid + j;
-    sum += e < experts ? total[e] : 0;
+    sum += e < experts ? total[e] + before[e] : 0;
   }
   int incl = sum;
 #pragma unroll
@@ -155,7 +427,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
       rank[w * experts + e] = next;
       next += v;
     }
-    at += total[e];
+    at += total[e] + before[e];
   }
   __syncthreads();
 
@@ -189,202 +461,206 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   if constexpr (COPY == MOE_SORT_ONLY) return;
   __syncthreads();
 
-  const int64_t H = p.hidden;
-  const int tokens = n / p.topk;
-  const int first_token = blockIdx.x * p.chunk_tokens;
-  const int cta = blockIdx.x * gridDim.y + blockIdx.y;
-  const int ctas = gridDim.x * gridDim.y;
-  if constexpr (COPY == MOE_COPY) {
-    using V = typename Elem<VEC>::type;
-    const int64_t nv = H / VEC;
-    const V* x = static_cast<const V*>(p.x);
-    V* rows = static_cast<V*>(p.rows);
-    // a warp takes (token, run of 32 * U vectors) pairs; the CTAs of a chunk
-    // take every segments-th pair
-    constexpr int U = 4;
-    const int parts = static_cast<int>((nv + 32 * U - 1) / (32 * U));
-    const int64_t items = static_cast<int64_t>(tokens) * parts;
-    for (int64_t it = static_cast<int64_t>(blockIdx.y) * (kSortThreads / 32) + warp; it < items;
-         it += static_cast<int64_t>(gridDim.y) * (kSortThreads / 32)) {
-      const int t = static_cast<int>(it / parts);
-      const int64_t v0 = (it % parts) * (32 * U) + lane;
-      V v[U];
-      const V* src = x + (first_token + t) * nv;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + 32 * u < nv) v[u] = __ldcs(src + v0 + 32 * u);
-      for (int s = 0; s < p.topk; ++s) {
-        const int row = place[t * p.topk + s];
-        if (row < 0) continue;
-        V* dst = rows + static_cast<int64_t>(row) * nv;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (v0 + 32 * u < nv) __stcs(dst + v0 + 32 * u, v[u]);
-      }
-    }
-    const int64_t tail = static_cast<int64_t>(p.slots - kept) * nv;
-    V* zero = rows + static_cast<int64_t>(kept) * nv;
-    for (int64_t i = static_cast<int64_t>(cta) * kSortThreads + tid; i < tail;
-         i += static_cast<int64_t>(ctas) * kSortThreads)
-      zero[i] = V{};
-  } else {
-    // 16 elements a lane, 8 lanes a block of 128, 512 elements a warp
-    const int64_t nv = H / 16;
-    const int blocks = static_cast<int>((H + 127) / 128);
-    const uint4* x = static_cast<const uint4*>(p.x);
-    uint4* rows = static_cast<uint4*>(p.rows);
-    const int parts = static_cast<int>((nv + 31) / 32);
-    const int64_t items = static_cast<int64_t>(tokens) * parts;
-    for (int64_t it = static_cast<int64_t>(blockIdx.y) * (kSortThreads / 32) + warp; it < items;
-         it += static_cast<int64_t>(gridDim.y) * (kSortThreads / 32)) {
-      const int t = static_cast<int>(it / parts);
-      const int64_t v = (it % parts) * 32 + lane;
-      const bool in = v < nv;
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (in) {
-        const uint4* src = x + ((first_token + t) * nv + v) * 2;
-        a = __ldcs(src);
-        b = __ldcs(src + 1);
-      }
-      float f[16];
-      uint32_t mag = unpack16<T>(a, b, f);
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d));
-      float inv;
-      const float sc = e4m3_scale(mag, inv);
-      const uint4 q = quant16(f, inv);
-      for (int s = 0; s < p.topk; ++s) {
-        const int row = place[t * p.topk + s];
-        if (row < 0 || !in) continue;
-        rows[static_cast<int64_t>(row) * nv + v] = q;
-        if ((lane & 7u) == 0) p.scale[static_cast<int64_t>(row) * blocks + (v >> 3)] = sc;
-      }
-    }
-    const int64_t tail = static_cast<int64_t>(p.slots - kept);
-    uint4* zero = rows + static_cast<int64_t>(kept) * nv;
-    float* ones = p.scale + static_cast<int64_t>(kept) * blocks;
-    for (int64_t i = static_cast<int64_t>(cta) * kSortThreads + tid; i < tail * nv;
-         i += static_cast<int64_t>(ctas) * kSortThreads)
-      zero[i] = make_uint4(0, 0, 0, 0);
-    for (int64_t i = static_cast<int64_t>(cta) * kSortThreads + tid; i < tail * blocks;
-         i += static_cast<int64_t>(ctas) * kSortThreads)
-      ones[i] = 1.0f;
+  const int parts = copy_parts<COPY, ANY>(p.hidden);
+  const int64_t items = static_cast<int64_t>(n / p.topk) * parts;
+  constexpr int kWarps = kSortThreads / 32;
+  for (int64_t it = static_cast<int64_t>(blockIdx.y) * kWarps + warp; it < items;
+       it += static_cast<int64_t>(gridDim.y) * kWarps) {
+    const int t = static_cast<int>(it / parts);
+    const int part = static_cast<int>(it - static_cast<int64_t>(t) * parts);
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * p.chunk_tokens + t;
+    if constexpr (COPY == MOE_COPY_FP8)
+      quant_item<T>(p, token, part, place + t * p.topk);
+    else
+      copy_item<ANY>(p, token, part, place + t * p.topk);
   }
+  clear_tail<COPY>(p, kept,
+                   static_cast<int64_t>(blockIdx.x * gridDim.y + blockIdx.y) * kSortThreads + tid,
+                   static_cast<int64_t>(gridDim.x) * gridDim.y * kSortThreads);
 }
 
 // ---------------------------------------------------------------- back again
-// Elements of a row as fp32: VEC 16-bit elements per access.
-template <typename T, int VEC>
-__device__ __forceinline__ void load_f32(const T* src, float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = Pair16<T>::unpack(u[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
-  } else {
-    f[0] = Pair16<T>::one(*src);
-  }
-}
+// The slots whose loads are in flight together (KS) are a template parameter: the
+// smallest of 2, 4 and 8 that holds topk, 8 for more. With 8 for 2 slots the
+// registers for the others cost half of the bandwidth (116 against 65 us, 16384
+// tokens of 4096).
 
-template <typename T, int VEC>
-__device__ __forceinline__ void store_f32(T* dst, const float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
-    __stcs(reinterpret_cast<uint4*>(dst),
-           make_uint4(Pair16<T>::pack(f[0], f[1]), Pair16<T>::pack(f[2], f[3]),
-                      Pair16<T>::pack(f[4], f[5]), Pair16<T>::pack(f[6], f[7])));
-  } else {
-    *dst = Pair16<T>::round(f[0]);
-  }
-}
-
-// out[t] = sum_s w[t][s] rows[row_of[t][s]] (WEIGHTED) or the plain sum. A
-// thread has VEC columns of one token.
-template <typename T, int VEC, bool WEIGHTED>
-__global__ void __launch_bounds__(256) moe_gather_kernel(const GatherParams p) {
+// out[t] = sum_s w[t][s] rows[row_of[t][s]] (WEIGHTED) or the plain sum.
+// Aligned: a thread has one word of a token's row. ANY: a warp has 31 of them;
+// its lanes load 32 aligned words of each row, and every lane shifts its word
+// out of its own and the next lane's.
+template <typename T, bool ANY, bool WEIGHTED, int KS>
+__global__ void __launch_bounds__(256, 3) moe_gather_kernel(const GatherParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t nv = p.hidden / VEC;
-  const T* rows = static_cast<const T*>(p.rows);
-  T* out = static_cast<T*>(p.out);
-  const int64_t items = p.tokens * nv;
+  const int64_t H = p.hidden, nv = words_of_row<ANY>(H);
+  const int64_t total = 2 * static_cast<int64_t>(p.slots) * H;
+  const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
+  const int64_t per = ANY ? (nv + 30) / 31 * 32 : nv;  // threads of a token
+  const int64_t items = p.tokens * per;
+  // (ANY: per and the stride are multiples of 32, a warp stays together)
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items;
        it += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t t = it / nv;
-    const int64_t c = (it - t * nv) * VEC;
-    float acc[VEC] = {};
-    for (int s = 0; s < p.topk; ++s) {
-      const int row = p.row_of[t * p.topk + s];
-      if (row < 0 || row >= p.slots) continue;
-      float f[VEC];
-      load_f32<T, VEC>(rows + row * p.hidden + c, f);
-      const float w = WEIGHTED ? p.weight[t * p.topk + s] : 1.0f;
+    const int64_t t = it / per;
+    const RowWords<ANY> r(H, t);
+    const int64_t i = it - t * per;
+    const int64_t col = r.column(ANY ? i / 32 * 31 + (i & 31) : i);
+    float acc[8] = {};
+    for (int s0 = 0; s0 < p.topk; s0 += KS) {
+      uint4 w[KS];
+      float weight[KS];
+      int row[KS];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      for (int j = 0; j < KS; ++j) {
+        row[j] = s0 + j < p.topk ? p.row_of[t * p.topk + s0 + j] : -1;
+        if (row[j] >= p.slots) row[j] = -1;
+        weight[j] = WEIGHTED && row[j] >= 0 ? p.weight[t * p.topk + s0 + j] : 1.0f;
+      }
+      if constexpr (!ANY) {
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+          if (row[j] >= 0) w[j] = load_words(p.rows, row[j], H, col);
+      } else {
+        // (a lane up to one word past the row still loads for the one before it)
+        bool inside = true;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          const int64_t at = 2 * (row[j] * H + col) & ~int64_t(15);
+          inside = inside && (row[j] < 0 || col >= H + 8 || (at >= 0 && at + 16 <= total));
+        }
+        if (inside) {
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+            if (row[j] >= 0 && col < H + 8)
+              w[j] = __ldcs(reinterpret_cast<const uint4*>(
+                  rows + (2 * (row[j] * H + col) & ~int64_t(15))));
+        } else {
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+            if (row[j] >= 0 && col < H + 8)
+              w[j] = word_at(rows, 2 * (row[j] * H + col) & ~int64_t(15), total);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          if (row[j] < 0) continue;  // the same in all lanes
+          const uint4 next = make_uint4(__shfl_down_sync(0xFFFFFFFFu, w[j].x, 1),
+                                        __shfl_down_sync(0xFFFFFFFFu, w[j].y, 1),
+                                        __shfl_down_sync(0xFFFFFFFFu, w[j].z, 1),
+                                        __shfl_down_sync(0xFFFFFFFFu, w[j].w, 1));
+          w[j] = shift_out(w[j], next, static_cast<uint32_t>(2 * (row[j] * H + col)) & 15u);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        if (row[j] < 0) continue;
+        float f[8];
+        unpack8<T>(w[j], f);
+#pragma unroll
+        for (int i8 = 0; i8 < 8; ++i8) acc[i8] = fmaf(weight[j], f[i8], acc[i8]);
+      }
     }
-    store_f32<T, VEC>(out + t * p.hidden + c, acc);
+    if (!ANY || (lane_id() < 31 && col < H)) store_words<ANY>(p.out, r, col, pack8<T>(acc));
   }
 }
 
 // d_rows[row] = w d_out[t], d_weight[t][s] = <d_out[t], rows[row]>: a CTA per
-// token, its threads' partial dot products added in a fixed order.
+// token. A thread adds its words' products per slot, the warps' sums are added
+// in a fixed order.
 constexpr int kGradThreads = 128;
 
-template <typename T, int VEC>
+template <typename T, bool ANY, int KS>
 __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const GatherParams p) {
   __shared__ float part[64][kGradThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t nv = p.hidden / VEC;
+  const int64_t H = p.hidden, nv = words_of_row<ANY>(H);
+  const int64_t t = blockIdx.x;
   const int warp = threadIdx.x >> 5;
-  const uint32_t lane = lane_id();
-  const T* rows = static_cast<const T*>(p.rows);
-  T* d_rows = static_cast<T*>(p.out);
-  if (static_cast<int>(blockIdx.x) < p.tokens) {
-    const int64_t t = blockIdx.x;
-    const T* d_out = static_cast<const T*>(p.d_out) + t * p.hidden;
-    for (int s = 0; s < p.topk; ++s) {
-      const int row = p.row_of[t * p.topk + s];
-      float dot = 0.0f;
-      if (row >= 0 && row < p.slots) {
-        const float w = p.weight[t * p.topk + s];
-        for (int64_t v = threadIdx.x; v < nv; v += kGradThreads) {
-          float d[VEC], r[VEC];
-          load_f32<T, VEC>(d_out + v * VEC, d);
-          load_f32<T, VEC>(rows + row * p.hidden + v * VEC, r);
+  const int64_t total = 2 * static_cast<int64_t>(p.tokens) * H;
+  const int64_t total_rows = 2 * static_cast<int64_t>(p.slots) * H;
+  const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
+  const uint8_t* d_out = static_cast<const uint8_t*>(p.d_out);
+  for (int s0 = 0; s0 < p.topk; s0 += KS) {
+    float dot[KS] = {}, w[KS];
+    int row[KS];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            dot = fmaf(d[i], r[i], dot);
-            d[i] *= w;
+    for (int j = 0; j < KS; ++j) {
+      row[j] = s0 + j < p.topk ? p.row_of[t * p.topk + s0 + j] : -1;
+      if (row[j] >= p.slots) row[j] = -1;
+      w[j] = row[j] >= 0 ? p.weight[t * p.topk + s0 + j] : 0.0f;
+    }
+    for (int64_t v = threadIdx.x; v < nv; v += kGradThreads) {
+      if constexpr (!ANY) {
+        uint4 x[KS];
+        float d[8];
+        unpack8<T>(*reinterpret_cast<const uint4*>(d_out + 2 * (t * H + 8 * v)), d);
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+          if (row[j] >= 0) x[j] = load_words(p.rows, row[j], H, 8 * v);
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          if (row[j] < 0) continue;
+          float f[8], o[8];
+          unpack8<T>(x[j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = fmaf(d[i], f[i], dot[j]);
+            o[i] = d[i] * w[j];
           }
-          store_f32<T, VEC>(d_rows + row * p.hidden + v * VEC, d);
+          store_words<false>(p.out, RowWords<false>(H, row[j]), 8 * v, pack8<T>(o));
+        }
+      } else {
+        // the words of rows and d_rows, which start alike, differ from slot to
+        // slot, and so does what they need of d_out. One slot after the other:
+        // with the loads of four in flight the registers cost more than that
+        // gains (123 against 82 us, 5003 tokens, 6 slots, 2047 columns)
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          if (row[j] < 0) continue;
+          const RowWords<true> r(H, row[j]);
+          const int64_t col = r.column(v);
+          if (col >= H) continue;
+          float d[8], f[8], o[8];
+          unpack8<T>(bytes_at(d_out, 2 * (t * H + col), total), d);
+          unpack8<T>(word_at(rows, 2 * (r.start + col), total_rows), f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool in = col + i >= 0 && col + i < H;  // else a neighbour's element
+            dot[j] = in ? fmaf(d[i], f[i], dot[j]) : dot[j];
+            o[i] = d[i] * w[j];
+          }
+          store_words<true>(p.out, r, col, pack8<T>(o));
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-      if (lane == 0) part[s][warp] = dot;
     }
-    __syncthreads();
-    for (int s = threadIdx.x; s < p.topk; s += kGradThreads) {
-      float dot = 0.0f;
-      for (int w = 0; w < kGradThreads / 32; ++w) dot += part[s][w];
-      p.d_weight[t * p.topk + s] = dot;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
+      if (lane_id() == 0 && s0 + j < p.topk) part[s0 + j][warp] = dot[j];
     }
   }
+  __syncthreads();
+  for (int s = threadIdx.x; s < p.topk; s += kGradThreads) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGradThreads / 32; ++i) dot += part[s][i];
+    p.d_weight[t * p.topk + s] = dot;
+  }
   // rows without a slot
-  const int kept = min(max(p.offsets[p.experts], 0), p.slots);
-  const int64_t tail = static_cast<int64_t>(p.slots - kept) * nv;
-  float z[VEC] = {};
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x; i < tail;
-       i += static_cast<int64_t>(gridDim.x) * kGradThreads)
-    store_f32<T, VEC>(d_rows + kept * p.hidden + i * VEC, z);
+  MoeParams tail = {};
+  tail.slots = p.slots;
+  tail.hidden = H;
+  tail.rows = p.out;
+  clear_tail<MOE_COPY>(tail, min(max(p.offsets[p.experts], 0), p.slots),
+                       static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x,
+                       static_cast<int64_t>(gridDim.x) * kGradThreads);
 }
 
 // -------------------------------------------------------------- quantisation
-// 1 x 128 blocks: 16 elements a lane, 8 lanes a block.
+// 1 x 128 blocks: 16 elements a lane, 8 lanes a block. A thread has two such
+// runs, 256 apart, both in flight.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t m, int64_t k, const uint4* x,
                                                             uint4* q, float* scale) {
@@ -393,76 +669,92 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t m, int64_t k
   const int64_t nv = k / 16, blocks = (k + 127) / 128;
   const int64_t padded = blocks * 8;  // lanes of a row, whole blocks
   const int64_t items = m * padded;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  // whole warps go round: items is a multiple of 8, the shuffles stay in a block
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-       it - static_cast<int64_t>(lane_id()) < items; it += step) {
-    const int64_t r = it / padded, v = it - r * padded;
-    const bool in = it < items && v < nv;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (in) {
-      a = __ldcs(x + (r * nv + v) * 2);
-      b = __ldcs(x + (r * nv + v) * 2 + 1);
+  // (items is a multiple of 8: the shuffles stay in a block)
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 512 + threadIdx.x;
+  uint4 a[2], b[2];
+  int64_t r[2], v[2];
+  bool in[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t it = first + 256 * i;
+    r[i] = it / padded;
+    v[i] = it - r[i] * padded;
+    in[i] = it < items && v[i] < nv;
+    a[i] = make_uint4(0, 0, 0, 0);
+    b[i] = a[i];
+    if (in[i]) {
+      a[i] = __ldcs(x + (r[i] * nv + v[i]) * 2);
+      b[i] = __ldcs(x + (r[i] * nv + v[i]) * 2 + 1);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
     float f[16];
-    uint32_t mag = unpack16<T>(a, b, f);
+    uint32_t mag = unpack16<T>(a[i], b[i], f);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d));
     float inv;
     const float sc = e4m3_scale(mag, inv);
-    if (in) {
-      q[r * nv + v] = quant16(f, inv);
-      if ((v & 7) == 0) scale[r * blocks + (v >> 3)] = sc;
+    if (in[i]) {
+      __stcs(q + r[i] * nv + v[i], quant16(f, inv));
+      if ((v[i] & 7) == 0) scale[r[i] * blocks + (v[i] >> 3)] = sc;
     }
   }
 }
 
 // 128 x 128 blocks: a CTA per block, its elements held in registers between
-// the maximum and the rounding.
+// the maximum and the rounding; three CTAs an SM keep loads in flight while
+// others convert.
+constexpr int kBlockThreads = 512;
+
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_blocks_kernel(int64_t m, int64_t k, int blocks_k,
-                                                              const uint4* x, uint4* q,
-                                                              float* scale) {
-  __shared__ uint32_t warp_mag[8];
+__global__ void __launch_bounds__(kBlockThreads, 3)
+    quantize_blocks_kernel(int64_t m, int64_t k, int blocks_k, const uint4* x, uint4* q,
+                           float* scale) {
+  __shared__ uint32_t warp_mag[kBlockThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int64_t nv = k / 16;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x / blocks_k) * 128;
-  const int kb = blockIdx.x % blocks_k;
-  const int64_t v = static_cast<int64_t>(kb) * 8 + (threadIdx.x & 7);
-  float f[4][16];
-  uint32_t mag = 0;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / blocks_k) * 128 + (threadIdx.x >> 3);
+  const int64_t v = static_cast<int64_t>(blockIdx.x % blocks_k) * 8 + (threadIdx.x & 7);
+  uint4 a[2], b[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + 32 * i + (threadIdx.x >> 3);
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = r0 + (kBlockThreads / 8) * i;
+    a[i] = make_uint4(0, 0, 0, 0);
+    b[i] = a[i];
     if (r < m && v < nv) {
-      a = __ldcs(x + (r * nv + v) * 2);
-      b = __ldcs(x + (r * nv + v) * 2 + 1);
+      a[i] = __ldcs(x + (r * nv + v) * 2);
+      b[i] = __ldcs(x + (r * nv + v) * 2 + 1);
     }
-    mag = max(mag, unpack16<T>(a, b, f[i]));
   }
+  float f[16];
+  uint32_t mag = max(unpack16<T>(a[0], b[0], f), unpack16<T>(a[1], b[1], f));
   mag = __reduce_max_sync(0xFFFFFFFFu, mag);
   if ((threadIdx.x & 31) == 0) warp_mag[threadIdx.x >> 5] = mag;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) mag = max(mag, warp_mag[w]);
+  for (int w = 0; w < kBlockThreads / 32; ++w) mag = max(mag, warp_mag[w]);
   float inv;
   const float sc = e4m3_scale(mag, inv);
   if (threadIdx.x == 0) scale[blockIdx.x] = sc;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + 32 * i + (threadIdx.x >> 3);
-    if (r < m && v < nv) q[r * nv + v] = quant16(f[i], inv);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = r0 + (kBlockThreads / 8) * i;
+    unpack16<T>(a[i], b[i], f);
+    if (r < m && v < nv) __stcs(q + r * nv + v, quant16(f, inv));
   }
 }
 
 template <typename T>
 cudaError_t dispatch_t(const MoeParams& p, int copy, cudaStream_t stream, int pdl) {
-  const dim3 grid(p.num_chunks, copy == MOE_SORT_ONLY ? 1 : p.segments, 1);
+  const bool any = p.hidden % 8 != 0;
+  // few slots: the sort and the copies in one kernel
+  const int fused = p.fused ? copy : MOE_SORT_ONLY;
+  const dim3 grid(p.num_chunks, fused == MOE_SORT_ONLY ? 1 : p.segments, 1);
   const size_t smem =
       ((2 + kRankWarps) * static_cast<size_t>(p.experts) + p.chunk_tokens * p.topk) * 4;
-  auto go = [&](auto kernel) -> cudaError_t {
+  auto sort = [&](auto kernel) -> cudaError_t {
     if (smem > 48 * 1024) {
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -471,10 +763,60 @@ cudaError_t dispatch_t(const MoeParams& p, int copy, cudaStream_t stream, int pd
     }
     return launch(kernel, grid, kSortThreads, smem, stream, pdl, p);
   };
-  if (copy == MOE_SORT_ONLY) return go(moe_dispatch_kernel<T, MOE_SORT_ONLY, 1>);
-  if (copy == MOE_COPY_FP8) return go(moe_dispatch_kernel<T, MOE_COPY_FP8, 8>);
-  return p.hidden % 8 == 0 ? go(moe_dispatch_kernel<T, MOE_COPY, 8>)
-                           : go(moe_dispatch_kernel<T, MOE_COPY, 1>);
+  const cudaError_t e =
+      fused == MOE_SORT_ONLY  ? sort(moe_dispatch_kernel<T, MOE_SORT_ONLY, false>)
+      : fused == MOE_COPY_FP8 ? sort(moe_dispatch_kernel<T, MOE_COPY_FP8, false>)
+      : any                   ? sort(moe_dispatch_kernel<T, MOE_COPY, true>)
+                              : sort(moe_dispatch_kernel<T, MOE_COPY, false>);
+  if (e != cudaSuccess || fused == copy) return e;
+  const int64_t parts = copy == MOE_COPY_FP8 ? (p.hidden / 16 + 31) / 32
+                        : any ? ((p.hidden + 14) / 8 + 32 * kCopyWords - 1) / (32 * kCopyWords)
+                              : (p.hidden / 8 + 32 * kCopyWords - 1) / (32 * kCopyWords);
+  auto go = [&](auto kernel) {
+    return launch(kernel, dim3(static_cast<unsigned>((p.tokens * parts + 7) / 8)), 256, 0, stream,
+                  pdl, p);
+  };
+  return copy == MOE_COPY_FP8 ? go(moe_copy_kernel<T, MOE_COPY_FP8, false>)
+         : any                ? go(moe_copy_kernel<T, MOE_COPY, true>)
+                              : go(moe_copy_kernel<T, MOE_COPY, false>);
+}
+
+// calls f with the number of slots at once
+template <typename F>
+cudaError_t for_slots(int topk, F f) {
+  if (topk <= 2) return f(std::integral_constant<int, 2>());
+  if (topk <= 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, 8>());
+}
+
+template <typename T>
+cudaError_t gather_t(const GatherParams& p, int sms, cudaStream_t stream, int pdl) {
+  const bool any = p.hidden % 8 != 0;
+  const int64_t items =
+      p.tokens * (any ? ((p.hidden + 14) / 8 + 30) / 31 * 32 : p.hidden / 8);
+  const int64_t want = (items + 255) / 256, most = static_cast<int64_t>(sms) * 64;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+  return for_slots(p.topk, [&](auto ks) {
+    constexpr int KS = decltype(ks)::value;
+    auto go = [&](auto kernel) { return launch(kernel, grid, 256, 0, stream, pdl, p); };
+    if (p.weight)
+      return any ? go(moe_gather_kernel<T, true, true, KS>)
+                 : go(moe_gather_kernel<T, false, true, KS>);
+    return any ? go(moe_gather_kernel<T, true, false, KS>)
+               : go(moe_gather_kernel<T, false, false, KS>);
+  });
+}
+
+template <typename T>
+cudaError_t grad_t(const GatherParams& p, cudaStream_t stream, int pdl) {
+  const dim3 grid(static_cast<unsigned>(p.tokens));
+  const bool any = p.hidden % 8 != 0;
+  return for_slots(p.topk, [&](auto ks) {
+    constexpr int KS = decltype(ks)::value;
+    auto go = [&](auto kernel) { return launch(kernel, grid, kGradThreads, 0, stream, pdl, p); };
+    return any ? go(moe_combine_grad_kernel<T, true, KS>)
+               : go(moe_combine_grad_kernel<T, false, KS>);
+  });
 }
 
 }  // namespace
@@ -494,49 +836,29 @@ cudaError_t launch_moe_dispatch(const MoeParams& p, int copy, int bf16, cudaStre
 
 cudaError_t launch_moe_gather(const GatherParams& p, int bf16, int sms, cudaStream_t stream,
                               int pdl) {
-  const bool vec = p.hidden % 8 == 0;
-  const int64_t items = p.tokens * (vec ? p.hidden / 8 : p.hidden);
-  const int64_t want = (items + 255) / 256, most = static_cast<int64_t>(sms) * 16;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-  auto go = [&](auto kernel) { return launch(kernel, grid, 256, 0, stream, pdl, p); };
-  if (p.weight) {
-    if (bf16)
-      return vec ? go(moe_gather_kernel<__nv_bfloat16, 8, true>)
-                 : go(moe_gather_kernel<__nv_bfloat16, 1, true>);
-    return vec ? go(moe_gather_kernel<__half, 8, true>) : go(moe_gather_kernel<__half, 1, true>);
-  }
-  if (bf16)
-    return vec ? go(moe_gather_kernel<__nv_bfloat16, 8, false>)
-               : go(moe_gather_kernel<__nv_bfloat16, 1, false>);
-  return vec ? go(moe_gather_kernel<__half, 8, false>) : go(moe_gather_kernel<__half, 1, false>);
+  return bf16 ? gather_t<__nv_bfloat16>(p, sms, stream, pdl)
+              : gather_t<__half>(p, sms, stream, pdl);
 }
 
 cudaError_t launch_moe_combine_grad(const GatherParams& p, int bf16, cudaStream_t stream,
                                     int pdl) {
-  const dim3 grid(static_cast<unsigned>(p.tokens));
-  const bool vec = p.hidden % 8 == 0;
-  auto go = [&](auto kernel) { return launch(kernel, grid, kGradThreads, 0, stream, pdl, p); };
-  if (bf16)
-    return vec ? go(moe_combine_grad_kernel<__nv_bfloat16, 8>)
-               : go(moe_combine_grad_kernel<__nv_bfloat16, 1>);
-  return vec ? go(moe_combine_grad_kernel<__half, 8>) : go(moe_combine_grad_kernel<__half, 1>);
+  return bf16 ? grad_t<__nv_bfloat16>(p, stream, pdl) : grad_t<__half>(p, stream, pdl);
 }
 
 cudaError_t launch_fp8_quantize(int64_t m, int64_t k, int bf16, int block_rows, const void* x,
-                                void* q, float* scale, int sms, cudaStream_t stream, int pdl) {
+                                void* q, float* scale, cudaStream_t stream, int pdl) {
   const uint4* src = static_cast<const uint4*>(x);
   uint4* dst = static_cast<uint4*>(q);
   const int64_t blocks_k = (k + 127) / 128;
   if (block_rows == 128) {
     const dim3 grid(static_cast<unsigned>((m + 127) / 128 * blocks_k));
     auto go = [&](auto kernel) {
-      return launch(kernel, grid, 256, 0, stream, pdl, m, k, static_cast<int>(blocks_k), src, dst,
-                    scale);
+      return launch(kernel, grid, kBlockThreads, 0, stream, pdl, m, k, static_cast<int>(blocks_k),
+                    src, dst, scale);
     };
     return bf16 ? go(quantize_blocks_kernel<__nv_bfloat16>) : go(quantize_blocks_kernel<__half>);
   }
-  const int64_t want = (m * blocks_k * 8 + 255) / 256, most = static_cast<int64_t>(sms) * 16;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+  const dim3 grid(static_cast<unsigned>((m * blocks_k * 8 + 511) / 512));
   auto go = [&](auto kernel) {
     return launch(kernel, grid, 256, 0, stream, pdl, m, k, src, dst, scale);
   };

@@ -13,6 +13,7 @@ struct MoeParams {
   int32_t chunk_tokens;  // tokens per CTA of the sort
   int32_t num_chunks;
   int32_t one_pass;      // 1: every CTA counts all slots; 0: counts from `counts`
+  int32_t fused;         // 1: the sort kernel copies too
   int32_t segments;      // CTAs that share the copies of one chunk (along hidden)
   int32_t* counts;       // [num_chunks][experts], written by the count kernel
   const int32_t* expert;
@@ -52,6 +53,6 @@ cudaError_t launch_moe_combine_grad(const GatherParams& p, int bf16, cudaStream_
                                     int pdl);
 
 cudaError_t launch_fp8_quantize(int64_t m, int64_t k, int bf16, int block_rows, const void* x,
-                                void* q, float* scale, int sms, cudaStream_t stream, int pdl);
+                                void* q, float* scale, cudaStream_t stream, int pdl);
 
 }  // namespace gf

@@ -69,6 +69,7 @@ struct gf_plan {
   int chunk_tokens;      // tokens per CTA of the sort
   int num_chunks;
   int one_pass;          // every CTA counts all slots itself: no count kernel
+  int fused;             // the sort kernel copies the rows too
   void* d_work;          // the sort's counts per chunk and expert; fp8 partial sums
   size_t work_bytes;
 };

@@ -988,7 +988,7 @@ GF_API gf_status gf_plan_describe(const gf_plan* p, int32_t* tile_m, int32_t* ti
 GF_API gf_status gf_plan_launches(const gf_plan* p, int32_t* launches) {
   if (!p || !launches) return fail(GF_ERR_INVALID_VALUE);
   if (p->epi == gf::EPI_MOE) {
-    *launches = p->one_pass ? 1 : 2;
+    *launches = (p->one_pass ? 0 : 1) + 1 + (p->fused ? 0 : 1);  // count, sort, copies
     return GF_OK;
   }
   const bool finalize = has_bgrad(p->epi) && p->bgrad_mode != GF_BGRAD_ATOMIC;

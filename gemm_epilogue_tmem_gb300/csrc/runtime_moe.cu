@@ -18,8 +18,10 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Slots up to which every CTA counts all of them itself, without the count
+// kernel; and up to which the sort kernel copies the rows too, without a copy
 // kernel.
-constexpr int64_t kOnePassSlots = 4096;
+constexpr int64_t kOnePassSlots = 32768;
+constexpr int64_t kFusedSlots = 4096;
 
 bool is_moe(const gf_plan* p) { return p != nullptr && p->epi == gf::EPI_MOE; }
 
@@ -43,6 +45,7 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   prm.chunk_tokens = p->chunk_tokens;
   prm.num_chunks = p->num_chunks;
   prm.one_pass = p->one_pass;
+  prm.fused = p->fused;
   prm.counts = static_cast<int32_t*>(p->d_work);
   prm.expert = expert;
   prm.offsets = offsets;
@@ -117,6 +120,7 @@ GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64
   p->chunk_tokens = static_cast<int>(chunk);
   p->num_chunks = static_cast<int>(chunks);
   p->one_pass = one_pass ? 1 : 0;
+  p->fused = tokens * topk <= kFusedSlots ? 1 : 0;
   p->grid = static_cast<int>(chunks);
   return p;
 }
@@ -197,8 +201,10 @@ GF_API gf_status gf_fp8_quantize(int64_t m, int64_t k, gf_dtype dtype, int32_t b
       (block_rows != 1 && block_rows != 128))
     return runtime_fail(GF_ERR_INVALID_VALUE);
   if (k % 16 != 0) return runtime_fail(GF_ERR_UNSUPPORTED);
-  // one CTA per 128 x 128 block
-  if (((m + 127) / 128) * ((k + 127) / 128) > kMaxDim) return runtime_fail(GF_ERR_UNSUPPORTED);
+  // one CTA per 128 x 128 block, or per 64 blocks of 1 x 128
+  const int64_t blocks_k = (k + 127) / 128;
+  if ((block_rows == 128 ? (m + 127) / 128 * blocks_k : m * blocks_k / 64 + 1) > kMaxDim)
+    return runtime_fail(GF_ERR_UNSUPPORTED);
   const bool empty = m == 0 || k == 0;
   if (!empty && (!given(x) || !given(q) || !given(scale)))
     return runtime_fail(GF_ERR_INVALID_VALUE);
@@ -207,7 +213,7 @@ GF_API gf_status gf_fp8_quantize(int64_t m, int64_t k, gf_dtype dtype, int32_t b
   if (st != GF_OK) return runtime_fail(st);
   if (empty) return GF_OK;
   if (cudaSetDevice(dev) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
-  return gf::launch_fp8_quantize(m, k, dtype == GF_BF16, block_rows, x, q, scale, sms,
+  return gf::launch_fp8_quantize(m, k, dtype == GF_BF16, block_rows, x, q, scale,
                                  reinterpret_cast<cudaStream_t>(stream), 1) == cudaSuccess
              ? GF_OK
              : runtime_fail(GF_ERR_CUDA);

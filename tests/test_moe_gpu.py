@@ -27,7 +27,7 @@ DTYPES = [gf.GF_F16, gf.GF_BF16]
 SHAPES = [
     (1, 1, 1, 1), (1, 8, 128, 5120), (0, 2, 4, 64), (3, 2, 4, 7), (17, 3, 5, 128), (64, 8, 128, 136),
     (33, 64, 70, 24), (500, 8, 60, 250), (513, 8, 1000, 16), (999, 6, 1024, 40), (5003, 2, 3, 33),
-    (9001, 1, 1, 8), (4100, 5, 256, 72),
+    (9001, 1, 1, 8), (4100, 5, 256, 72), (9000, 4, 130, 16), (4100, 8, 1024, 24), (33000, 1, 600, 8),
 ]
 
 
@@ -91,7 +91,7 @@ def test_dispatch(tokens, topk, experts, hidden, dtype, drop):
     want = torch.zeros_like(rows)
     want[:kept] = x[dev(slot_of[:kept] // topk)]
     assert torch.equal(rows, want)
-    assert gf.gf_plan_describe(plan)["launches"] == (1 if slots <= 4096 else 2)
+    assert gf.gf_plan_describe(plan)["launches"] == (1 if slots <= 4096 else 2 if slots <= 32768 else 3)
     plan.free()
 
 
