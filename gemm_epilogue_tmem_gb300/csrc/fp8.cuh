@@ -31,17 +31,20 @@ __device__ __forceinline__ float e4m3_scale(uint32_t mag, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
-// two values times inv, rounded to nearest even e4m3 (lo in the low byte).
+// Two values times inv, rounded to nearest even e4m3 (lo in the low byte).
 // Finite values are at most 448 after scaling; the conversion would saturate
 // infinities, which become NaN here (x * 0 is NaN for infinities and NaN).
+// FINITE: the caller knows that there are none.
+template <bool FINITE = false>
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
-  lo = fmaf(lo, inv, lo * 0.0f);
-  hi = fmaf(hi, inv, hi * 0.0f);
+  lo = FINITE ? lo * inv : fmaf(lo, inv, lo * 0.0f);
+  hi = FINITE ? hi * inv : fmaf(hi, inv, hi * 0.0f);
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+template <bool FINITE = false>
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv) {
-  return e4m3x2(a, b, inv) | (e4m3x2(c, d, inv) << 16);
+  return e4m3x2<FINITE>(a, b, inv) | (e4m3x2<FINITE>(c, d, inv) << 16);
 }
 
 // 16-bit element pairs of a 32-bit word <-> floats
@@ -88,10 +91,12 @@ __device__ __forceinline__ uint32_t unpack16(const uint4& a, const uint4& b, flo
   return mag;
 }
 
+template <bool FINITE = false>
 __device__ __forceinline__ uint4 quant16(const float (&f)[16], float inv) {
-  return make_uint4(e4m3x4(f[0], f[1], f[2], f[3], inv), e4m3x4(f[4], f[5], f[6], f[7], inv),
-                    e4m3x4(f[8], f[9], f[10], f[11], inv),
-                    e4m3x4(f[12], f[13], f[14], f[15], inv));
+  return make_uint4(e4m3x4<FINITE>(f[0], f[1], f[2], f[3], inv),
+                    e4m3x4<FINITE>(f[4], f[5], f[6], f[7], inv),
+                    e4m3x4<FINITE>(f[8], f[9], f[10], f[11], inv),
+                    e4m3x4<FINITE>(f[12], f[13], f[14], f[15], inv));
 }
 
 }  // namespace gf

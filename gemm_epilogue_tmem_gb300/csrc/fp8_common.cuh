@@ -212,9 +212,61 @@ __device__ __forceinline__ int group_of_tile(const GroupTable& g, int groups, in
   return lo;
 }
 
+// silu(g) u = g u / (1 + 2^(-g log2 e)), with the hardware's exponential and
+// reciprocal (relative errors of 2^-22 and 2^-23): the result is rounded to
+// e4m3. Below g = -87 the reciprocal is flushed to the limit 0.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  // e^-g overflows to infinity below -88, where g / infinity is the limit 0
-  return __fdividef(g, 1.0f + __expf(-g)) * u;
+  float t, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+  return g * r * u;
+}
+
+// The SwiGLU of a thread's 64 gate (acc[0..31], two a register pair) and up
+// columns (acc[32..63]), in place of the gate; columns from `valid` on are zero.
+// Returns the largest finite magnitude's bits; `finite`: whether all are.
+__device__ __forceinline__ uint32_t swiglu64(uint64_t (&acc)[64], int valid, bool& finite) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float2 g = split2(acc[j]), u = split2(acc[32 + j]);
+    acc[j] = pack2(silu_mul(g.x, u.x), silu_mul(g.y, u.y));
+  }
+  if (valid < 64) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float2 h = split2(acc[j]);
+      acc[j] = pack2(2 * j < valid ? h.x : 0.0f, 2 * j + 1 < valid ? h.y : 0.0f);
+    }
+  }
+  uint32_t mag = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float2 h = split2(acc[j]);
+    mag = max(mag, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));
+  }
+  finite = mag < 0x7F800000u;
+  if (!finite) {
+    mag = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float2 h = split2(acc[j]);
+      mag = max(mag, max(finite_mag_bits(h.x), finite_mag_bits(h.y)));
+    }
+  }
+  return mag;
+}
+
+// columns 16 i .. 16 i + 15 of swiglu64's result in e4m3
+__device__ __forceinline__ uint4 quant_columns(const uint64_t (&acc)[64], int i, float inv,
+                                               bool finite) {
+  float f[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 h = split2(acc[8 * i + j]);
+    f[2 * j] = h.x;
+    f[2 * j + 1] = h.y;
+  }
+  return finite ? quant16<true>(f, inv) : quant16<false>(f, inv);
 }
 
 }  // namespace gf

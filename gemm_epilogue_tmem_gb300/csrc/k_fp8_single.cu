@@ -304,16 +304,10 @@ __global__ void __launch_bounds__(kThreadsSingle, 1)
         // h of this row's 64 columns, its largest magnitude over the tile's
         // 128 with the other warp of the quarter
         const int n0 = nt * 128 + 64 * sub;
-        float h[64];
+        bool finite = true;
         uint32_t mag = 0;
         if (busy) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 gate = split2(acc[j]), up = split2(acc[32 + j]);
-            h[2 * j] = n0 + 2 * j < p.N ? silu_mul(gate.x, up.x) : 0.0f;
-            h[2 * j + 1] = n0 + 2 * j + 1 < p.N ? silu_mul(gate.y, up.y) : 0.0f;
-            mag = max(mag, max(finite_mag_bits(h[2 * j]), finite_mag_bits(h[2 * j + 1])));
-          }
+          mag = swiglu64(acc, p.N - n0, finite);
           row_mag[TR * sub + r] = mag;
         }
         named_bar_sync(1, kEpiThreads);
@@ -324,12 +318,9 @@ __global__ void __launch_bounds__(kThreadsSingle, 1)
           if (sub == 0 && r < rows)
             p.out_scale[static_cast<int64_t>(row + r) * p.num_n_blocks + nt] = sc;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = h[16 * j + i];
-            *reinterpret_cast<uint4*>(stg + lane * 80 + 16 * j) = quant16(f, inv);
-          }
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(stg + lane * 80 + 16 * j) =
+                quant_columns(acc, j, inv, finite);
           __syncwarp();
           const int n = n0 + 16 * static_cast<int>(lane & 3u);
 #pragma unroll

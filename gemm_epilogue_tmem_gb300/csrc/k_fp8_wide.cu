@@ -389,15 +389,8 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         // h of this row's 64 columns, its largest magnitude over the tile's
         // 128 with the other warp of the quarter
         const int n = nt * 128 + 64 * sub;
-        float h[64];
-        uint32_t mag = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 gate = split2(acc[j]), up = split2(acc[32 + j]);
-          h[2 * j] = n + 2 * j < p.N ? silu_mul(gate.x, up.x) : 0.0f;
-          h[2 * j + 1] = n + 2 * j + 1 < p.N ? silu_mul(gate.y, up.y) : 0.0f;
-          mag = max(mag, max(finite_mag_bits(h[2 * j]), finite_mag_bits(h[2 * j + 1])));
-        }
+        bool finite;
+        uint32_t mag = swiglu64(acc, p.N - n, finite);
         row_mag[128 * sub + 32 * q + lane] = mag;
         named_bar_sync(1, kEpiThreadsWide);
         mag = max(mag, row_mag[128 * (sub ^ 1) + 32 * q + lane]);
@@ -406,12 +399,8 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         if (sub == 0 && my_row < row_end)
           p.out_scale[static_cast<int64_t>(my_row) * p.num_n_blocks + nt] = sc;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] = h[16 * j + i];
-          *reinterpret_cast<uint4*>(my_stg + 16 * j) = quant16(f, inv);
-        }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(my_stg + 16 * j) = quant_columns(acc, j, inv, finite);
         fence_proxy_async_smem();
         if (my_row < row_end && n < p.N)
           bulk_store(static_cast<uint8_t*>(p.out) + static_cast<int64_t>(my_row) * p.N + n,
