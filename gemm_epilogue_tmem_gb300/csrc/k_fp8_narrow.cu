@@ -33,13 +33,20 @@ constexpr int kEpiThreads = 128;
 constexpr int kBBytes = 128 * 128;
 constexpr int kRing = 8;  // blocks of scales in flight
 
+// shared memory besides the stages and the table of groups
 constexpr int narrow_fixed(int tr) {
-  return kSmemAlignSlack + kSmemCtrlBytes + 2 * (kFp8MaxGroups + 2) * 4 + 4 * tr * 4 +
-         kRing * (tr + 4) * 4;
+  return kSmemAlignSlack + kSmemCtrlBytes + 4 * tr * 4 + kRing * (tr + 4) * 4;
 }
+constexpr int narrow_table(int groups) { return 2 * (groups + 2) * 4; }
+// 16-row tiles: two CTAs fit on an SM (113 KB each, with the table of 128
+// groups), so that the next launch's are set up and waiting when this one ends;
+// their 90 KB of stages still cover the HBM latency (45 KB at the copy rate).
+// 64-row tiles take the whole SM.
+constexpr int kSmemHalf = 113 * 1024;
 constexpr int narrow_stages(int tr, bool dual) {
   const int stage = (dual ? 2 : 1) * kBBytes + tr * 128;
-  const int left = kSmemPerCta - narrow_fixed(tr);
+  const int left = tr == 16 ? kSmemHalf - narrow_fixed(tr) - narrow_table(128)
+                            : kSmemPerCta - narrow_fixed(tr) - narrow_table(kFp8MaxGroups);
   return left / stage > 12 ? 12 : left / stage;
 }
 
@@ -55,9 +62,10 @@ struct NarrowCfg {
                                    : kBufs * kAccCols <= 128 ? 128
                                    : kBufs * kAccCols <= 256 ? 256
                                                              : 512;
-  static constexpr int kSmemBytes = narrow_fixed(TR) + kStages * kStageBytes;
+  static constexpr int kSmemBytes = narrow_fixed(TR) + kStages * kStageBytes;  // + the table
   static_assert(16 * kStages + 16 * kBufs + 16 + 16 * kRing <= kSmemCtrlBytes, "control region");
-  static_assert(kSmemBytes <= kSmemPerCta && kStages >= 3, "shared memory budget");
+  static_assert(kSmemBytes + narrow_table(kFp8MaxGroups) <= kSmemPerCta && kStages >= 3,
+                "shared memory budget");
 };
 
 // A run of k-blocks of one tile.
@@ -141,7 +149,7 @@ __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[CH
 }
 
 template <typename T, int TR, bool DUAL>
-__global__ void __launch_bounds__(kThreadsNarrow, 1)
+__global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmB2, const Fp8Params p) {
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kThreadsNarrow, 1)
   uint32_t* warp_mag = reinterpret_cast<uint32_t*>(ring + kRing * C::kSlot);
   GroupTable table;
   table.row0 = reinterpret_cast<int32_t*>(warp_mag + 4 * TR);
-  table.tile0 = table.row0 + kFp8MaxGroups + 2;
+  table.tile0 = table.row0 + p.groups + 2;
   __shared__ int last_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -540,9 +548,10 @@ __global__ void __launch_bounds__(kThreadsNarrow, 1)
 template <typename T, int TR, bool DUAL>
 cudaError_t launch_narrow(const Fp8LaunchArgs& a) {
   auto kernel = fp8_narrow_kernel<T, TR, DUAL>;
-  constexpr int smem = NarrowCfg<TR, DUAL>::kSmemBytes;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = NarrowCfg<TR, DUAL>::kSmemBytes + narrow_table(a.params->groups);
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      NarrowCfg<TR, DUAL>::kSmemBytes + narrow_table(kFp8MaxGroups));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.grid, 1, 1);

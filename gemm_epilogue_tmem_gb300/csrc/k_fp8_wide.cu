@@ -53,7 +53,7 @@ constexpr int kStagesWide = (kSmemPerCta - kSmemAlignSlack - kSmemCtrlBytes - kS
                             kStageBytes;
 constexpr int kSmemWide = kSmemAlignSlack + kStagesWide * kStageBytes + kSmemCtrlBytes +
                           kStagingBytes + kTableBytes + kMagBytes + kScaleBytes;
-constexpr int kRasterRows = 8;  // row tiles visited together, column by column
+constexpr int kRasterRows = 16;  // row tiles visited together, column by column
 
 // bulk copy of `bytes` (a multiple of 16) from shared to global memory
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {

@@ -19,6 +19,11 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// scales are read and written one at a time: a part of a larger array will do
+bool given_scale(const void* p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
 // GF_OPT_KERNEL
 enum : int { kNarrow16 = 1, kNarrow64 = 2, kSingle = 3, kPair = 4 };
 
@@ -149,10 +154,10 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   const bool dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT;
   const bool empty = p->m == 0 || p->n == 0;
   if (!empty) {
-    if (!given(out) || (dual && !given(out_scale))) return runtime_fail(GF_ERR_INVALID_VALUE);
-    if (p->k > 0 && (!given(A) || !given(a_scale) || !given(B) || !given(b_scale)))
+    if (!given(out) || (dual && !given_scale(out_scale))) return runtime_fail(GF_ERR_INVALID_VALUE);
+    if (p->k > 0 && (!given(A) || !given_scale(a_scale) || !given(B) || !given_scale(b_scale)))
       return runtime_fail(GF_ERR_INVALID_VALUE);
-    if (p->k > 0 && dual && (!given(B2) || !given(b2_scale)))
+    if (p->k > 0 && dual && (!given(B2) || !given_scale(b2_scale)))
       return runtime_fail(GF_ERR_INVALID_VALUE);
     if (offsets == nullptr ? p->groups != 1 : !given(offsets))
       return runtime_fail(GF_ERR_INVALID_VALUE);

@@ -17,6 +17,11 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// scales are read and written one at a time: a part of a larger array will do
+bool given_scale(const void* p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
 // Slots up to which every CTA counts all of them itself, without the count
 // kernel; and up to which the sort kernel copies the rows too, without a copy
 // kernel.
@@ -34,7 +39,7 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
     return runtime_fail(GF_ERR_INVALID_VALUE);
   if (some && copy != gf::MOE_SORT_ONLY && (!given(x) || !given(rows)))
     return runtime_fail(GF_ERR_INVALID_VALUE);
-  if (some && copy == gf::MOE_COPY_FP8 && !given(scale)) return runtime_fail(GF_ERR_INVALID_VALUE);
+  if (some && copy == gf::MOE_COPY_FP8 && !given_scale(scale)) return runtime_fail(GF_ERR_INVALID_VALUE);
   if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
   gf::MoeParams prm = {};
   prm.tokens = static_cast<int32_t>(p->m);
@@ -206,7 +211,7 @@ GF_API gf_status gf_fp8_quantize(int64_t m, int64_t k, gf_dtype dtype, int32_t b
   if ((block_rows == 128 ? (m + 127) / 128 * blocks_k : m * blocks_k / 64 + 1) > kMaxDim)
     return runtime_fail(GF_ERR_UNSUPPORTED);
   const bool empty = m == 0 || k == 0;
-  if (!empty && (!given(x) || !given(q) || !given(scale)))
+  if (!empty && (!given(x) || !given(q) || !given_scale(scale)))
     return runtime_fail(GF_ERR_INVALID_VALUE);
   int dev = 0, sms = 0;
   const gf_status st = gf::runtime_device(&dev, &sms);

@@ -299,6 +299,8 @@ GF_API gf_status gf_moe_combine_grad_execute(const gf_plan* plan, const int32_t*
  * one; it costs at most one bit of e4m3's exponent range. x: device [m, k] of
  * dtype; q: device bytes [m, k]; scale: device fp32 [ceil(m / block_rows),
  * ceil(k / 128)]. 0 <= m, k < 2^31, k % 16 == 0 (else GF_ERR_UNSUPPORTED).
+ * x and q 16-byte aligned; scales, here and below, as fp32 values are (4 bytes),
+ * so that a part of a larger array will do.
  * Asynchronous on stream; needs no plan and no workspace.
  */
 GF_API gf_status gf_fp8_quantize(int64_t m, int64_t k, gf_dtype dtype, int32_t block_rows,

@@ -65,6 +65,26 @@ def test_quantize_edges(block_rows, dtype):
     np.testing.assert_array_equal(q.view(torch.float8_e4m3fn).double().cpu().numpy(), want)
 
 
+def test_scales_at_any_fp32_address():
+    """Scales that begin at any 4-byte address: quantised into, and read from, parts of larger arrays."""
+    m, n, k = 40, 136, 272
+    x = torch.randn(m, k, generator=gen(4), device="cuda").half()
+    w = torch.randn(n, k, generator=gen(5), device="cuda").half()
+    qa, qb = torch.empty(m, k, dtype=torch.uint8, device="cuda"), torch.empty(n, k, dtype=torch.uint8, device="cuda")
+    plan = gf.gf_fp8_matmul_plan(m, n, k, 1, gf.GF_F16)
+    outs = []
+    for lead in (0, 1, 3):
+        sa, sb = torch.full((lead + m * 3 + 5,), 7.0, device="cuda"), torch.full((lead + 6 + 5,), 7.0, device="cuda")
+        a, b = sa[lead:lead + m * 3], sb[lead:lead + 6]
+        gf.gf_fp8_quantize(m, k, gf.GF_F16, 1, x, qa, a)
+        gf.gf_fp8_quantize(n, k, gf.GF_F16, 128, w, qb, b)
+        assert bool((sa[:lead] == 7).all() and (sa[lead + m * 3:] == 7).all() and (sb[lead + 6:] == 7).all())
+        outs.append(torch.empty(m, n, dtype=torch.half, device="cuda"))
+        gf.gf_fp8_matmul_execute(plan, qa, a, qb, b, out=outs[-1])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    plan.free()
+
+
 def test_quantize_refusals():
     x = torch.zeros(4, 32, dtype=torch.half, device="cuda")
     q, s = torch.zeros(4, 32, dtype=torch.uint8, device="cuda"), torch.zeros(4, 1, device="cuda")
@@ -124,7 +144,7 @@ def by_group(off, a, b):
 SHAPES = [  # m, n, k, groups
     (1, 8, 16, 1), (1, 136, 5120, 1), (3, 128, 128, 1), (16, 256, 384, 1), (17, 264, 272, 1), (64, 520, 1040, 1),
     (65, 128, 2048, 1), (200, 72, 144, 1), (300, 640, 512, 1), (1030, 1288, 656, 1), (2048, 1024, 1024, 1),
-    (40, 256, 256, 5), (500, 136, 400, 7), (1500, 384, 1040, 4), (700, 264, 128, 130), (33, 128, 256, 1024),
+    (40, 256, 256, 5), (500, 136, 400, 7), (3000, 264, 272, 9), (1500, 384, 1040, 4), (700, 264, 128, 130), (33, 128, 256, 1024),
 ]
 
 
@@ -231,6 +251,27 @@ def test_offsets_out_of_range_stay_inside():
         assert torch.equal(out, good)
         assert bool((flat[:4096] == 7).all()) and bool((flat[-4096:] == 7).all())
         plan.free()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_every_tail_length(kernel):
+    """Groups whose rows end on both sides of every tile size, and in more
+    tiles than the grid has CTAs."""
+    counts = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 383, 384, 385, 511, 512, 513] * 3
+    off = np.concatenate([[0], np.cumsum(counts)])
+    m, groups, n, k = int(off[-1]), len(counts), 1416, 144
+    plan = gf.gf_fp8_matmul_plan(m, n, k, groups, gf.GF_BF16)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_KERNEL, kernel)
+    a, b = operand((m, k), 71), operand((groups, n, k), 72)
+    sa, sb = scales((m, 2), 73), scales((groups, 12, 2), 74)
+    out = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    gf.gf_fp8_matmul_execute(plan, a, sa, b, sb, offsets=torch.from_numpy(off.astype(np.int32)).cuda(), out=out)
+    av, bv = values(a, sa, 1), values(b, sb, 128)
+    want, mag = by_group(off, av, bv), by_group(off, av.abs(), bv.abs())
+    bound = (k + 4) * 2.0 ** -23 * mag
+    bound = bound + 2.0 ** -8 * (want.abs() + bound)
+    assert bool(((out.double() - want).abs() <= bound).all())
+    plan.free()
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
