@@ -24,21 +24,32 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kRankWarps = 8;        // warps that rank the slots of a chunk
 constexpr int kMaxChunkSlots = 4096;
+constexpr uint32_t kSortCluster = 8;
 
 template <typename K, typename... A>
-cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, int pdl,
-                   A... args) {
+cudaError_t launch_clusters(K kernel, dim3 grid, unsigned cluster, int threads, size_t smem,
+                            cudaStream_t stream, int pdl, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, int pdl,
+                   A... args) {
+  return launch_clusters(kernel, grid, 1, threads, smem, stream, pdl, args...);
 }
 
 // ------------------------------------------------------------------- the sort
@@ -46,23 +57,16 @@ cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s
 // of a slot is its expert's first row, plus the kept slots of that expert in
 // earlier chunks, in earlier warps of its chunk and earlier in its warp. Every
 // term is a count, so the order is stable and the same in every run.
+//
+// The counts over all slots are made by every cluster of kSortCluster CTAs for
+// itself, a part by each, and shared through its distributed shared memory: one
+// launch and no workspace (65536 slots: 11 us with a kernel that counts the
+// chunks first). Up to kFusedSlots a CTA counts them alone.
 
-// counts[chunk][e]: the chunk's slots of expert e
-__global__ void __launch_bounds__(kSortThreads) moe_count_kernel(const MoeParams p) {
-  extern __shared__ int32_t hist[];
-  grid_dep_wait();
-  grid_dep_launch();
-  for (int e = threadIdx.x; e < p.experts; e += kSortThreads) hist[e] = 0;
-  __syncthreads();
-  const int first = blockIdx.x * p.chunk_tokens * p.topk;
-  const int last = min(p.slots, first + p.chunk_tokens * p.topk);
-  for (int i = first + threadIdx.x; i < last; i += kSortThreads) {
-    const uint32_t e = static_cast<uint32_t>(p.expert[i]);
-    if (e < static_cast<uint32_t>(p.experts)) atomicAdd(&hist[e], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += kSortThreads)
-    p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
+__device__ __forceinline__ int ld_cluster(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
 }
 
 // --------------------------------------------------------- rows of any length
@@ -81,20 +85,25 @@ __device__ __forceinline__ uint4 word_at(const uint8_t* array, int64_t at, int64
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// the 16 bytes that begin `shift` (even, below 16) bytes into a and end in b
+// The 16 bytes that begin `shift` (even, below 16) bytes into a and end in b.
+// The shift is the same for all words of a row, and so for the warp: a branch
+// per 4 bytes of it instead of selecting every word.
 __device__ __forceinline__ uint4 shift_out(const uint4& a, const uint4& b, uint32_t shift) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (shift & 8u) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (shift & 4u) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
   const uint32_t r = 8u * (shift & 2u);
-  return make_uint4(__funnelshift_r(w[0], w[1], r), __funnelshift_r(w[1], w[2], r),
-                    __funnelshift_r(w[2], w[3], r), __funnelshift_r(w[3], w[4], r));
+  switch (shift >> 2) {
+    case 0:
+      return make_uint4(__funnelshift_r(a.x, a.y, r), __funnelshift_r(a.y, a.z, r),
+                        __funnelshift_r(a.z, a.w, r), __funnelshift_r(a.w, b.x, r));
+    case 1:
+      return make_uint4(__funnelshift_r(a.y, a.z, r), __funnelshift_r(a.z, a.w, r),
+                        __funnelshift_r(a.w, b.x, r), __funnelshift_r(b.x, b.y, r));
+    case 2:
+      return make_uint4(__funnelshift_r(a.z, a.w, r), __funnelshift_r(a.w, b.x, r),
+                        __funnelshift_r(b.x, b.y, r), __funnelshift_r(b.y, b.z, r));
+    default:
+      return make_uint4(__funnelshift_r(a.w, b.x, r), __funnelshift_r(b.x, b.y, r),
+                        __funnelshift_r(b.y, b.z, r), __funnelshift_r(b.z, b.w, r));
+  }
 }
 
 // The 16 bytes from byte `at` (even) on, out of the two aligned words around
@@ -105,10 +114,11 @@ __device__ __forceinline__ uint4 bytes_at(const uint8_t* array, int64_t at, int6
                    shift);
 }
 
-// whether both aligned words around byte `at` lie in the array: their loads need
-// no checks, so that those of several rows can be in flight together
-__device__ __forceinline__ bool pair_inside(int64_t at, int64_t total) {
-  return at >= 0 && (at & ~int64_t(15)) + 32 <= total;
+// Whether every aligned word that holds an element of the row, and the word
+// before and after it, lies in an array of `rows` rows of H elements: their
+// loads then need no checks. So it does for all rows but the first and last.
+__device__ __forceinline__ bool row_inside(int row, int rows, int H) {
+  return H >= 32 && row > 0 && row < rows - 1;
 }
 
 // How a row of H 16-bit elements is cut into words of 8. Aligned: column 8 v.
@@ -116,28 +126,30 @@ __device__ __forceinline__ bool pair_inside(int64_t at, int64_t total) {
 // hold neighbours' elements too.
 template <bool ANY>
 struct RowWords {
-  int64_t H, start;  // elements; first element of the row in its array
-  int lead;          // elements before the row in its first word
-  __device__ __forceinline__ RowWords(int64_t h, int64_t row)
-      : H(h), start(row * h), lead(ANY ? static_cast<int>((row * h) & 7) : 0) {}
+  int H;
+  int lead;       // elements before the row in its first word
+  int64_t start;  // first element of the row in its array
+  __device__ __forceinline__ RowWords(int h, int row)
+      : H(h), start(static_cast<int64_t>(row) * h) {
+    lead = ANY ? static_cast<int>(start) & 7 : 0;
+  }
   // column of word v's first element (below 0 in a first word with a lead)
-  __device__ __forceinline__ int64_t column(int64_t v) const { return 8 * v - lead; }
+  __device__ __forceinline__ int column(int v) const { return 8 * v - lead; }
 };
 template <bool ANY>
-__device__ __forceinline__ int64_t words_of_row(int64_t H) {
+__device__ __forceinline__ int words_of_row(int H) {
   return ANY ? (H + 14) / 8 : H / 8;  // the most that a row touches
 }
 
 // elements `col` .. `col` + 7 of an aligned row
-__device__ __forceinline__ uint4 load_words(const void* array, int64_t row, int64_t H,
-                                            int64_t col) {
-  return __ldcs(
-      reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(array) + row * H + col));
+__device__ __forceinline__ uint4 load_words(const void* array, int row, int H, int col) {
+  return __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(array) +
+                                               static_cast<int64_t>(row) * H + col));
 }
 
 // the word at column `col` of the row that the words were cut by
 template <bool ANY>
-__device__ __forceinline__ void store_words(void* array, const RowWords<ANY>& r, int64_t col,
+__device__ __forceinline__ void store_words(void* array, const RowWords<ANY>& r, int col,
                                             const uint4& w) {
   uint16_t* dst = static_cast<uint16_t*>(array) + r.start + col;
   if (!ANY || (col >= 0 && col + 8 <= r.H)) {
@@ -174,41 +186,44 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 constexpr int kCopyWords = 4;  // words a lane holds (U)
 
 template <bool ANY>
-__device__ __forceinline__ void copy_item(const MoeParams& p, int64_t token, int part,
+__device__ __forceinline__ void copy_item(const MoeParams& p, int token, int part,
                                           const int32_t* place) {
   constexpr int U = kCopyWords;
-  const int64_t H = p.hidden;
-  const int64_t v0 = static_cast<int64_t>(part) * (32 * U) + lane_id();
+  const int H = p.hidden;
+  const int v0 = part * (32 * U) + static_cast<int>(lane_id());
   if constexpr (!ANY) {
-    const int64_t nv = H / 8;
-    const uint4* src = static_cast<const uint4*>(p.x) + token * nv;
+    const int nv = H / 8;
+    const uint4* src = static_cast<const uint4*>(p.x) + static_cast<int64_t>(token) * nv + v0;
     uint4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (v0 + 32 * u < nv) v[u] = __ldcs(src + v0 + 32 * u);
+      if (v0 + 32 * u < nv) v[u] = __ldcs(src + 32 * u);
     for (int s = 0; s < p.topk; ++s) {
       const int row = place[s];
       if (row < 0) continue;
-      uint4* dst = static_cast<uint4*>(p.rows) + static_cast<int64_t>(row) * nv;
+      uint4* dst = static_cast<uint4*>(p.rows) + static_cast<int64_t>(row) * nv + v0;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (v0 + 32 * u < nv) __stcs(dst + v0 + 32 * u, v[u]);
+        if (v0 + 32 * u < nv) __stcs(dst + 32 * u, v[u]);
     }
   } else {
     const int64_t total = 2 * static_cast<int64_t>(p.tokens) * H;
     const uint8_t* x = static_cast<const uint8_t*>(p.x);
+    const bool inside = row_inside(token, p.tokens, H);
     for (int s = 0; s < p.topk; ++s) {
       const int row = place[s];
       if (row < 0) continue;
       const RowWords<true> r(H, row);
       // (the row's alignment, and so the shift, is the same for all its words)
-      const int64_t at0 = 2 * (token * H + r.column(v0));
+      const int col0 = r.column(v0);
+      const int64_t at0 = 2 * (static_cast<int64_t>(token) * H + col0);
       const uint32_t shift = static_cast<uint32_t>(at0) & 15u;
       uint4 a[U], b[U];
-      if (pair_inside(at0, total) && pair_inside(at0 + 512 * (U - 1), total)) {
+      if (inside) {
         const uint4* src = reinterpret_cast<const uint4*>(x + at0 - shift);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+          if (col0 + 256 * u >= H) continue;
           a[u] = __ldg(src + 32 * u);
           b[u] = __ldg(src + 32 * u + 1);
         }
@@ -221,7 +236,7 @@ __device__ __forceinline__ void copy_item(const MoeParams& p, int64_t token, int
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t col = r.column(v0 + 32 * u);
+        const int col = col0 + 256 * u;
         if (col < H) store_words<true>(p.rows, r, col, shift_out(a[u], b[u], shift));
       }
     }
@@ -231,16 +246,15 @@ __device__ __forceinline__ void copy_item(const MoeParams& p, int64_t token, int
 // The same, quantised: 16 elements a lane, 8 lanes a block of 128, 512
 // elements a warp.
 template <typename T>
-__device__ __forceinline__ void quant_item(const MoeParams& p, int64_t token, int part,
+__device__ __forceinline__ void quant_item(const MoeParams& p, int token, int part,
                                            const int32_t* place) {
-  const int64_t nv = p.hidden / 16;
-  const int blocks = static_cast<int>((p.hidden + 127) / 128);
+  const int nv = p.hidden / 16, blocks = (p.hidden + 127) / 128;
   const uint32_t lane = lane_id();
-  const int64_t v = static_cast<int64_t>(part) * 32 + lane;
+  const int v = part * 32 + static_cast<int>(lane);
   const bool in = v < nv;
   uint4 a = make_uint4(0, 0, 0, 0), b = a;
   if (in) {
-    const uint4* src = static_cast<const uint4*>(p.x) + (token * nv + v) * 2;
+    const uint4* src = static_cast<const uint4*>(p.x) + (static_cast<int64_t>(token) * nv + v) * 2;
     a = __ldcs(src);
     b = __ldcs(src + 1);
   }
@@ -261,10 +275,9 @@ __device__ __forceinline__ void quant_item(const MoeParams& p, int64_t token, in
 }
 
 template <int COPY, bool ANY>
-__device__ __forceinline__ int copy_parts(int64_t H) {
-  return COPY == MOE_COPY_FP8
-             ? static_cast<int>((H / 16 + 31) / 32)
-             : static_cast<int>((words_of_row<ANY>(H) + 32 * kCopyWords - 1) / (32 * kCopyWords));
+__device__ __forceinline__ int copy_parts(int H) {
+  return COPY == MOE_COPY_FP8 ? (H / 16 + 31) / 32
+                              : (words_of_row<ANY>(H) + 32 * kCopyWords - 1) / (32 * kCopyWords);
 }
 
 // rows [kept, slots) of the output: zeros (e4m3: with scale 1), by thread
@@ -275,7 +288,7 @@ __device__ __forceinline__ void clear_tail(const MoeParams& p, int kept, int64_t
   const int64_t tail = p.slots - kept;
   if (tail <= 0) return;
   if constexpr (COPY == MOE_COPY_FP8) {
-    const int64_t nv = p.hidden / 16, blocks = (p.hidden + 127) / 128;
+    const int64_t nv = p.hidden / 16, blocks = (p.hidden + 127) / 128;  // times rows: 64 bits
     uint4* zero = static_cast<uint4*>(p.rows) + kept * nv;
     for (int64_t i = first; i < tail * nv; i += threads) zero[i] = make_uint4(0, 0, 0, 0);
     float* ones = p.scale + kept * blocks;
@@ -283,7 +296,8 @@ __device__ __forceinline__ void clear_tail(const MoeParams& p, int kept, int64_t
   } else {
     // 16-bit zeros from element `begin` on; the array's aligned words between
     uint16_t* rows = static_cast<uint16_t*>(p.rows);
-    const int64_t begin = kept * p.hidden, end = static_cast<int64_t>(p.slots) * p.hidden;
+    const int64_t begin = static_cast<int64_t>(kept) * p.hidden;
+    const int64_t end = static_cast<int64_t>(p.slots) * p.hidden;
     const int64_t w0 = (begin + 7) / 8, w1 = end / 8;
     for (int64_t i = w0 + first; i < w1; i += threads)
       reinterpret_cast<uint4*>(rows)[i] = make_uint4(0, 0, 0, 0);
@@ -301,12 +315,13 @@ __global__ void __launch_bounds__(256) moe_copy_kernel(const MoeParams p) {
   const int parts = copy_parts<COPY, ANY>(p.hidden);
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (item < static_cast<int64_t>(p.tokens) * parts) {
-    const int64_t token = item / parts;
-    const int part = static_cast<int>(item - token * parts);
+    const int token = static_cast<int>(item / parts);
+    const int part = static_cast<int>(item - static_cast<int64_t>(token) * parts);
+    const int32_t* place = p.row_of + static_cast<int64_t>(token) * p.topk;
     if constexpr (COPY == MOE_COPY_FP8)
-      quant_item<T>(p, token, part, p.row_of + token * p.topk);
+      quant_item<T>(p, token, part, place);
     else
-      copy_item<ANY>(p, token, part, p.row_of + token * p.topk);
+      copy_item<ANY>(p, token, part, place);
   }
   clear_tail<COPY>(p, p.offsets[p.experts], static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x,
                    static_cast<int64_t>(gridDim.x) * 256);
@@ -318,69 +333,47 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   extern __shared__ int32_t smem[];
   int32_t* total = smem;                                // [experts], less `before`
   int32_t* before = total + p.experts;                  // [experts]
-  int32_t* rank = before + p.experts;                   // [kRankWarps][experts]
+  int32_t* mine = before + p.experts;                   // [experts], of this chunk
+  int32_t* rank = mine + p.experts;                     // [kRankWarps][experts]
   int32_t* place = rank + kRankWarps * p.experts;       // [chunk slots]
   __shared__ int32_t warp_sum[kSortThreads / 32];
+  static_assert(kSortThreads >= 1024, "a thread per expert");
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t lane = lane_id();
   const int experts = p.experts;
-  const int first = blockIdx.x * p.chunk_tokens * p.topk;
-  const int last = min(p.slots, first + p.chunk_tokens * p.topk);
+  const int64_t chunk_slots = static_cast<int64_t>(p.chunk_tokens) * p.topk;
+  const int first = static_cast<int>(min(static_cast<int64_t>(p.slots), blockIdx.x * chunk_slots));
+  const int last = static_cast<int>(min(static_cast<int64_t>(p.slots), first + chunk_slots));
   const int n = last - first;
   const bool writer = blockIdx.y == 0;  // of the chunk's CTAs, the one that writes the indexes
+  // this CTA's place in its cluster, and the first slot of the cluster's chunks
+  const uint32_t cta = p.clusters ? cluster_ctarank() : 0u;
+  const uint32_t ctas = p.clusters ? kSortCluster : 1u;
+  const int lead = static_cast<int>(
+      min(static_cast<int64_t>(p.slots), (blockIdx.x - cta) * chunk_slots));
 
-  for (int i = tid; i < (2 + kRankWarps) * experts; i += kSortThreads) smem[i] = 0;
+  for (int i = tid; i < (3 + kRankWarps) * experts; i += kSortThreads) smem[i] = 0;
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
 
-  // the slots of every expert: in all chunks, and in the chunks before this
-  if (p.one_pass) {
-    // `before` counts what lies before the chunk, `total` the rest
-    const int lead = first & ~3;
-    for (int i = 4 * tid; i < p.slots; i += 4 * kSortThreads) {
-      int e[4];
-      if (i + 4 <= p.slots) {
-        const int4 v = *reinterpret_cast<const int4*>(p.expert + i);
-        e[0] = v.x, e[1] = v.y, e[2] = v.z, e[3] = v.w;
-      } else {
+  // this CTA's part of all slots, four at a time: `before` counts what lies
+  // before the cluster's chunks, `total` the rest
+  const int64_t quads = (static_cast<int64_t>(p.slots) + 3) / 4;
+  for (int64_t i = quads * cta / ctas + tid; i < quads * (cta + 1) / ctas; i += kSortThreads) {
+    const int64_t at = 4 * i;
+    int e[4];
+    if (at + 4 <= p.slots) {
+      const int4 v = *reinterpret_cast<const int4*>(p.expert + at);
+      e[0] = v.x, e[1] = v.y, e[2] = v.z, e[3] = v.w;
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = i + j < p.slots ? p.expert[i + j] : -1;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (static_cast<uint32_t>(e[j]) < static_cast<uint32_t>(experts))
-          atomicAdd(i < lead || i + j < first ? &before[e[j]] : &total[e[j]], 1);
+      for (int j = 0; j < 4; ++j) e[j] = at + j < p.slots ? p.expert[at + j] : -1;
     }
-  } else {
-    // a warp's 32 lanes take 32 experts; the warps of the same experts share
-    // the chunks, kBatch loads at a time
-    constexpr int kBatch = 16, kWarps = kSortThreads / 32;
-    const int sets = (experts + 31) / 32;
-    const int sharing = sets < kWarps ? kWarps / sets : 1;  // warps per set of experts
-    for (int set = warp % (sets < kWarps ? sets : kWarps); set < sets && warp / sets < sharing;
-         set += kWarps) {
-      const int e = 32 * set + static_cast<int>(lane);
-      int rest = 0, prior = 0;
-      const int part = sets < kWarps ? warp / sets : 0;
-      for (int c0 = part; c0 < p.num_chunks; c0 += sharing * kBatch) {
-        int v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int c = c0 + j * sharing;
-          v[j] = c < p.num_chunks && e < experts
-                     ? p.counts[static_cast<int64_t>(c) * experts + e]
-                     : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          (c0 + j * sharing < static_cast<int>(blockIdx.x) ? prior : rest) += v[j];
-      }
-      if (e < experts) {
-        atomicAdd(&total[e], rest);
-        atomicAdd(&before[e], prior);
-      }
-    }
+    for (int j = 0; j < 4; ++j)
+      if (static_cast<uint32_t>(e[j]) < static_cast<uint32_t>(experts))
+        atomicAdd(at + j < lead ? &before[e[j]] : &total[e[j]], 1);
   }
   // this chunk's slots of every expert, for each ranking warp's run of slots
   const int run = (n + kRankWarps * 32 - 1) / (kRankWarps * 32) * 32;
@@ -392,15 +385,34 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   }
   __syncthreads();
 
-  // total -> the expert's first row (exclusive sum); thread t has the experts
-  // per * t .. per * t + per - 1
-  const int per = (experts + kSortThreads - 1) / kSortThreads;
-  int sum = 0;
-  for (int j = 0; j < per; ++j) {
-    const int e = per * tid + j;
-    sum += e < experts ? total[e] + before[e] : 0;
+  // thread t's expert: all its slots, and those before this chunk
+  int all = 0, prior = 0;
+  if (p.clusters) {
+    if (tid < experts) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < kRankWarps; ++w) sum += rank[w * experts + tid];
+      mine[tid] = sum;
+    }
+    __syncwarp();
+    cluster_sync();
+    if (tid < experts) {
+#pragma unroll
+      for (uint32_t c = 0; c < kSortCluster; ++c) {
+        const int b = ld_cluster(mapa_shared(smem_u32(&before[tid]), c));
+        all += b + ld_cluster(mapa_shared(smem_u32(&total[tid]), c));
+        prior += b + (c < cta ? ld_cluster(mapa_shared(smem_u32(&mine[tid]), c)) : 0);
+      }
+    }
+    // (no CTA ends before the others have read its counts: awaited at the end)
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  } else if (tid < experts) {
+    prior = before[tid];
+    all = prior + total[tid];
   }
-  int incl = sum;
+
+  // the experts' first rows (exclusive sum)
+  int incl = all;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -408,26 +420,25 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int at = incl - sum;
+  int at = incl - all;
   int kept = 0;
+#pragma unroll
   for (int w = 0; w < kSortThreads / 32; ++w) {
     at += w < warp ? warp_sum[w] : 0;
     kept += warp_sum[w];
   }
   const bool index_writer = writer && blockIdx.x == 0;
   if (index_writer && tid == 0) p.offsets[experts] = kept;
-  for (int j = 0; j < per; ++j) {
-    const int e = per * tid + j;
-    if (e >= experts) break;
-    if (index_writer) p.offsets[e] = at;
+  if (tid < experts) {
+    if (index_writer) p.offsets[tid] = at;
     // the first row of each ranking warp's slots of this expert
-    int next = at + before[e];
+    int next = at + prior;
+#pragma unroll
     for (int w = 0; w < kRankWarps; ++w) {
-      const int v = rank[w * experts + e];
-      rank[w * experts + e] = next;
+      const int v = rank[w * experts + tid];
+      rank[w * experts + tid] = next;
       next += v;
     }
-    at += total[e] + before[e];
   }
   __syncthreads();
 
@@ -458,6 +469,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
     for (int r = kept + blockIdx.x * kSortThreads + tid; r < p.slots;
          r += gridDim.x * kSortThreads)
       p.slot_of[r] = -1;
+  if (p.clusters) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   if constexpr (COPY == MOE_SORT_ONLY) return;
   __syncthreads();
 
@@ -468,7 +480,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
        it += static_cast<int64_t>(gridDim.y) * kWarps) {
     const int t = static_cast<int>(it / parts);
     const int part = static_cast<int>(it - static_cast<int64_t>(t) * parts);
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * p.chunk_tokens + t;
+    const int token = static_cast<int>(blockIdx.x) * p.chunk_tokens + t;
     if constexpr (COPY == MOE_COPY_FP8)
       quant_item<T>(p, token, part, place + t * p.topk);
     else
@@ -481,9 +493,9 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
 
 // ---------------------------------------------------------------- back again
 // The slots whose loads are in flight together (KS) are a template parameter: the
-// smallest of 2, 4 and 8 that holds topk, 8 for more. With 8 for 2 slots the
+// smallest of 2, 4, 6 and 8 that holds topk, 8 for more. With 8 for 2 slots the
 // registers for the others cost half of the bandwidth (116 against 65 us, 16384
-// tokens of 4096).
+// tokens of 4096), with 8 for 6 a tenth (42 against 38 us, 5003 of 2047).
 
 // out[t] = sum_s w[t][s] rows[row_of[t][s]] (WEIGHTED) or the plain sum.
 // Aligned: a thread has one word of a token's row. ANY: a warp has 31 of them;
@@ -493,28 +505,33 @@ template <typename T, bool ANY, bool WEIGHTED, int KS>
 __global__ void __launch_bounds__(256, 3) moe_gather_kernel(const GatherParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t H = p.hidden, nv = words_of_row<ANY>(H);
+  const int H = p.hidden, nv = words_of_row<ANY>(H);
   const int64_t total = 2 * static_cast<int64_t>(p.slots) * H;
   const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
-  const int64_t per = ANY ? (nv + 30) / 31 * 32 : nv;  // threads of a token
-  const int64_t items = p.tokens * per;
+  const int per = ANY ? (nv + 30) / 31 * 32 : nv;  // threads of a token
+  const int64_t items = static_cast<int64_t>(p.tokens) * per;
   // (ANY: per and the stride are multiples of 32, a warp stays together)
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items;
        it += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t t = it / per;
+    const int t = static_cast<int>(it / per);
     const RowWords<ANY> r(H, t);
-    const int64_t i = it - t * per;
-    const int64_t col = r.column(ANY ? i / 32 * 31 + (i & 31) : i);
+    const int i = static_cast<int>(it - static_cast<int64_t>(t) * per);
+    const int col = r.column(ANY ? i / 32 * 31 + (i & 31) : i);
+    const int32_t* row_of = p.row_of + static_cast<int64_t>(t) * p.topk;
     float acc[8] = {};
     for (int s0 = 0; s0 < p.topk; s0 += KS) {
       uint4 w[KS];
       float weight[KS];
       int row[KS];
+      bool inside = true;
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        row[j] = s0 + j < p.topk ? p.row_of[t * p.topk + s0 + j] : -1;
+        row[j] = s0 + j < p.topk ? row_of[s0 + j] : -1;
         if (row[j] >= p.slots) row[j] = -1;
-        weight[j] = WEIGHTED && row[j] >= 0 ? p.weight[t * p.topk + s0 + j] : 1.0f;
+        weight[j] = WEIGHTED && row[j] >= 0
+                        ? p.weight[static_cast<int64_t>(t) * p.topk + s0 + j]
+                        : 1.0f;
+        if (ANY) inside = inside && (row[j] < 0 || row_inside(row[j], p.slots, H));
       }
       if constexpr (!ANY) {
 #pragma unroll
@@ -522,23 +539,14 @@ __global__ void __launch_bounds__(256, 3) moe_gather_kernel(const GatherParams p
           if (row[j] >= 0) w[j] = load_words(p.rows, row[j], H, col);
       } else {
         // (a lane up to one word past the row still loads for the one before it)
-        bool inside = true;
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-          const int64_t at = 2 * (row[j] * H + col) & ~int64_t(15);
-          inside = inside && (row[j] < 0 || col >= H + 8 || (at >= 0 && at + 16 <= total));
-        }
-        if (inside) {
-#pragma unroll
-          for (int j = 0; j < KS; ++j)
-            if (row[j] >= 0 && col < H + 8)
-              w[j] = __ldcs(reinterpret_cast<const uint4*>(
-                  rows + (2 * (row[j] * H + col) & ~int64_t(15))));
-        } else {
-#pragma unroll
-          for (int j = 0; j < KS; ++j)
-            if (row[j] >= 0 && col < H + 8)
-              w[j] = word_at(rows, 2 * (row[j] * H + col) & ~int64_t(15), total);
+          if (row[j] < 0 || col >= H + 8) continue;
+          const int64_t at = 2 * (static_cast<int64_t>(row[j]) * H + col) & ~int64_t(15);
+          if (inside)
+            w[j] = __ldcs(reinterpret_cast<const uint4*>(rows + at));
+          else
+            w[j] = word_at(rows, at, total);
         }
         __syncwarp();
 #pragma unroll
@@ -548,7 +556,8 @@ __global__ void __launch_bounds__(256, 3) moe_gather_kernel(const GatherParams p
                                         __shfl_down_sync(0xFFFFFFFFu, w[j].y, 1),
                                         __shfl_down_sync(0xFFFFFFFFu, w[j].z, 1),
                                         __shfl_down_sync(0xFFFFFFFFu, w[j].w, 1));
-          w[j] = shift_out(w[j], next, static_cast<uint32_t>(2 * (row[j] * H + col)) & 15u);
+          w[j] = shift_out(w[j], next,
+                           2 * (static_cast<uint32_t>(row[j]) * H + static_cast<uint32_t>(col)) & 15u);
         }
       }
 #pragma unroll
@@ -574,23 +583,25 @@ __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const Ga
   __shared__ float part[64][kGradThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t H = p.hidden, nv = words_of_row<ANY>(H);
-  const int64_t t = blockIdx.x;
+  const int H = p.hidden, nv = words_of_row<ANY>(H);
+  const int t = static_cast<int>(blockIdx.x);
+  const int64_t slot0 = static_cast<int64_t>(t) * p.topk;
   const int warp = threadIdx.x >> 5;
   const int64_t total = 2 * static_cast<int64_t>(p.tokens) * H;
   const int64_t total_rows = 2 * static_cast<int64_t>(p.slots) * H;
   const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
   const uint8_t* d_out = static_cast<const uint8_t*>(p.d_out);
+  const bool t_inside = ANY && row_inside(t, p.tokens, H);
   for (int s0 = 0; s0 < p.topk; s0 += KS) {
     float dot[KS] = {}, w[KS];
     int row[KS];
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
-      row[j] = s0 + j < p.topk ? p.row_of[t * p.topk + s0 + j] : -1;
+      row[j] = s0 + j < p.topk ? p.row_of[slot0 + s0 + j] : -1;
       if (row[j] >= p.slots) row[j] = -1;
-      w[j] = row[j] >= 0 ? p.weight[t * p.topk + s0 + j] : 0.0f;
+      w[j] = row[j] >= 0 ? p.weight[slot0 + s0 + j] : 0.0f;
     }
-    for (int64_t v = threadIdx.x; v < nv; v += kGradThreads) {
+    for (int v = threadIdx.x; v < nv; v += kGradThreads) {
       if constexpr (!ANY) {
         uint4 x[KS];
         float d[8];
@@ -619,11 +630,20 @@ __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const Ga
         for (int j = 0; j < KS; ++j) {
           if (row[j] < 0) continue;
           const RowWords<true> r(H, row[j]);
-          const int64_t col = r.column(v);
+          const int col = r.column(v);
           if (col >= H) continue;
           float d[8], f[8], o[8];
-          unpack8<T>(bytes_at(d_out, 2 * (t * H + col), total), d);
-          unpack8<T>(word_at(rows, 2 * (r.start + col), total_rows), f);
+          const int64_t at = 2 * (static_cast<int64_t>(t) * H + col);
+          if (t_inside && row_inside(row[j], p.slots, H)) {
+            const uint32_t shift = static_cast<uint32_t>(at) & 15u;
+            const uint4* src = reinterpret_cast<const uint4*>(d_out + at - shift);
+            const uint4 x = __ldcs(reinterpret_cast<const uint4*>(rows + 2 * (r.start + col)));
+            unpack8<T>(shift_out(__ldg(src), __ldg(src + 1), shift), d);
+            unpack8<T>(x, f);
+          } else {
+            unpack8<T>(bytes_at(d_out, at, total), d);
+            unpack8<T>(word_at(rows, 2 * (r.start + col), total_rows), f);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const bool in = col + i >= 0 && col + i < H;  // else a neighbour's element
@@ -646,7 +666,7 @@ __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const Ga
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kGradThreads / 32; ++i) dot += part[s][i];
-    p.d_weight[t * p.topk + s] = dot;
+    p.d_weight[slot0 + s] = dot;
   }
   // rows without a slot
   MoeParams tail = {};
@@ -751,9 +771,11 @@ cudaError_t dispatch_t(const MoeParams& p, int copy, cudaStream_t stream, int pd
   const bool any = p.hidden % 8 != 0;
   // few slots: the sort and the copies in one kernel
   const int fused = p.fused ? copy : MOE_SORT_ONLY;
-  const dim3 grid(p.num_chunks, fused == MOE_SORT_ONLY ? 1 : p.segments, 1);
+  const unsigned cluster = p.clusters ? kSortCluster : 1;
+  const dim3 grid((p.num_chunks + cluster - 1) / cluster * cluster,
+                  fused == MOE_SORT_ONLY ? 1 : p.segments, 1);
   const size_t smem =
-      ((2 + kRankWarps) * static_cast<size_t>(p.experts) + p.chunk_tokens * p.topk) * 4;
+      ((3 + kRankWarps) * static_cast<size_t>(p.experts) + p.chunk_tokens * p.topk) * 4;
   auto sort = [&](auto kernel) -> cudaError_t {
     if (smem > 48 * 1024) {
       const cudaError_t e =
@@ -761,7 +783,7 @@ cudaError_t dispatch_t(const MoeParams& p, int copy, cudaStream_t stream, int pd
                                static_cast<int>(smem));
       if (e != cudaSuccess) return e;
     }
-    return launch(kernel, grid, kSortThreads, smem, stream, pdl, p);
+    return launch_clusters(kernel, grid, cluster, kSortThreads, smem, stream, pdl, p);
   };
   const cudaError_t e =
       fused == MOE_SORT_ONLY  ? sort(moe_dispatch_kernel<T, MOE_SORT_ONLY, false>)
@@ -786,6 +808,7 @@ template <typename F>
 cudaError_t for_slots(int topk, F f) {
   if (topk <= 2) return f(std::integral_constant<int, 2>());
   if (topk <= 4) return f(std::integral_constant<int, 4>());
+  if (topk <= 6) return f(std::integral_constant<int, 6>());
   return f(std::integral_constant<int, 8>());
 }
 
@@ -793,7 +816,8 @@ template <typename T>
 cudaError_t gather_t(const GatherParams& p, int sms, cudaStream_t stream, int pdl) {
   const bool any = p.hidden % 8 != 0;
   const int64_t items =
-      p.tokens * (any ? ((p.hidden + 14) / 8 + 30) / 31 * 32 : p.hidden / 8);
+      static_cast<int64_t>(p.tokens) *
+      (any ? ((p.hidden + 14) / 8 + 30) / 31 * 32 : p.hidden / 8);
   const int64_t want = (items + 255) / 256, most = static_cast<int64_t>(sms) * 64;
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
   return for_slots(p.topk, [&](auto ks) {
@@ -822,11 +846,6 @@ cudaError_t grad_t(const GatherParams& p, cudaStream_t stream, int pdl) {
 }  // namespace
 
 int moe_max_chunk_slots() { return kMaxChunkSlots; }
-
-cudaError_t launch_moe_count(const MoeParams& p, cudaStream_t stream, int pdl) {
-  return launch(moe_count_kernel, dim3(p.num_chunks), kSortThreads,
-                static_cast<size_t>(p.experts) * 4, stream, pdl, p);
-}
 
 cudaError_t launch_moe_dispatch(const MoeParams& p, int copy, int bf16, cudaStream_t stream,
                                 int pdl) {

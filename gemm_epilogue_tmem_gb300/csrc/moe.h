@@ -8,14 +8,13 @@ namespace gf {
 
 struct MoeParams {
   int32_t tokens, topk, experts;
-  int64_t hidden;
+  int32_t hidden;
   int32_t slots;         // tokens * topk
   int32_t chunk_tokens;  // tokens per CTA of the sort
   int32_t num_chunks;
-  int32_t one_pass;      // 1: every CTA counts all slots; 0: counts from `counts`
+  int32_t clusters;      // 1: clusters of CTAs share the counting; 0: every CTA counts alone
   int32_t fused;         // 1: the sort kernel copies too
   int32_t segments;      // CTAs that share the copies of one chunk (along hidden)
-  int32_t* counts;       // [num_chunks][experts], written by the count kernel
   const int32_t* expert;
   int32_t* offsets;
   int32_t* row_of;
@@ -29,13 +28,12 @@ enum MoeCopy : int { MOE_SORT_ONLY = 0, MOE_COPY = 1, MOE_COPY_FP8 = 2 };
 
 // most tokens of a chunk: its slots' rows are held in shared memory
 int moe_max_chunk_slots();
-cudaError_t launch_moe_count(const MoeParams& p, cudaStream_t stream, int pdl);
 cudaError_t launch_moe_dispatch(const MoeParams& p, int copy, int bf16, cudaStream_t stream,
                                 int pdl);
 
 struct GatherParams {
   int32_t tokens, topk;
-  int64_t hidden;
+  int32_t hidden;
   int32_t slots;
   const int32_t* offsets;  // gradient: its entry `experts` bounds the rows with a slot
   int32_t experts;

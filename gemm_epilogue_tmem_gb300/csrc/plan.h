@@ -68,8 +68,7 @@ struct gf_plan {
   int64_t topk, experts;
   int chunk_tokens;      // tokens per CTA of the sort
   int num_chunks;
-  int one_pass;          // every CTA counts all slots itself: no count kernel
-  int fused;             // the sort kernel copies the rows too
-  void* d_work;          // the sort's counts per chunk and expert; fp8 partial sums
+  int fused;             // few slots: the sort kernel copies the rows too
+  void* d_work;          // e4m3 products: counters and partial sums of split tiles
   size_t work_bytes;
 };

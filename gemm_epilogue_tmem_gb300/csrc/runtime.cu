@@ -721,7 +721,7 @@ gf_status runtime_device(int* dev, int* sms) {
   return major == 10 && minor == 3 ? GF_OK : GF_ERR_UNSUPPORTED;
 }
 
-gf_plan* runtime_new_plan(int epi, gf_dtype dtype, size_t work_bytes) {
+gf_plan* runtime_new_plan(int epi, gf_dtype dtype) {
   g_last = GF_OK;
   int dev = 0, sms = 0;
   const gf_status st = runtime_device(&dev, &sms);
@@ -751,20 +751,16 @@ gf_plan* runtime_new_plan(int epi, gf_dtype dtype, size_t work_bytes) {
     if (us >= 1000 && us <= 600000000) p->wait_limit_ns = static_cast<uint64_t>(us) * 1000ull;
   }
   gf_status got = GF_OK;
-  if (cudaMalloc(&p->d_status, 256) != cudaSuccess ||
-      (work_bytes > 0 && cudaMalloc(&p->d_work, work_bytes) != cudaSuccess)) {
+  if (cudaMalloc(&p->d_status, 256) != cudaSuccess)
     got = GF_ERR_OUT_OF_MEMORY;
-  } else if (cudaMemset(p->d_status, 0, 256) != cudaSuccess ||
-             (work_bytes > 0 && cudaMemset(p->d_work, 0, work_bytes) != cudaSuccess)) {
+  else if (cudaMemset(p->d_status, 0, 256) != cudaSuccess)
     got = GF_ERR_CUDA;
-  }
   if (got != GF_OK) {
     cudaGetLastError();
     gf_plan_free(p);
     fail(got);
     return nullptr;
   }
-  p->work_bytes = work_bytes;
   return p;
 }
 
@@ -988,7 +984,7 @@ GF_API gf_status gf_plan_describe(const gf_plan* p, int32_t* tile_m, int32_t* ti
 GF_API gf_status gf_plan_launches(const gf_plan* p, int32_t* launches) {
   if (!p || !launches) return fail(GF_ERR_INVALID_VALUE);
   if (p->epi == gf::EPI_MOE) {
-    *launches = (p->one_pass ? 0 : 1) + 1 + (p->fused ? 0 : 1);  // count, sort, copies
+    *launches = p->fused ? 1 : 2;  // sort, copies
     return GF_OK;
   }
   const bool finalize = has_bgrad(p->epi) && p->bgrad_mode != GF_BGRAD_ATOMIC;

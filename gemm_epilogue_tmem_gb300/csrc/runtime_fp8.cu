@@ -128,7 +128,7 @@ GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t grou
     runtime_fail(GF_ERR_UNSUPPORTED);
     return nullptr;
   }
-  gf_plan* p = gf::runtime_new_plan(dual ? gf::EPI_FP8_SWIGLU_QUANT : gf::EPI_FP8, dtype, 0);
+  gf_plan* p = gf::runtime_new_plan(dual ? gf::EPI_FP8_SWIGLU_QUANT : gf::EPI_FP8, dtype);
   if (!p) return nullptr;
   p->m = m;
   p->n = n;

@@ -28,10 +28,9 @@ bool runtime_encode_2d_u8(CUtensorMap* map, const void* ptr, uint64_t inner, uin
                           uint32_t box_inner, uint32_t box_outer);
 
 // A plan of an operator that is not a 16-bit GEMM (epi >= EPI_FP8) on the
-// calling thread's device, checked to be one the kernels run on: defaults, the
-// status word and `work_bytes` of zeroed workspace. nullptr with the reason in
-// gf_last_error.
-gf_plan* runtime_new_plan(int epi, gf_dtype dtype, size_t work_bytes);
+// calling thread's device, checked to be one the kernels run on: defaults and
+// the status word. nullptr with the reason in gf_last_error.
+gf_plan* runtime_new_plan(int epi, gf_dtype dtype);
 
 // GF_OPT_KERNEL of an e4m3 product's plan.
 gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value);

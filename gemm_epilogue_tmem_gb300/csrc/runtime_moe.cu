@@ -14,6 +14,7 @@ namespace {
 using gf::runtime_fail;
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxHidden = int64_t(1) << 24;  // columns are int32 in the kernels
 
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -22,10 +23,9 @@ bool given_scale(const void* p) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 }
 
-// Slots up to which every CTA counts all of them itself, without the count
-// kernel; and up to which the sort kernel copies the rows too, without a copy
-// kernel.
-constexpr int64_t kOnePassSlots = 32768;
+// Slots up to which every CTA of the sort counts all of them alone and copies
+// its tokens' rows too; above, clusters of CTAs share the counting, and the
+// copies have a kernel of their own (whose CTAs the hardware balances).
 constexpr int64_t kFusedSlots = 4096;
 
 bool is_moe(const gf_plan* p) { return p != nullptr && p->epi == gf::EPI_MOE; }
@@ -45,13 +45,12 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   prm.tokens = static_cast<int32_t>(p->m);
   prm.topk = static_cast<int32_t>(p->topk);
   prm.experts = static_cast<int32_t>(p->experts);
-  prm.hidden = p->k;
+  prm.hidden = static_cast<int32_t>(p->k);
   prm.slots = static_cast<int32_t>(p->m * p->topk);
   prm.chunk_tokens = p->chunk_tokens;
   prm.num_chunks = p->num_chunks;
-  prm.one_pass = p->one_pass;
+  prm.clusters = p->fused ? 0 : 1;
   prm.fused = p->fused;
-  prm.counts = static_cast<int32_t*>(p->d_work);
   prm.expert = expert;
   prm.offsets = offsets;
   prm.row_of = row_of;
@@ -68,8 +67,6 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   seg = seg > room ? room : seg;
   prm.segments = static_cast<int32_t>(seg < 1 ? 1 : seg);
   const int bf16 = p->dtype == GF_BF16 ? 1 : 0;
-  if (!p->one_pass && gf::launch_moe_count(prm, st, p->pdl) != cudaSuccess)
-    return runtime_fail(GF_ERR_CUDA);
   if (gf::launch_moe_dispatch(prm, copy, bf16, st, p->pdl) != cudaSuccess)
     return runtime_fail(GF_ERR_CUDA);
   return GF_OK;
@@ -80,7 +77,7 @@ gf::GatherParams gather_params(const gf_plan* p, const int32_t* row_of, const fl
   gf::GatherParams g = {};
   g.tokens = static_cast<int32_t>(p->m);
   g.topk = static_cast<int32_t>(p->topk);
-  g.hidden = p->k;
+  g.hidden = static_cast<int32_t>(p->k);
   g.slots = static_cast<int32_t>(p->m * p->topk);
   g.experts = static_cast<int32_t>(p->experts);
   g.row_of = row_of;
@@ -97,7 +94,7 @@ extern "C" {
 GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
                             gf_dtype dtype) {
   if (tokens < 0 || tokens > kMaxDim || topk < 1 || topk > 64 || experts < 1 || experts > 1024 ||
-      hidden < 1 || hidden > kMaxDim || tokens * topk > kMaxDim ||
+      hidden < 1 || hidden > kMaxHidden || tokens * topk > kMaxDim ||
       (dtype != GF_F16 && dtype != GF_BF16)) {
     runtime_fail(GF_ERR_INVALID_VALUE);
     return nullptr;
@@ -113,9 +110,7 @@ GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64
   const int64_t most = gf::moe_max_chunk_slots() / topk;
   chunk = chunk > most ? most : chunk < 1 ? 1 : chunk;
   const int64_t chunks = tokens == 0 ? 1 : (tokens + chunk - 1) / chunk;
-  const bool one_pass = tokens * topk <= kOnePassSlots;
-  gf_plan* p = gf::runtime_new_plan(gf::EPI_MOE, dtype,
-                                    one_pass ? 0 : static_cast<size_t>(chunks * experts) * 4);
+  gf_plan* p = gf::runtime_new_plan(gf::EPI_MOE, dtype);
   if (!p) return nullptr;
   p->m = tokens;
   p->k = hidden;
@@ -124,7 +119,6 @@ GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64
   p->experts = experts;
   p->chunk_tokens = static_cast<int>(chunk);
   p->num_chunks = static_cast<int>(chunks);
-  p->one_pass = one_pass ? 1 : 0;
   p->fused = tokens * topk <= kFusedSlots ? 1 : 0;
   p->grid = static_cast<int>(chunks);
   return p;

@@ -231,8 +231,8 @@ GF_API gf_status gf_dswiglu_execute(const gf_plan* plan, const void* dout, const
  * Sums run in fp32 in slot order, so results do not vary from run to run. A
  * token whose slots are all dropped gets zeros.
  *
- * tokens >= 0, 1 <= topk <= 64, 1 <= experts <= 1024, 1 <= hidden,
- * tokens * topk < 2^31. The plan owns the sort's workspace. GF_OPT_PDL is its
+ * tokens >= 0, 1 <= topk <= 64, 1 <= experts <= 1024, 1 <= hidden <= 2^24,
+ * tokens * topk < 2^31. The calls need no workspace. GF_OPT_PDL is the plan's
  * one option; gf_plan_status, gf_plan_describe (tile_m: tokens per CTA of the
  * sort), gf_plan_launches (of gf_moe_dispatch_execute) and gf_plan_free take
  * it as any other plan.
