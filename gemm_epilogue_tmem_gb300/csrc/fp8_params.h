@@ -10,7 +10,7 @@ namespace gf {
 constexpr int kFp8MaxGroups = 1024;
 
 struct Fp8Params {
-  int32_t M, N, K;          // rows of all groups, columns of one B, inner length
+  int32_t M, N;             // rows of all groups, columns of one B
   int32_t groups;
   int32_t num_k_blocks;     // blocks of 128
   int32_t num_n_blocks;     // scale blocks of 128 columns

@@ -121,10 +121,10 @@ GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t grou
     return nullptr;
   }
   const bool dual = epilog == GF_FP8_EPILOG_SWIGLU_QUANT;
-  // rows of B over all groups and the tiles of 16 rows x 128 columns are int32
-  // in the kernels
-  if (k % 16 != 0 || n % (dual ? 16 : 8) != 0 || groups * n > kMaxDim ||
-      (m / 16 + groups + 1) * ((n + 127) / 128) > kMaxDim) {
+  // the kernels count rows, rows of B over all groups and tiles (the smallest
+  // are 16 rows x 128 columns) in int32, a tile or a round past the last one too
+  if (k % 16 != 0 || n % (dual ? 16 : 8) != 0 || m > kMaxDim - 512 || groups * n > kMaxDim - 512 ||
+      (m / 16 + groups + 1) * ((n + 127) / 128) > (int64_t(1) << 30)) {
     runtime_fail(GF_ERR_UNSUPPORTED);
     return nullptr;
   }
@@ -180,7 +180,6 @@ GF_API gf_status gf_fp8_matmul_execute(const gf_plan* p, const void* A, const fl
   gf::Fp8Params prm = {};
   prm.M = static_cast<int32_t>(p->m);
   prm.N = static_cast<int32_t>(p->n);
-  prm.K = static_cast<int32_t>(p->k);
   prm.groups = static_cast<int32_t>(p->groups);
   prm.num_k_blocks = static_cast<int32_t>((p->k + 127) / 128);
   prm.num_n_blocks = static_cast<int32_t>((p->n + 127) / 128);

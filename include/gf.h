@@ -324,7 +324,8 @@ typedef enum gf_fp8_epilog {
  *
  * m rows, n columns, k; groups >= 1. 0 <= m, n, k < 2^31, 1 <= groups <= 1024.
  * k % 16 == 0 (16-byte rows for the tensor maps), n % 8 == 0, or n % 16 == 0
- * for SWIGLU_QUANT, else GF_ERR_UNSUPPORTED. dtype: the element type of out
+ * for SWIGLU_QUANT, and m, groups * n up to 2^31 - 513, at most 2^30 tiles of 16 x
+ * 128, else GF_ERR_UNSUPPORTED. dtype: the element type of out
  * (NONE). Options: GF_OPT_KERNEL (0 the plan's choice by the average number of
  * rows a group and the number of tiles; 1 and 2 the kernel for few rows with
  * tiles of 16 and 64 rows; 3 the single-CTA kernel with tiles of 128; 4 the

@@ -293,6 +293,64 @@ def test_nan_rows_stay_alone(kernel):
     plan.free()
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("m,n,k,groups", [(1, 16, 16, 1), (17, 144, 272, 3), (300, 272, 144, 4), (513, 400, 128, 2)])
+def test_no_stray_stores(m, n, k, groups, kernel):
+    """Outputs and scales between canaries, at sizes that end inside every tile."""
+    kb, nb = -(-k // 128), -(-n // 128)
+    a, b = operand((m, k), 91), operand((groups, n, k), 92)
+    sa, sb = scales((m, kb), 93), scales((groups, nb, kb), 94)
+    off = torch.from_numpy(split(m, groups, 95).astype(np.int32)).cuda()
+
+    def between(count, dtype):
+        flat = torch.full((8192 + count * torch.empty(0, dtype=dtype).element_size(),), 0x5A, dtype=torch.uint8, device="cuda")
+        return flat, flat[4096:-4096].view(dtype)
+
+    flats = []
+    for quant in (False, True):
+        epilog = gf.GF_FP8_EPILOG_SWIGLU_QUANT if quant else gf.GF_FP8_EPILOG_NONE
+        plan = gf.gf_fp8_matmul_plan(m, n, k, groups, gf.GF_F16, epilog)
+        gf.gf_plan_set_option(plan, gf.GF_OPT_KERNEL, kernel)
+        flat, out = between(m * n, torch.uint8 if quant else torch.half)
+        flat_s, os = between(m * nb, torch.float32)
+        gf.gf_fp8_matmul_execute(plan, a, sa, b, sb, b if quant else None, sb if quant else None, off, out,
+                                 os if quant else None)
+        assert gf.gf_plan_status(plan) == gf.GF_OK
+        flats += [flat, flat_s]
+        plan.free()
+    assert all(bool((f[:4096] == 0x5A).all()) and bool((f[-4096:] == 0x5A).all()) for f in flats)
+
+
+@pytest.mark.parametrize("m,n,k,kernel", [
+    (140000, 136, 16400, 3), (140000, 136, 16400, 4), (300000, 16384, 16, 3), (300000, 16384, 16, 4), (16, 16384, 140016, 1)])
+def test_past_32_bit_offsets(m, n, k, kernel):
+    """Operands and outputs of more than 2^31 bytes and elements: the first and
+    the last rows, whose operands are set, come out right, the others are zero."""
+    kb, nb = -(-k // 128), -(-n // 128)
+    a = torch.zeros(m, k, dtype=torch.float8_e4m3fn, device="cuda")
+    b = torch.zeros(1, n, k, dtype=torch.float8_e4m3fn, device="cuda")
+    rows = [0, 1, m // 2, m - 2, m - 1] if m > 16 else list(range(m))
+    cols = [0, n // 2, n - 1]
+    a.view(torch.uint8)[rows] = operand((len(rows), k), 81).view(torch.uint8)
+    b.view(torch.uint8)[0, cols] = operand((len(cols), k), 82).view(torch.uint8)
+    sa, sb = torch.ones(m, kb, device="cuda"), scales((1, nb, kb), 83)
+    sa[rows] = scales((len(rows), kb), 84)
+    plan = gf.gf_fp8_matmul_plan(m, n, k, 1, gf.GF_BF16)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_KERNEL, kernel)
+    out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    gf.gf_fp8_matmul_execute(plan, a, sa, b, sb, out=out)
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    av = values(a[rows], sa[rows], 1)
+    bv = torch.stack([values(b[0, c:c + 1], sb[0, c // 128:c // 128 + 1], 1)[0] for c in cols])
+    want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
+    bound = (k + 4) * 2.0 ** -23 * mag
+    bound = bound + 2.0 ** -8 * (want.abs() + bound)
+    assert bool(((out[rows][:, cols].double() - want).abs() <= bound).all())
+    out[torch.tensor(rows)[:, None].cuda(), torch.tensor(cols).cuda()] = 0
+    assert int(torch.count_nonzero(out)) == 0
+    plan.free()
+
+
 def test_empty():
     for m, n, k in ((0, 128, 128), (4, 0, 128)):
         plan = gf.gf_fp8_matmul_plan(m, n, k, 1, gf.GF_F16)

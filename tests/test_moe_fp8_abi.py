@@ -21,6 +21,7 @@ def L():
     ((8, 2, 0, 64, 0), gf.GF_ERR_INVALID_VALUE),
     ((8, 2, 1025, 64, 0), gf.GF_ERR_INVALID_VALUE),
     ((8, 2, 4, 0, 0), gf.GF_ERR_INVALID_VALUE),
+    ((8, 2, 4, (1 << 24) + 1, 0), gf.GF_ERR_INVALID_VALUE),
     ((8, 2, 4, 64, 2), gf.GF_ERR_INVALID_VALUE),
     ((1 << 30, 2, 4, 64, 0), gf.GF_ERR_INVALID_VALUE),   # tokens * topk >= 2^31
 ])
@@ -40,6 +41,8 @@ def test_moe_plan_rejects_before_device(L, args, status):
     ((8, 24, 128, 1, 0, 1), gf.GF_ERR_UNSUPPORTED),      # n % 16 for the e4m3 output
     ((8, 1 << 22, 128, 1024, 0, 0), gf.GF_ERR_UNSUPPORTED),  # groups * n
     ((1 << 31, 128, 128, 1, 0, 0), gf.GF_ERR_INVALID_VALUE),
+    (((1 << 31) - 512, 128, 16, 1, 0, 0), gf.GF_ERR_UNSUPPORTED),     # rows past the last tile
+    ((1 << 24, 1 << 20, 16, 1, 0, 0), gf.GF_ERR_UNSUPPORTED),         # tiles
 ])
 def test_fp8_plan_rejects_before_device(L, args, status):
     assert not L.gf_fp8_matmul_plan(*args)

@@ -278,6 +278,50 @@ def test_rows_past_32_bit_offsets():
     plan.free()
 
 
+class Guarded:
+    """n elements between two runs of canaries, 16-byte aligned."""
+
+    def __init__(self, *shape, dtype):
+        n = int(np.prod(shape))
+        self.flat = torch.full((4096 + n + 4096,), 0x5A, dtype=torch.int32, device="cuda").view(torch.uint8)
+        size = torch.empty(0, dtype=dtype).element_size()
+        self.lo, self.hi = 4096, 4096 + n * size
+        self.flat.fill_(0x5A)
+        self.t = self.flat[self.lo:self.hi].view(dtype).view(*shape)
+
+    def intact(self):
+        return bool((self.flat[:self.lo] == 0x5A).all()) and bool((self.flat[self.hi:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("tokens,topk,experts,hidden", [
+    (1, 3, 5, 1), (1, 1, 1, 7), (5, 2, 3, 15), (9, 5, 7, 33), (40, 8, 20, 2047), (700, 7, 9, 250), (33, 3, 40, 264), (1500, 3, 5, 13)])
+@pytest.mark.parametrize("drop", [0.0, 0.4])
+def test_no_stray_stores(tokens, topk, experts, hidden, drop):
+    """Every output of every call between canaries, at widths that end inside a word."""
+    slots = tokens * topk
+    e = dev(routing(tokens, topk, experts, 21, drop))
+    x = randn(tokens, hidden, seed=22, dtype=torch.float16)
+    w = torch.rand(tokens, topk, device="cuda")
+    f16, i32 = torch.float16, torch.int32
+    o, r, s = Guarded(experts + 1, dtype=i32), Guarded(tokens, topk, dtype=i32), Guarded(slots, dtype=i32)
+    rows, d_rows = Guarded(slots, hidden, dtype=f16), Guarded(slots, hidden, dtype=f16)
+    out, d_x = Guarded(tokens, hidden, dtype=f16), Guarded(tokens, hidden, dtype=f16)
+    d_w = Guarded(tokens, topk, dtype=torch.float32)
+    plan = gf.gf_moe_plan(tokens, topk, experts, hidden, gf.GF_F16)
+    gf.gf_moe_dispatch_execute(plan, e, x, o.t, r.t, s.t, rows.t)
+    gf.gf_moe_combine_execute(plan, r.t, w, rows.t, out.t)
+    gf.gf_moe_combine_grad_execute(plan, o.t, r.t, w, rows.t, x, d_rows.t, d_w.t)
+    gf.gf_moe_dispatch_grad_execute(plan, r.t, d_rows.t, d_x.t)
+    guarded = [o, r, s, rows, d_rows, out, d_x, d_w]
+    if hidden % 16 == 0:
+        q, sc = Guarded(slots, hidden, dtype=torch.uint8), Guarded(slots, -(-hidden // 128), dtype=torch.float32)
+        gf.gf_moe_dispatch_fp8_execute(plan, e, x, o.t, r.t, s.t, q.t, sc.t)
+        guarded += [q, sc]
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    assert all(g.intact() for g in guarded)
+    plan.free()
+
+
 def test_graph_capture():
     tokens, topk, experts, hidden = 700, 8, 32, 256
     plan = gf.gf_moe_plan(tokens, topk, experts, hidden, gf.GF_BF16)
