@@ -106,6 +106,47 @@ __device__ __forceinline__ uint4 shift_out(const uint4& a, const uint4& b, uint3
   }
 }
 
+// The same, of this lane's word and the next lane's: a shuffle for each 4 bytes
+// that the next one gives, one to four. Called by whole warps with one shift.
+__device__ __forceinline__ uint4 shift_in(const uint4& a, uint32_t shift) {
+  const uint32_t r = 8u * (shift & 2u);
+  auto next = [](uint32_t w) { return __shfl_down_sync(0xFFFFFFFFu, w, 1); };
+  switch (shift >> 2) {
+    case 0: {
+      const uint32_t x = next(a.x);
+      return make_uint4(__funnelshift_r(a.x, a.y, r), __funnelshift_r(a.y, a.z, r),
+                        __funnelshift_r(a.z, a.w, r), __funnelshift_r(a.w, x, r));
+    }
+    case 1: {
+      const uint32_t x = next(a.x), y = next(a.y);
+      return make_uint4(__funnelshift_r(a.y, a.z, r), __funnelshift_r(a.z, a.w, r),
+                        __funnelshift_r(a.w, x, r), __funnelshift_r(x, y, r));
+    }
+    case 2: {
+      const uint32_t x = next(a.x), y = next(a.y), z = next(a.z);
+      return make_uint4(__funnelshift_r(a.z, a.w, r), __funnelshift_r(a.w, x, r),
+                        __funnelshift_r(x, y, r), __funnelshift_r(y, z, r));
+    }
+    default: {
+      const uint32_t x = next(a.x), y = next(a.y), z = next(a.z), v = next(a.w);
+      return make_uint4(__funnelshift_r(a.w, x, r), __funnelshift_r(x, y, r),
+                        __funnelshift_r(y, z, r), __funnelshift_r(z, v, r));
+    }
+  }
+}
+
+// acc += w f, both columns in one instruction
+__device__ __forceinline__ void add_scaled(float2& acc, const float2& f, float w) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "mov.b64 c, {%4, %4};\n\t"
+      "fma.rn.f32x2 a, b, c, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "f"(f.x), "f"(f.y), "f"(w));
+}
+
 // The 16 bytes from byte `at` (even) on, out of the two aligned words around
 // them; bytes outside the array are zero and are not read.
 __device__ __forceinline__ uint4 bytes_at(const uint8_t* array, int64_t at, int64_t total) {
@@ -161,23 +202,6 @@ __device__ __forceinline__ void store_words(void* array, const RowWords<ANY>& r,
       if (col + i >= 0 && col + i < r.H)
         dst[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
   }
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = Pair16<T>::unpack(u[i]);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(Pair16<T>::pack(f[0], f[1]), Pair16<T>::pack(f[2], f[3]),
-                    Pair16<T>::pack(f[4], f[5]), Pair16<T>::pack(f[6], f[7]));
 }
 
 // ------------------------------------------------------------------ the copies
@@ -495,177 +519,258 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
 // The slots whose loads are in flight together (KS) are a template parameter: the
 // smallest of 2, 4, 6 and 8 that holds topk, 8 for more. With 8 for 2 slots the
 // registers for the others cost half of the bandwidth (116 against 65 us, 16384
-// tokens of 4096), with 8 for 6 a tenth (42 against 38 us, 5003 of 2047).
+// tokens of 4096), with 8 for 6 a tenth (29.6 against 27.1 us, 5003 of 2047).
 
 // out[t] = sum_s w[t][s] rows[row_of[t][s]] (WEIGHTED) or the plain sum.
-// Aligned: a thread has one word of a token's row. ANY: a warp has 31 of them;
-// its lanes load 32 aligned words of each row, and every lane shifts its word
-// out of its own and the next lane's.
-template <typename T, bool ANY, bool WEIGHTED, int KS>
+template <typename T>
+__device__ __forceinline__ void add_word(float2 (&acc)[4], const uint4& w, float weight) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add_scaled(acc[i], Pair16<T>::unpack(u[i]), weight);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_word(const float2 (&acc)[4]) {
+  return make_uint4(Pair16<T>::pack(acc[0].x, acc[0].y), Pair16<T>::pack(acc[1].x, acc[1].y),
+                    Pair16<T>::pack(acc[2].x, acc[2].y), Pair16<T>::pack(acc[3].x, acc[3].y));
+}
+
+// the rows of slots s0 .. s0 + KS - 1 of token t (below 0: none)
+template <int KS>
+__device__ __forceinline__ void rows_of(const GatherParams& p, int t, int s0, int (&row)[KS]) {
+  const int32_t* row_of = p.row_of + static_cast<int64_t>(t) * p.topk + s0;
+#pragma unroll
+  for (int j = 0; j < KS; ++j) {
+    row[j] = s0 + j < p.topk ? row_of[j] : -1;
+    if (row[j] >= p.slots) row[j] = -1;
+  }
+}
+
+// their weights. KEPT: of the slots with a row only, so that the loads follow
+// the rows' indexes: where the indexes are a thread's own, loads for all slots
+// beside those of the rows cost 2 us of 180; where they are the CTA's, 2 of 30
+// are gained.
+template <bool WEIGHTED, bool KEPT, int KS>
+__device__ __forceinline__ void weights_of(const GatherParams& p, int t, int s0,
+                                           const int (&row)[KS], float (&weight)[KS]) {
+  const float* w = p.weight + static_cast<int64_t>(t) * p.topk + s0;
+#pragma unroll
+  for (int j = 0; j < KS; ++j)
+    weight[j] = WEIGHTED && (KEPT ? row[j] >= 0 : s0 + j < p.topk) ? w[j] : 1.0f;
+}
+
+// Aligned rows: a thread has one word of a token's row.
+template <typename T, bool WEIGHTED, int KS>
 __global__ void __launch_bounds__(256, 3) moe_gather_kernel(const GatherParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int H = p.hidden, nv = words_of_row<ANY>(H);
-  const int64_t total = 2 * static_cast<int64_t>(p.slots) * H;
-  const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
-  const int per = ANY ? (nv + 30) / 31 * 32 : nv;  // threads of a token
-  const int64_t items = static_cast<int64_t>(p.tokens) * per;
-  // (ANY: per and the stride are multiples of 32, a warp stays together)
+  const int H = p.hidden, nv = H / 8;
+  const int64_t items = static_cast<int64_t>(p.tokens) * nv;
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items;
        it += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int t = static_cast<int>(it / per);
-    const RowWords<ANY> r(H, t);
-    const int i = static_cast<int>(it - static_cast<int64_t>(t) * per);
-    const int col = r.column(ANY ? i / 32 * 31 + (i & 31) : i);
-    const int32_t* row_of = p.row_of + static_cast<int64_t>(t) * p.topk;
-    float acc[8] = {};
+    const int t = static_cast<int>(it / nv);
+    const int col = 8 * static_cast<int>(it - static_cast<int64_t>(t) * nv);
+    float2 acc[4] = {};
     for (int s0 = 0; s0 < p.topk; s0 += KS) {
       uint4 w[KS];
       float weight[KS];
       int row[KS];
+      rows_of<KS>(p, t, s0, row);
+      weights_of<WEIGHTED, true, KS>(p, t, s0, row, weight);
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+        if (row[j] >= 0) w[j] = load_words(p.rows, row[j], H, col);
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+        if (row[j] >= 0) add_word<T>(acc, w[j], weight[j]);
+    }
+    store_words<false>(p.out, RowWords<false>(H, t), col, pack_word<T>(acc));
+  }
+}
+
+// Rows of any length: a CTA per token, so that the slots' rows and shifts are
+// the CTA's, and a warp for 31 words at a time: its lanes load 32 aligned words
+// of each row, and every lane shifts its word out of its own and the next
+// lane's. (With the words of all tokens dealt out to the warps in one row the
+// index arithmetic took most of the instructions: gradient of dispatch, 5003
+// tokens, 6 slots, 2047 columns of fp16, 39 against 27 us.) Up to four warps a
+// CTA, as few as the same number of turns needs: 27 us, with up to eight 27.5,
+// with two 31. Seven CTAs' registers (72 a thread): 2000 tokens, 8 slots, 7169
+// columns 47 us, with 80 registers 55.
+constexpr int kAnyWarps = 4;
+
+template <typename T, bool WEIGHTED, int KS>
+__global__ void __launch_bounds__(32 * kAnyWarps, 7)
+    moe_gather_any_kernel(const GatherParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int H = p.hidden, t = static_cast<int>(blockIdx.x);
+  const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
+  const int lane = static_cast<int>(lane_id());
+  const RowWords<true> r(H, t);
+  const int words = (r.lead + H + 7) / 8;
+  for (int v = static_cast<int>(threadIdx.x >> 5) * 31; v < words;
+       v += static_cast<int>(blockDim.x >> 5) * 31) {
+    const int col = r.column(v + lane);
+    float2 acc[4] = {};
+    for (int s0 = 0; s0 < p.topk; s0 += KS) {
+      uint4 w[KS];
+      float weight[KS];
+      int row[KS];
+      rows_of<KS>(p, t, s0, row);
+      weights_of<WEIGHTED, false, KS>(p, t, s0, row, weight);
       bool inside = true;
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        row[j] = s0 + j < p.topk ? row_of[s0 + j] : -1;
-        if (row[j] >= p.slots) row[j] = -1;
-        weight[j] = WEIGHTED && row[j] >= 0
-                        ? p.weight[static_cast<int64_t>(t) * p.topk + s0 + j]
-                        : 1.0f;
-        if (ANY) inside = inside && (row[j] < 0 || row_inside(row[j], p.slots, H));
-      }
-      if constexpr (!ANY) {
+      for (int j = 0; j < KS; ++j)
+        inside = inside && (row[j] < 0 || row_inside(row[j], p.slots, H));
+      // (a lane up to one word past the row still loads for the one before it)
+      if (inside) {
 #pragma unroll
         for (int j = 0; j < KS; ++j)
-          if (row[j] >= 0) w[j] = load_words(p.rows, row[j], H, col);
+          if (row[j] >= 0 && col < H + 8)
+            w[j] = __ldcs(reinterpret_cast<const uint4*>(
+                rows + (2 * (static_cast<int64_t>(row[j]) * H + col) & ~int64_t(15))));
       } else {
-        // (a lane up to one word past the row still loads for the one before it)
+        const int64_t total = 2 * static_cast<int64_t>(p.slots) * H;
 #pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          if (row[j] < 0 || col >= H + 8) continue;
-          const int64_t at = 2 * (static_cast<int64_t>(row[j]) * H + col) & ~int64_t(15);
-          if (inside)
-            w[j] = __ldcs(reinterpret_cast<const uint4*>(rows + at));
-          else
-            w[j] = word_at(rows, at, total);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          if (row[j] < 0) continue;  // the same in all lanes
-          const uint4 next = make_uint4(__shfl_down_sync(0xFFFFFFFFu, w[j].x, 1),
-                                        __shfl_down_sync(0xFFFFFFFFu, w[j].y, 1),
-                                        __shfl_down_sync(0xFFFFFFFFu, w[j].z, 1),
-                                        __shfl_down_sync(0xFFFFFFFFu, w[j].w, 1));
-          w[j] = shift_out(w[j], next,
-                           2 * (static_cast<uint32_t>(row[j]) * H + static_cast<uint32_t>(col)) & 15u);
-        }
+        for (int j = 0; j < KS; ++j)
+          if (row[j] >= 0 && col < H + 8)
+            w[j] = word_at(rows, 2 * (static_cast<int64_t>(row[j]) * H + col) & ~int64_t(15), total);
       }
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        if (row[j] < 0) continue;
-        float f[8];
-        unpack8<T>(w[j], f);
-#pragma unroll
-        for (int i8 = 0; i8 < 8; ++i8) acc[i8] = fmaf(weight[j], f[i8], acc[i8]);
-      }
+      for (int j = 0; j < KS; ++j)
+        if (row[j] >= 0)  // the same in the whole CTA, and so the shift: column() is -lead mod 8
+          add_word<T>(acc,
+                      shift_in(w[j], 2 * (static_cast<uint32_t>(row[j]) * H -
+                                          static_cast<uint32_t>(r.lead)) & 15u),
+                      weight[j]);
     }
-    if (!ANY || (lane_id() < 31 && col < H)) store_words<ANY>(p.out, r, col, pack8<T>(acc));
+    if (lane < 31 && col < H) store_words<true>(p.out, r, col, pack_word<T>(acc));
   }
 }
 
 // d_rows[row] = w d_out[t], d_weight[t][s] = <d_out[t], rows[row]>: a CTA per
 // token. A thread adds its words' products per slot, the warps' sums are added
 // in a fixed order.
-constexpr int kGradThreads = 128;
+constexpr int kGradWarps = 4;  // most of a CTA
+// The words of all slots at once are in flight, and as many CTAs as the
+// registers for them allow: 5003 tokens, 6 slots, 2047 columns 58 us, with one
+// word in flight 70, with the compiler's own number of registers 66; 16384
+// tokens, 8 slots, 4096 columns 337, 340 without the bound.
+constexpr int grad_ctas(int slots) { return slots == 8 ? 5 : slots == 6 ? 7 : slots == 4 ? 9 : 12; }
+
+// one word of a slot: dot += <d, x>, and w d
+template <typename T>
+__device__ __forceinline__ uint4 grad_word(float2& dot, const uint4& d, const uint4& x, float w) {
+  const uint32_t du[4] = {d.x, d.y, d.z, d.w}, xu[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Pair16<T>::unpack(du[i]);
+    const float2 g = Pair16<T>::unpack(xu[i]);
+    dot.x = fmaf(f.x, g.x, dot.x);
+    dot.y = fmaf(f.y, g.y, dot.y);
+    o[i] = Pair16<T>::pack(f.x * w, f.y * w);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// the word's elements of columns outside [0, H) (a neighbour's) set to zero
+__device__ __forceinline__ uint4 inside_row(const uint4& x, int col, int H) {
+  uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = col + 2 * i;
+    u[i] &= (c >= 0 && c < H ? 0xFFFFu : 0u) | (c + 1 >= 0 && c + 1 < H ? 0xFFFF0000u : 0u);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
 
 template <typename T, bool ANY, int KS>
-__global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const GatherParams p) {
-  __shared__ float part[64][kGradThreads / 32];
+__global__ void __launch_bounds__(32 * kGradWarps, grad_ctas(KS))
+    moe_combine_grad_kernel(const GatherParams p) {
+  __shared__ float part[64][kGradWarps];
   grid_dep_wait();
   grid_dep_launch();
   const int H = p.hidden, nv = words_of_row<ANY>(H);
   const int t = static_cast<int>(blockIdx.x);
   const int64_t slot0 = static_cast<int64_t>(t) * p.topk;
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t total = 2 * static_cast<int64_t>(p.tokens) * H;
   const int64_t total_rows = 2 * static_cast<int64_t>(p.slots) * H;
   const uint8_t* rows = static_cast<const uint8_t*>(p.rows);
   const uint8_t* d_out = static_cast<const uint8_t*>(p.d_out);
-  const bool t_inside = ANY && row_inside(t, p.tokens, H);
+  const int64_t d_start = static_cast<int64_t>(t) * H;
   for (int s0 = 0; s0 < p.topk; s0 += KS) {
-    float dot[KS] = {}, w[KS];
+    float2 dot[KS] = {};
+    float w[KS];
     int row[KS];
+    bool inside = ANY && row_inside(t, p.tokens, H);
+    rows_of<KS>(p, t, s0, row);
+    weights_of<true, false, KS>(p, t, s0, row, w);
 #pragma unroll
-    for (int j = 0; j < KS; ++j) {
-      row[j] = s0 + j < p.topk ? p.row_of[slot0 + s0 + j] : -1;
-      if (row[j] >= p.slots) row[j] = -1;
-      w[j] = row[j] >= 0 ? p.weight[slot0 + s0 + j] : 0.0f;
-    }
-    for (int v = threadIdx.x; v < nv; v += kGradThreads) {
+    for (int j = 0; j < KS; ++j)
+      if (ANY) inside = inside && (row[j] < 0 || row_inside(row[j], p.slots, H));
+    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+      uint4 x[KS];
       if constexpr (!ANY) {
-        uint4 x[KS];
-        float d[8];
-        unpack8<T>(*reinterpret_cast<const uint4*>(d_out + 2 * (t * H + 8 * v)), d);
+        const uint4 d = *reinterpret_cast<const uint4*>(d_out + 2 * (d_start + 8 * v));
 #pragma unroll
         for (int j = 0; j < KS; ++j)
           if (row[j] >= 0) x[j] = load_words(p.rows, row[j], H, 8 * v);
 #pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          if (row[j] < 0) continue;
-          float f[8], o[8];
-          unpack8<T>(x[j], f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dot[j] = fmaf(d[i], f[i], dot[j]);
-            o[i] = d[i] * w[j];
-          }
-          store_words<false>(p.out, RowWords<false>(H, row[j]), 8 * v, pack8<T>(o));
-        }
+        for (int j = 0; j < KS; ++j)
+          if (row[j] >= 0)
+            store_words<false>(p.out, RowWords<false>(H, row[j]), 8 * v,
+                               grad_word<T>(dot[j], d, x[j], w[j]));
       } else {
         // the words of rows and d_rows, which start alike, differ from slot to
-        // slot, and so does what they need of d_out. One slot after the other:
-        // with the loads of four in flight the registers cost more than that
-        // gains (123 against 82 us, 5003 tokens, 6 slots, 2047 columns)
+        // slot, and so does what they need of d_out
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          if (row[j] < 0) continue;
+          const RowWords<true> r(H, row[j]);
+          const int64_t at = 2 * (r.start + r.column(v));
+          if (r.column(v) < H)
+            x[j] = inside ? __ldcs(reinterpret_cast<const uint4*>(rows + at))
+                          : word_at(rows, at, total_rows);
+        }
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
           if (row[j] < 0) continue;
           const RowWords<true> r(H, row[j]);
           const int col = r.column(v);
           if (col >= H) continue;
-          float d[8], f[8], o[8];
-          const int64_t at = 2 * (static_cast<int64_t>(t) * H + col);
-          if (t_inside && row_inside(row[j], p.slots, H)) {
+          const int64_t at = 2 * (d_start + col);
+          uint4 d;
+          if (inside) {
             const uint32_t shift = static_cast<uint32_t>(at) & 15u;
             const uint4* src = reinterpret_cast<const uint4*>(d_out + at - shift);
-            const uint4 x = __ldcs(reinterpret_cast<const uint4*>(rows + 2 * (r.start + col)));
-            unpack8<T>(shift_out(__ldg(src), __ldg(src + 1), shift), d);
-            unpack8<T>(x, f);
+            d = shift_out(__ldg(src), __ldg(src + 1), shift);
           } else {
-            unpack8<T>(bytes_at(d_out, at, total), d);
-            unpack8<T>(word_at(rows, 2 * (r.start + col), total_rows), f);
+            d = bytes_at(d_out, at, total);
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bool in = col + i >= 0 && col + i < H;  // else a neighbour's element
-            dot[j] = in ? fmaf(d[i], f[i], dot[j]) : dot[j];
-            o[i] = d[i] * w[j];
+          if (col < 0 || col + 8 > H) {
+            d = inside_row(d, col, H);
+            x[j] = inside_row(x[j], col, H);
           }
-          store_words<true>(p.out, r, col, pack8<T>(o));
+          store_words<true>(p.out, r, col, grad_word<T>(dot[j], d, x[j], w[j]));
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
+      float sum = dot[j].x + dot[j].y;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
-      if (lane_id() == 0 && s0 + j < p.topk) part[s0 + j][warp] = dot[j];
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      if (lane_id() == 0 && s0 + j < p.topk) part[s0 + j][warp] = sum;
     }
   }
   __syncthreads();
-  for (int s = threadIdx.x; s < p.topk; s += kGradThreads) {
+  for (int s = threadIdx.x; s < p.topk; s += blockDim.x) {
     float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kGradThreads / 32; ++i) dot += part[s][i];
+    for (int i = 0; i < warps; ++i) dot += part[s][i];
     p.d_weight[slot0 + s] = dot;
   }
   // rows without a slot
@@ -674,8 +779,8 @@ __global__ void __launch_bounds__(kGradThreads) moe_combine_grad_kernel(const Ga
   tail.hidden = H;
   tail.rows = p.out;
   clear_tail<MOE_COPY>(tail, min(max(p.offsets[p.experts], 0), p.slots),
-                       static_cast<int64_t>(blockIdx.x) * kGradThreads + threadIdx.x,
-                       static_cast<int64_t>(gridDim.x) * kGradThreads);
+                       static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+                       static_cast<int64_t>(gridDim.x) * blockDim.x);
 }
 
 // -------------------------------------------------------------- quantisation
@@ -812,22 +917,32 @@ cudaError_t for_slots(int topk, F f) {
   return f(std::integral_constant<int, 8>());
 }
 
+// up to `most` warps for `windows` of a row: as few as the same turns need
+int even_warps(int windows, int most) {
+  const int turns = (windows + most - 1) / most;
+  return turns == 0 ? 1 : (windows + turns - 1) / turns;
+}
+
 template <typename T>
 cudaError_t gather_t(const GatherParams& p, int sms, cudaStream_t stream, int pdl) {
-  const bool any = p.hidden % 8 != 0;
-  const int64_t items =
-      static_cast<int64_t>(p.tokens) *
-      (any ? ((p.hidden + 14) / 8 + 30) / 31 * 32 : p.hidden / 8);
+  if (p.hidden % 8 != 0) {
+    const int threads = 32 * even_warps(((p.hidden + 14) / 8 + 30) / 31, kAnyWarps);
+    return for_slots(p.topk, [&](auto ks) {
+      constexpr int KS = decltype(ks)::value;
+      auto go = [&](auto kernel) {
+        return launch(kernel, dim3(static_cast<unsigned>(p.tokens)), threads, 0, stream, pdl, p);
+      };
+      return p.weight ? go(moe_gather_any_kernel<T, true, KS>)
+                      : go(moe_gather_any_kernel<T, false, KS>);
+    });
+  }
+  const int64_t items = static_cast<int64_t>(p.tokens) * (p.hidden / 8);
   const int64_t want = (items + 255) / 256, most = static_cast<int64_t>(sms) * 64;
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
   return for_slots(p.topk, [&](auto ks) {
     constexpr int KS = decltype(ks)::value;
     auto go = [&](auto kernel) { return launch(kernel, grid, 256, 0, stream, pdl, p); };
-    if (p.weight)
-      return any ? go(moe_gather_kernel<T, true, true, KS>)
-                 : go(moe_gather_kernel<T, false, true, KS>);
-    return any ? go(moe_gather_kernel<T, true, false, KS>)
-               : go(moe_gather_kernel<T, false, false, KS>);
+    return p.weight ? go(moe_gather_kernel<T, true, KS>) : go(moe_gather_kernel<T, false, KS>);
   });
 }
 
@@ -835,9 +950,11 @@ template <typename T>
 cudaError_t grad_t(const GatherParams& p, cudaStream_t stream, int pdl) {
   const dim3 grid(static_cast<unsigned>(p.tokens));
   const bool any = p.hidden % 8 != 0;
+  const int threads =
+      32 * even_warps(((any ? p.hidden + 14 : p.hidden) / 8 + 31) / 32, kGradWarps);
   return for_slots(p.topk, [&](auto ks) {
     constexpr int KS = decltype(ks)::value;
-    auto go = [&](auto kernel) { return launch(kernel, grid, kGradThreads, 0, stream, pdl, p); };
+    auto go = [&](auto kernel) { return launch(kernel, grid, threads, 0, stream, pdl, p); };
     return any ? go(moe_combine_grad_kernel<T, true, KS>)
                : go(moe_combine_grad_kernel<T, false, KS>);
   });
