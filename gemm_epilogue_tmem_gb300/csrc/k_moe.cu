@@ -348,6 +348,27 @@ __global__ void __launch_bounds__(256) moe_copy_kernel(const MoeParams p) {
                    static_cast<int64_t>(gridDim.x) * 256);
 }
 
+// The rows of x that this chunk's tokens are copied from, on their way to L2
+// while the sort, which leaves HBM idle, ends: where x fills at most half of L2.
+// Asked for before the counts have been shared they hold those up. 2048 tokens,
+// 8 slots, 5120 columns: 35.4 us (e4m3 23.3), without 37.6 (24.6); 4096 tokens
+// 64.4 (40.2) and 65.5 (40.7).
+constexpr int64_t kPrefetchBytes = 64 << 20;
+
+__device__ __forceinline__ void prefetch_rows(const MoeParams& p) {
+  const int64_t row = 2 * static_cast<int64_t>(p.hidden), total = p.tokens * row;
+  if (p.x == nullptr || total > kPrefetchBytes) return;
+  // (whole 16-byte words: of an odd row's last one the copy loads the rest itself)
+  const int64_t begin = min(blockIdx.x * p.chunk_tokens * row, total) & ~int64_t(15);
+  const int64_t end = min((blockIdx.x + int64_t(1)) * p.chunk_tokens * row, total) & ~int64_t(15);
+  constexpr int64_t kPiece = 16384;
+  for (int64_t at = begin; at < end; at += kPiece)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                     static_cast<const uint8_t*>(p.x) + at),
+                 "r"(static_cast<uint32_t>(min(kPiece, end - at)))
+                 : "memory");
+}
+
 // The sort, and with few slots (fused) the copies of the chunk's tokens too.
 template <typename T, int COPY, bool ANY>
 __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoeParams p) {
@@ -431,6 +452,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
     prior = before[tid];
     all = prior + total[tid];
   }
+
+  if (COPY == MOE_SORT_ONLY && tid == kSortThreads - 1) prefetch_rows(p);
 
   // the experts' first rows (exclusive sum)
   int incl = all;
