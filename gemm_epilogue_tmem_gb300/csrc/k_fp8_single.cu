@@ -34,7 +34,8 @@ constexpr int kLaunchRegs = 168, kCtlRegs = 56, kEpiRegs = 224;
 static_assert(128 * kCtlRegs + 256 * kEpiRegs <= kThreadsSingle * kLaunchRegs,
               "register redistribution within the launch's registers");
 constexpr int kBPart = 128 * 128;  // 128 rows of a weight
-constexpr int kRing = 8;           // blocks of scales in flight
+constexpr int kScaleGroup = 8;     // blocks whose scales come together
+constexpr int kRing = 2;           // such groups in flight
 constexpr int kPad = 144;          // staged row: 128 bytes + 16 against bank conflicts
 
 constexpr int TR = 128;            // rows of a tile
@@ -44,7 +45,7 @@ constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kStaging = kEpiWarps * 32 * kPad;
 constexpr int kSlot = TR + 4;      // floats of a ring slot: rows, two column blocks
 constexpr int kTable = 2 * (kFp8MaxGroups + 2) * 4;
-constexpr int kFixed = kSmemAlignSlack + kSmemCtrlBytes + kStaging + kRing * kSlot * 4 +
+constexpr int kFixed = kSmemAlignSlack + kSmemCtrlBytes + kStaging + kRing * kScaleGroup * kSlot * 4 +
                        2 * TR * 4 + kTable;
 constexpr int S = (kSmemPerCta - kFixed) / kStageBytes;
 constexpr int kSmemSingle = kFixed + S * kStageBytes;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreadsSingle, 1)
   const uint32_t sfull0 = ctrl + 16u * S + 48u, sempty0 = sfull0 + 8u * kRing;
   uint8_t* staging = gctrl + kSmemCtrlBytes;
   float* ring = reinterpret_cast<float*>(staging + kStaging);
-  uint32_t* row_mag = reinterpret_cast<uint32_t*>(ring + kRing * kSlot);
+  uint32_t* row_mag = reinterpret_cast<uint32_t*>(ring + kRing * kScaleGroup * kSlot);
   GroupTable table;
   table.row0 = reinterpret_cast<int32_t*>(row_mag + 2 * TR);
   table.tile0 = table.row0 + kFp8MaxGroups + 2;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreadsSingle, 1)
         const float* bs = (DUAL && lane == 1 ? p.b2_scale : p.b_scale) +
                           (static_cast<int64_t>(g) * p.num_n_blocks + nb) * KB;
         const bool b_in = lane < 2 && nb < p.num_n_blocks;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb0 = 0; kb0 < KB; kb0 += kScaleGroup) {
           ok = mbar_wait_bounded(sempty0 + 8u * slot, phase ^ 1u, abort_flag, p.wait_limit_ns);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) {
@@ -244,14 +245,17 @@ __global__ void __launch_bounds__(kThreadsSingle, 1)
             aborted = true;
             break;
           }
-          const uint32_t dst = ring_s + 4u * (kSlot * slot + lane);
+          const int last = min(kb0 + kScaleGroup, KB);
+          uint32_t dst = ring_s + 4u * (kSlot * kScaleGroup * slot + lane);
+          for (int kb = kb0; kb < last; ++kb, dst += 4u * kSlot) {
 #pragma unroll
-          for (int i = 0; i < TR / 32; ++i) {
-            const bool in = 32 * i + static_cast<int>(lane) < rows;
-            cp_async_4(dst + 128u * i,
-                       in ? as + static_cast<int64_t>(32 * i) * KB + kb : p.a_scale, in);
+            for (int i = 0; i < TR / 32; ++i) {
+              const bool in = 32 * i + static_cast<int>(lane) < rows;
+              cp_async_4(dst + 128u * i,
+                         in ? as + static_cast<int64_t>(32 * i) * KB + kb : p.a_scale, in);
+            }
+            if (lane < 2) cp_async_4(dst + 4u * TR, b_in ? bs + kb : p.b_scale, b_in);
           }
-          if (lane < 2) cp_async_4(dst + 4u * TR, b_in ? bs + kb : p.b_scale, b_in);
           cp_async_arrive(sfull0 + 8u * slot);
           if (++slot == kRing) {
             slot = 0;
@@ -349,50 +353,48 @@ __global__ void __launch_bounds__(kThreadsSingle, 1)
       const bool busy = 32 * q < rows;  // the warp has rows of this tile
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int left = KB; left > 0 && ok; left -= kScaleGroup) {
         ok = mbar_wait_bounded(sfull0 + 8u * slot, sphase, abort_flag, p.wait_limit_ns);
-        const float* sc = ring + kSlot * slot;
-        const float sa = sc[r];
-        const uint64_t s_a = both(sa * sc[DUAL ? TR : TR + sub]);
-        const uint64_t s_b = DUAL ? both(sa * sc[TR + 1]) : s_a;
-        ok = mbar_wait_bounded(tfull0 + 8u * buf, bphase, abort_flag, p.wait_limit_ns) && ok;
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                               256u * static_cast<uint32_t>(buf);
-        if (busy) {
-          // 64 columns at a time: two loads in flight, and the accumulator is
-          // released as soon as the second pair is in registers
-          uint32_t v[2][32];
+        const float* sc = ring + kSlot * kScaleGroup * slot;
+        for (int kb = min(left, kScaleGroup); kb > 0; --kb, sc += kSlot) {
+          const float sa = sc[r];
+          const uint64_t s_a = both(sa * sc[DUAL ? TR : TR + sub]);
+          const uint64_t s_b = DUAL ? both(sa * sc[TR + 1]) : s_a;
+          ok = mbar_wait_bounded(tfull0 + 8u * buf, bphase, abort_flag, p.wait_limit_ns) && ok;
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                 256u * static_cast<uint32_t>(buf);
+          if (busy) {
+            // 64 columns at a time: two loads in flight, and the accumulator is
+            // released as soon as the second pair is in registers
+            uint32_t v[2][32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b), v[0]);
-            tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b) + 32u, v[1]);
-            tmem_ld_wait_tied(v[0]);
-            tmem_tie(v[1]);
-            if (c == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(tempty0 + 8u * buf);
-                mbar_arrive(sempty0 + 8u * slot);
+            for (int c = 0; c < 2; ++c) {
+              tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b), v[0]);
+              tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b) + 32u, v[1]);
+              tmem_ld_wait_tied(v[0]);
+              tmem_tie(v[1]);
+              if (c == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tempty0 + 8u * buf);
               }
-            }
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              fma2(acc[32 * c + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1],
-                   c == 0 ? s_a : s_b);
+              for (int j = 0; j < 32; ++j)
+                fma2(acc[32 * c + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1],
+                     c == 0 ? s_a : s_b);
+            }
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty0 + 8u * buf);
           }
-        } else {
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(tempty0 + 8u * buf);
-            mbar_arrive(sempty0 + 8u * slot);
-          }
+          buf ^= 1;
+          bphase ^= buf == 0 ? 1u : 0u;
         }
-        buf ^= 1;
-        bphase ^= buf == 0 ? 1u : 0u;
+        __syncwarp();  // all lanes have read their scales
+        if (lane == 0) mbar_arrive(sempty0 + 8u * slot);
         if (++slot == kRing) {
           slot = 0;
           sphase ^= 1u;

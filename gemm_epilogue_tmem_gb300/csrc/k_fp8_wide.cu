@@ -52,9 +52,10 @@ constexpr int kStageBytes = 2 * kPartBytes;      // per CTA
 constexpr int kStagePad = 272;
 constexpr int kStagePadDual = 80;
 constexpr int kStagingBytes = kEpiWarps * 32 * kStagePad;
-constexpr int kScaleRing = 8;
-constexpr int kScaleSlot = 132;                  // floats: 128 rows, two column blocks
-constexpr int kScaleBytes = kScaleRing * kScaleSlot * 4;
+constexpr int kScaleGroup = 8;                   // blocks whose scales come together
+constexpr int kScaleRing = 2;                    // groups
+constexpr int kScaleSlot = 132;                  // floats of a block: 128 rows, two column blocks
+constexpr int kScaleBytes = kScaleRing * kScaleGroup * kScaleSlot * 4;
 constexpr int kTableBytes = 2 * (kFp8MaxGroups + 2) * 4;
 constexpr int kMagBytes = 2 * 128 * 4;
 constexpr int kStagesWide = (kSmemPerCta - kSmemAlignSlack - kSmemCtrlBytes - kStagingBytes -
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         const float* bs = (DUAL && lane == 1 ? p.b2_scale : p.b_scale) +
                           (static_cast<int64_t>(g) * p.num_n_blocks + nb) * KB;
         const bool b_in = lane < 2 && nb < p.num_n_blocks;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb0 = 0; kb0 < nkb; kb0 += kScaleGroup) {
           ok = mbar_wait_bounded(sempty0 + 8u * slot, phase ^ 1u, abort_flag, p.wait_limit_ns);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) {
@@ -289,14 +290,17 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
             aborted = true;
             break;
           }
-          const uint32_t dst = ring + 4u * (kScaleSlot * slot + lane);
+          const int last = min(kb0 + kScaleGroup, nkb);
+          uint32_t dst = ring + 4u * (kScaleSlot * kScaleGroup * slot + lane);
+          for (int kb = kb0; kb < last; ++kb, dst += 4u * kScaleSlot) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = r0 + 32 * i < p.M;
-            cp_async_4(dst + 128u * i,
-                       in ? as + static_cast<int64_t>(32 * i) * KB + kb : p.a_scale, in);
+            for (int i = 0; i < 4; ++i) {
+              const bool in = r0 + 32 * i < p.M;
+              cp_async_4(dst + 128u * i,
+                         in ? as + static_cast<int64_t>(32 * i) * KB + kb : p.a_scale, in);
+            }
+            if (lane < 2) cp_async_4(dst + 512u, b_in ? bs + kb : p.b_scale, b_in);
           }
-          if (lane < 2) cp_async_4(dst + 512u, b_in ? bs + kb : p.b_scale, b_in);
           cp_async_arrive(sfull0 + 8u * slot);
           if (++slot == kScaleRing) {
             slot = 0;
@@ -331,42 +335,43 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0ull;
       bool ok = true;
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int left = nkb; left > 0 && ok; left -= kScaleGroup) {
         ok = mbar_wait_bounded(sfull0 + 8u * slot, sphase, abort_flag, p.wait_limit_ns);
-        const float* sc = scales + kScaleSlot * slot;
-        const float sa = sc[32 * q + lane];
-        const uint64_t s_a = both(sa * sc[DUAL ? 128 : 128 + sub]);
-        const uint64_t s_b = DUAL ? both(sa * sc[129]) : s_a;
-        ok = mbar_wait_bounded(tfull0 + 8u * buf, bphase, abort_flag, p.wait_limit_ns) && ok;
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                               256u * static_cast<uint32_t>(buf);
-        // 64 columns at a time: two loads in flight, and the accumulator is
-        // released as soon as the second pair is in registers
-        uint32_t v[2][32];
+        const float* sc = scales + kScaleSlot * kScaleGroup * slot;
+        for (int kb = min(left, kScaleGroup); kb > 0; --kb, sc += kScaleSlot) {
+          const float sa = sc[32 * q + lane];
+          const uint64_t s_a = both(sa * sc[DUAL ? 128 : 128 + sub]);
+          const uint64_t s_b = DUAL ? both(sa * sc[129]) : s_a;
+          ok = mbar_wait_bounded(tfull0 + 8u * buf, bphase, abort_flag, p.wait_limit_ns) && ok;
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                 256u * static_cast<uint32_t>(buf);
+          // 64 columns at a time: two loads in flight, and the accumulator is
+          // released as soon as the second pair is in registers
+          uint32_t v[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b), v[0]);
-          tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b) + 32u, v[1]);
-          tmem_ld_wait_tied(v[0]);
-          tmem_tie(v[1]);
-          if (c == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_remote_relaxed(tempty_leader + 8u * buf);
-              mbar_arrive(sempty0 + 8u * slot);
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b), v[0]);
+            tmem_ld_32x32b_x32(taddr + (c == 0 ? col_a : col_b) + 32u, v[1]);
+            tmem_ld_wait_tied(v[0]);
+            tmem_tie(v[1]);
+            if (c == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote_relaxed(tempty_leader + 8u * buf);
             }
-          }
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            fma2(acc[32 * c + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1],
-                 c == 0 ? s_a : s_b);
+            for (int j = 0; j < 32; ++j)
+              fma2(acc[32 * c + j], v[j >> 4][2 * (j & 15)], v[j >> 4][2 * (j & 15) + 1],
+                   c == 0 ? s_a : s_b);
+          }
+          buf ^= 1;
+          bphase ^= buf == 0 ? 1u : 0u;
         }
-        buf ^= 1;
-        bphase ^= buf == 0 ? 1u : 0u;
+        __syncwarp();  // all lanes have read their scales
+        if (lane == 0) mbar_arrive(sempty0 + 8u * slot);
         if (++slot == kScaleRing) {
           slot = 0;
           sphase ^= 1u;
