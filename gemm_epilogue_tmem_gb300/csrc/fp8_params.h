@@ -42,6 +42,12 @@ struct Fp8LaunchArgs {
   cudaStream_t stream;
 };
 
+// What it costs the narrow kernel to join the parts of split tiles, in k-blocks
+// of a CTA's time (6 to 8 us)
+__host__ __device__ constexpr int fp8_join_blocks(int tile_rows, int dual) {
+  return dual ? 12 : tile_rows == 16 ? 24 : 32;
+}
+
 // the narrow kernel: 128 columns of B x tile_rows (16 or 64) rows per tile
 cudaError_t launch_fp8_narrow(const Fp8LaunchArgs& a);
 int fp8_narrow_stages(int tile_rows, int dual);

@@ -12,14 +12,14 @@
 // another lane by shuffles instead, the shuffles set the pace: 219 against
 // 165 us on 1.07 GB of weights with 64-row tiles).
 //
-// CTA c has the tiles c, c + G, ... whole when those fill at least 60 % of the
-// grid's rounds: an SM alone takes more than its share of the HBM rate, so that
-// the others make up for an idle one (136 tiles on 152 SMs, one 89 MB weight:
-// 19.4 us whole, 21.9 us split). Fewer tiles are split evenly in units of
-// one k-block: CTA c has the units [c W / G, (c + 1) W / G) of the tiles laid
-// end to end. A tile that falls to several CTAs is summed by the last of them
-// to finish, over the partial sums in the plan's workspace in k order: no CTA
-// waits for another, and the sum's order does not depend on which is last.
+// CTA c has the tiles c, c + G, ... whole where splitting them evenly would
+// spare each CTA fewer k-blocks than the join of the parts costs (8 rows, 9000
+// columns, k = 2048, 71 tiles on 152 SMs: 8.2 us whole, 11.7 split; one row,
+// 5120 columns, k = 17408, 40 tiles: 17 split, 35 whole). Otherwise they are split
+// in units of one k-block: CTA c has the units [c W / G, (c + 1) W / G) of the
+// tiles laid end to end. A tile that falls to several CTAs is summed by the last
+// of them to finish, over the partial sums in the plan's workspace in k order:
+// no CTA waits for another, and the sum's order does not depend on which is last.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issue, warps 2-5 epilogue, warp 6
 // scale loads. All waits are bounded.
@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
   constexpr int kMinUnits = 4;
   const int cta = static_cast<int>(blockIdx.x), grid = static_cast<int>(gridDim.x);
   const int rounds = (product_tiles + grid - 1) / grid;
-  const bool whole = 10ll * product_tiles >= 6ll * rounds * grid;
+  const bool whole = (static_cast<int64_t>(rounds) * grid - product_tiles) * KB <=
+                     static_cast<int64_t>(fp8_join_blocks(TR, DUAL)) * grid;
   const int64_t units = static_cast<int64_t>(product_tiles) * KB;
   const int64_t most = units / kMinUnits;
   const int ctas = most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;

@@ -5,6 +5,9 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "fp8_params.h"
 #include "gf.h"
 #include "params.h"
@@ -27,30 +30,57 @@ bool given_scale(const void* p) {
 // GF_OPT_KERNEL
 enum : int { kNarrow16 = 1, kNarrow64 = 2, kSingle = 3, kPair = 4 };
 
-// Kernel and tiles of the plan. The average number of rows a group decides:
-// the counts themselves are on the device. Measured, in us (m rows, n, k; "64 x"
-// is 64 groups of m rows with 0.5 GB of weights):
-//                       16-row  64-row  single  pair
-//   1, 17408, 5120        14      20      28     33   up to 16 rows: the 16-row tiles
-//   64, 17408, 5120       41      18      27     25   68 tiles do not fill the SMs
-//   64 x 64, 4096, 2048    -      94      94    134   tiles that do: each weight read
-//   64 x 128, 4096, 2048   -     158     119    137     once by one SM
-//   128, 17408, 5120       -      30      28     25   68 pair tiles on 76 pairs
-//   128, 5120, 17408       -      34      75     63   20 pair tiles: k is split
+// What a kernel takes, in us: start + block * (k-blocks one after the other on
+// an SM) + round * (tiles one after the other on it). Fitted to the times of all four
+// for 526 products (8 to 51200 rows, 1 to 128 groups, 256 to 17408 columns, k 512
+// to 16384). The kernel that it names is within 1 % of the best of the four on
+// average and 30 % at worst (48 rows, 1000 columns, k = 16384: 64-row tiles 18.5
+// us, 16-row tiles 14.1). Some of them (rows, columns, k; "64 x": groups):
+//                           16-row  64-row  single  pair
+//   8, 17408, 8192            26      31      52     40
+//   48, 9000, 8192            32      23      32     30
+//   256, 4096, 8192           59      24      32     30
+//   256, 17408, 8192         294      87      38     36
+//   64 x 64, 4096, 2048        -     119      90    130
+//   64 x 256, 4096, 2048       -     353     161    181
+//   8 x 1024, 4096, 16384      -       -     482    425
+struct Pace {
+  double start, block, round;
+};
+constexpr Pace kPace[2][4] = {
+    // 16-row tiles, 64-row tiles, single CTA, CTA pair
+    {{4.0, 0.22, 0.8}, {4.0, 0.29, 1.2}, {3.4, 0.38, 2.8}, {4.2, 0.34, 2.8}},
+    {{4.0, 0.32, 3.0}, {4.0, 0.75, 7.0}, {4.6, 0.35, 3.0}, {4.8, 0.33, 3.6}}};  // SwiGLU
+
+// The time of one kernel for the plan. The rows of each group are on the
+// device: they are taken to be about alike, with a part of a tile more each.
+double expected_time(const gf_plan* p, int kernel) {
+  const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
+  const int64_t tile_rows = kernel == kNarrow16 ? 16 : kernel == kNarrow64 ? 64
+                            : kernel == kSingle ? 128 : 256;
+  const int64_t tile_n = kernel <= kNarrow64 || dual ? 128 : 256;
+  const double groups = static_cast<double>(p->groups), m = static_cast<double>(p->m);
+  const double row_tiles = p->groups == 1 ? std::ceil(m / tile_rows)
+                                          : groups * std::max(1.0, m / groups / tile_rows + 0.4);
+  const double tiles = row_tiles * static_cast<double>((p->n + tile_n - 1) / tile_n);
+  const double each = tiles / (kernel == kPair ? p->max_pair_clusters : p->num_sms);
+  const double rounds = p->groups == 1 ? std::ceil(each) : std::max(1.0, each);
+  const double kb = static_cast<double>((p->k + 127) / 128);
+  double blocks = rounds * kb;
+  if (kernel <= kNarrow64) blocks = std::min(blocks, each * kb + gf::fp8_join_blocks(static_cast<int>(tile_rows), dual));
+  const Pace& c = kPace[dual][kernel - 1];
+  return c.start + c.block * blocks + c.round * rounds;
+}
+
+// Kernel and tiles of the plan.
 void plan_tiles(gf_plan* p) {
   const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
-  const int64_t rows = p->m / p->groups;
   const int tile_n = dual ? 128 : 256;  // of the single-CTA and the pair kernel
   int kernel = p->forced_kernel;
   if (kernel == 0) {
-    const int64_t tiles = p->groups * ((p->n + tile_n - 1) / tile_n);
-    const bool fills = 10 * tiles >= 6 * ((tiles + p->num_sms - 1) / p->num_sms) * p->num_sms;
-    if (rows <= 16)
-      kernel = kNarrow16;
-    else if (rows <= 128 && fills)
-      kernel = kSingle;
-    else
-      kernel = rows <= 64 || (rows <= 128 && 2 * tiles < p->max_pair_clusters) ? kNarrow64 : kPair;
+    kernel = kNarrow16;
+    for (int other = kNarrow64; other <= (p->max_pair_clusters > 0 ? kPair : kSingle); ++other)
+      if (expected_time(p, other) < expected_time(p, kernel)) kernel = other;
   }
   if (kernel == kPair && p->max_pair_clusters == 0) kernel = kSingle;
   p->kernel = kernel;
