@@ -13,21 +13,24 @@
 //
 // What bounds it: an accumulator's way round. A block's products take 512
 // cycles; its commit, the epilogue's wake-up, loads and release and the next
-// issue take about 1100 more, of which the second accumulator hides its own
-// 512: (512 + 1100) / 2 = 806 cycles a block, measured with that handshake alone,
-// and 850 in this kernel. Tensor memory has no room for a third accumulator of
-// this width, and with four of 128 columns the N = 128 instructions (365 cycles
-// a half) are the slower choice (475 against 420 us). Measured at m = 8192,
-// n = 16384, k = 4096: 420 us, 2.62 PFLOP/s (k = 16384: 2.8); 445-460 us in a
+// issue take about 900 more, of which the second accumulator hides its own
+// 512: 713 cycles a block (0.375 us, from k = 1024 against k = 4096). Tensor
+// memory has no room for a third accumulator of this width, and with four of 128
+// columns the N = 128 instructions (365 cycles a half) are the slower choice.
+// Measured at m = 8192, n = 16384, k = 4096: 378 us, 2.9 PFLOP/s; 390-420 us in a
 // steady loop at the power cap.
 //
 // The rows' scales lie a row apart in memory, so that a warp's load of one block
 // touches 32 sectors: a warp of its own copies them asynchronously into a ring
-// of kScaleRing blocks in shared memory, ahead of the epilogue.
+// in shared memory, ahead of the epilogue, kScaleGroup blocks at a time. With one
+// block at a time, released with the accumulator, that warp woke up and loaded
+// exactly when the epilogue warps of its scheduler were in the accumulator's
+// way: 420 us instead of 383.
 //
-// A finished tile goes through a shared-memory staging buffer of the whole tile
-// and leaves it by bulk copies of a row segment each, while the next tile's
-// blocks are already being added.
+// A finished tile goes through a shared-memory staging buffer of each warp's own
+// and leaves it in whole row segments (by one bulk copy a row instead, which
+// a warp issues one after the other: 527 against 503 us, 64 groups of 512 rows,
+// gate and up projections of 4096 x 2048).
 //
 // Roles: warpgroup 0 = TMA producer, MMA issue (leader CTA), scale loads, one
 // idle warp; warpgroups 1 and 2 epilogue. All waits are bounded.
@@ -39,7 +42,6 @@ namespace {
 constexpr int kThreadsWide = 384;
 constexpr int kCtlWarps = 4;
 constexpr int kEpiWarps = 8;
-constexpr int kEpiThreadsWide = 256;
 // registers per thread at launch (65536 / 384, in steps of 8), and after the
 // redistribution from the control to the epilogue warpgroups
 constexpr int kLaunchRegs = 168, kCtlRegs = 56, kEpiRegs = 224;
@@ -66,13 +68,6 @@ constexpr int kSmemWide = kSmemAlignSlack + kStagesWide * kStageBytes + kSmemCtr
 // row tiles visited together, column by column: 442 us in a steady loop at
 // m = 8192, n = 16384, k = 4096, against 448 with 8 and 458 with 4
 constexpr int kRasterRows = 16;
-
-// bulk copy of `bytes` (a multiple of 16) from shared to global memory
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
-               "r"(bytes)
-               : "memory");
-}
 
 template <typename T, bool DUAL>
 __global__ void __launch_bounds__(kThreadsWide, 1)
@@ -377,14 +372,13 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
           sphase ^= 1u;
         }
       }
-      if constexpr (DUAL) ok = !named_bar_red_or(1, kEpiThreadsWide, !ok);
+      // (DUAL: the two warps of a quarter agree on the outcome, a barrier follows)
+      if constexpr (DUAL) ok = !named_bar_red_or(1 + q, 64, !ok);
       if (!ok) {
         fp8_raise(p, abort_flag, ST_TIMEOUT_EPILOGUE);
         aborted = true;
         break;
       }
-      // this lane's row of the previous tile has left the staging buffer
-      bulk_wait_read<0>();
       if constexpr (!DUAL) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -396,11 +390,18 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
           }
           *reinterpret_cast<uint4*>(my_stg + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        const int n = nt * 256 + 128 * sub;
-        fence_proxy_async_smem();
-        if (my_row < row_end && n < p.N)
-          bulk_store(static_cast<T*>(p.out) + static_cast<int64_t>(my_row) * p.N + n,
-                     smem_u32(my_stg), 2u * min(128, p.N - n));
+        __syncwarp();
+        const int n = nt * 256 + 128 * sub + 8 * static_cast<int>(lane & 15u);
+        const int r0 = my_row - static_cast<int>(lane) + static_cast<int>(lane >> 4);
+        T* dst = static_cast<T*>(p.out) + static_cast<int64_t>(r0) * p.N + n;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stg + (2 * j + (lane >> 4)) * kPad +
+                                                          16 * (lane & 15u));
+          if (r0 + 2 * j < row_end && n < p.N)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(2 * j) * p.N) = w;
+        }
+        __syncwarp();
       } else {
         // h of this row's 64 columns, its largest magnitude over the tile's
         // 128 with the other warp of the quarter
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
         bool finite;
         uint32_t mag = swiglu64(acc, p.N - n, finite);
         row_mag[128 * sub + 32 * q + lane] = mag;
-        named_bar_sync(1, kEpiThreadsWide);
+        named_bar_sync(1 + q, 64);
         mag = max(mag, row_mag[128 * (sub ^ 1) + 32 * q + lane]);
         float inv;
         const float sc = e4m3_scale(mag, inv);
@@ -417,15 +418,19 @@ __global__ void __launch_bounds__(kThreadsWide, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4*>(my_stg + 16 * j) = quant_columns(acc, j, inv, finite);
-        fence_proxy_async_smem();
-        if (my_row < row_end && n < p.N)
-          bulk_store(static_cast<uint8_t*>(p.out) + static_cast<int64_t>(my_row) * p.N + n,
-                     smem_u32(my_stg), min(64, p.N - n));
-        named_bar_sync(1, kEpiThreadsWide);  // row_mag is read before the next tile writes it
+        __syncwarp();
+        const int c0 = n + 16 * static_cast<int>(lane & 3u);
+        const int r0 = my_row - static_cast<int>(lane) + static_cast<int>(lane >> 2);
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(r0) * p.N + c0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stg + (8 * j + (lane >> 2)) * kPad +
+                                                          16 * (lane & 3u));
+          if (r0 + 8 * j < row_end && c0 < p.N)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(8 * j) * p.N) = w;
+        }
       }
-      bulk_commit();
     }
-    bulk_wait_all();  // this lane's stores have completed
   }
 
   // a CTA that gave up may still have loads in flight towards its shared
