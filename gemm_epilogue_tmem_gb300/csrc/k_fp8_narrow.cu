@@ -31,11 +31,12 @@ namespace {
 constexpr int kThreadsNarrow = 224;
 constexpr int kEpiThreads = 128;
 constexpr int kBBytes = 128 * 128;
-constexpr int kRing = 8;  // blocks of scales in flight
+constexpr int kScaleGroup = 8;  // blocks whose scales come together
+constexpr int kRing = 2;        // such groups in flight
 
 // shared memory besides the stages and the table of groups
 constexpr int narrow_fixed(int tr) {
-  return kSmemAlignSlack + kSmemCtrlBytes + 4 * tr * 4 + kRing * (tr + 4) * 4;
+  return kSmemAlignSlack + kSmemCtrlBytes + 4 * tr * 4 + kRing * kScaleGroup * (tr + 4) * 4;
 }
 constexpr int narrow_table(int groups) { return 2 * (groups + 2) * 4; }
 // 16-row tiles: two CTAs fit on an SM (113 KB each, with the table of 128
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 1);
   // the ring first: its slots are read 16 bytes at a time
   float* ring = reinterpret_cast<float*>(gctrl + kSmemCtrlBytes);
-  uint32_t* warp_mag = reinterpret_cast<uint32_t*>(ring + kRing * C::kSlot);
+  uint32_t* warp_mag = reinterpret_cast<uint32_t*>(ring + kRing * kScaleGroup * C::kSlot);
   GroupTable table;
   table.row0 = reinterpret_cast<int32_t*>(warp_mag + 4 * TR);
   table.tile0 = table.row0 + p.groups + 2;
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
       // lanes 0 and 1: the scales of the tile's columns of B and of B2
       const float* bs = (DUAL && lane == 1 ? p.b2_scale : p.b_scale) +
                         (static_cast<int64_t>(g) * p.num_n_blocks + nt) * KB;
-      for (int kb = u.kb0; kb < u.kb1; ++kb) {
+      for (int kb0 = u.kb0; kb0 < u.kb1; kb0 += kScaleGroup) {
         ok = mbar_wait_bounded(sempty0 + 8u * slot, phase ^ 1u, abort_flag, p.wait_limit_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) {
@@ -363,16 +364,19 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
           aborted = true;
           break;
         }
-        const uint32_t dst = ring_s + 4u * (C::kSlot * slot + lane);
+        const int last = min(kb0 + kScaleGroup, u.kb1);
+        uint32_t dst = ring_s + 4u * (C::kSlot * kScaleGroup * slot + lane);
+        for (int kb = kb0; kb < last; ++kb, dst += 4u * C::kSlot) {
 #pragma unroll
-        for (int i = 0; i < (TR + 31) / 32; ++i) {
-          const int r = 32 * i + static_cast<int>(lane);
-          const bool in = r < rows;  // rows past the tile's: zero
-          if (r < TR)
-            cp_async_4(dst + 128u * i,
-                       in ? as + static_cast<int64_t>(32 * i) * KB + kb : p.a_scale, in);
+          for (int i = 0; i < (TR + 31) / 32; ++i) {
+            const int r = 32 * i + static_cast<int>(lane);
+            const bool in = r < rows;  // rows past the tile's: zero
+            if (r < TR)
+              cp_async_4(dst + 128u * i,
+                         in ? as + static_cast<int64_t>(32 * i) * KB + kb : p.a_scale, in);
+          }
+          if (lane < (DUAL ? 2 : 1)) cp_async_4(dst + 4u * TR, bs + kb, true);
         }
-        if (lane < (DUAL ? 2 : 1)) cp_async_4(dst + 4u * TR, bs + kb, true);
         cp_async_arrive(sfull0 + 8u * slot);
         if (++slot == kRing) {
           slot = 0;
@@ -444,37 +448,38 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
       tile_at(u.tile, g, row, rows, nt);
 #pragma unroll
       for (int j = 0; j < NACC; ++j) acc[j] = 0ull;
-      for (int kb = u.kb0; kb < u.kb1; ++kb) {
+      for (int left = u.kb1 - u.kb0; left > 0 && ok; left -= kScaleGroup) {
         ok = mbar_wait_bounded(sfull0 + 8u * slot, sphase, abort_flag, p.wait_limit_ns);
-        ok = mbar_wait_bounded(tfull0 + 8u * buf, bphase, abort_flag, p.wait_limit_ns) && ok;
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const float* sc = ring + C::kSlot * slot;
-        const uint64_t sb = both(sc[TR]);
-        const uint64_t sb2 = DUAL ? both(sc[TR + 1]) : sb;
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                               static_cast<uint32_t>(buf * C::kAccCols);
+        const float* sc = ring + C::kSlot * kScaleGroup * slot;
+        for (int kb = min(left, kScaleGroup); kb > 0; --kb, sc += C::kSlot) {
+          ok = mbar_wait_bounded(tfull0 + 8u * buf, bphase, abort_flag, p.wait_limit_ns) && ok;
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t sb = both(sc[TR]);
+          const uint64_t sb2 = DUAL ? both(sc[TR + 1]) : sb;
+          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                 static_cast<uint32_t>(buf * C::kAccCols);
 #pragma unroll
-        for (int c = 0; c < TR; c += CH) {
-          uint32_t v[CH];
-          load_acc<CH>(taddr + c, v);
-          add_scaled<CH>(acc + c / 2, v, sb, sc + c);
-          if constexpr (DUAL) {
-            load_acc<CH>(taddr + TR + c, v);
-            add_scaled<CH>(acc + (TR + c) / 2, v, sb2, sc + c);
+          for (int c = 0; c < TR; c += CH) {
+            uint32_t v[CH];
+            load_acc<CH>(taddr + c, v);
+            add_scaled<CH>(acc + c / 2, v, sb, sc + c);
+            if constexpr (DUAL) {
+              load_acc<CH>(taddr + TR + c, v);
+              add_scaled<CH>(acc + (TR + c) / 2, v, sb2, sc + c);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty0 + 8u * buf);
+          if (++buf == C::kBufs) {
+            buf = 0;
+            bphase ^= 1u;
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(tempty0 + 8u * buf);
-          mbar_arrive(sempty0 + 8u * slot);
-        }
-        if (++buf == C::kBufs) {
-          buf = 0;
-          bphase ^= 1u;
-        }
+        __syncwarp();  // all lanes have read their scales
+        if (lane == 0) mbar_arrive(sempty0 + 8u * slot);
         if (++slot == kRing) {
           slot = 0;
           sphase ^= 1u;
