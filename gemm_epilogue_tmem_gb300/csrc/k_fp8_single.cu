@@ -1,6 +1,8 @@
-// Block-scaled e4m3 product on single CTAs, for groups of up to 128 rows: a tile
-// is 128 rows x 256 columns of B (SwiGLU: 128 columns of each of the two
-// weights), so that every weight passes through one SM once.
+// Block-scaled e4m3 product on single CTAs, for groups of some ten to some
+// hundred rows: a tile is 128 rows x 256 columns of B (SwiGLU: 128 columns of
+// each of the two weights). With up to 128 rows a group every weight passes
+// through one SM once; with more, a group leaves half as much of its last tile
+// empty as it does in tiles of a CTA pair.
 //
 // The rows are the tensor core's 128-row side whatever their number: an
 // instruction of 128 x N x 32 takes 128 cycles for every N up to 256 (measured,
@@ -11,13 +13,17 @@
 // The tensor core sums one block of 128 along k into one of two 256-column
 // accumulators in tensor memory; eight epilogue warps, two per 32 rows, add it
 // times its two scales to fp32 sums in registers (lane = row). The scales come
-// through a ring in shared memory that a warp of its own fills. Warps without
-// rows in a tile release its accumulators unread.
+// through a ring in shared memory that a warp of its own fills, kScaleGroup blocks
+// at a time (one at a time, that warp held up the epilogue's: 168 against 137 us, 64
+// groups of 192 rows, 4096 x 2048). Warps without rows in a tile release its
+// accumulators unread.
 //
-// What bounds it: with few rows HBM (64 groups of 4 to 64 rows, 0.54 GB of
-// weights: 89-94 us, 85-90 % of the copy rate), with 128 the 48 KB that a block
-// of k brings into each SM (119 us; the CTA-pair kernel, which brings 32 KB for
-// twice the rows, takes 137).
+// What bounds it: with few rows HBM (64 groups of 32 or 64 rows, 0.54 GB of
+// weights: 87-90 us, 90 % of the copy rate); with 128 rows and more shared
+// memory, through which the 48 KB of a k-block pass twice, written by the loads and
+// read by the tensor core, in 768 cycles at 128 bytes a cycle (64 groups of 128 rows
+// 112 us, of 512 290-310; the CTA pair, which brings 32 KB for the same products
+// of each SM, 133 and 306-323).
 //
 // Roles: warpgroup 0 = TMA producer, MMA issue, scale loads, one idle warp;
 // warpgroups 1 and 2 epilogue. All waits are bounded.

@@ -458,3 +458,24 @@ def test_refusals():
     with pytest.raises(gf.GfError):
         gf.gf_fp8_matmul_execute(matmul, **good)
     assert gf.lib().gf_fp8_matmul_execute(matmul.handle, *[a.data_ptr()] * 9, None) == gf.GF_ERR_INVALID_VALUE
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("m,n,k,groups", [
+    (40, 256, 6400, 1), (100, 136, 5120, 3), (64, 264, 8192, 1), (128, 2600, 5120, 1), (500, 2600, 5120, 1), (9, 1000, 9872, 4)])
+def test_split_tiles(m, n, k, groups, kernel):
+    """Tiles whose k falls to several CTAs, some in the second round only, joined in k order."""
+    test_matmul(m, n, k, groups, kernel)
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("m,n,k,groups", [(40, 272, 5120, 1), (30, 144, 4112, 3), (200, 1040, 2064, 2)])
+def test_split_tiles_swiglu(m, n, k, groups, kernel):
+    test_swiglu_quant(m, n, k, groups, kernel)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("blocks", [7, 8, 9, 15, 16, 17, 24, 25])
+def test_blocks_of_k(blocks, kernel):
+    """Numbers of k-blocks around the groups that their scales come in, over several tiles of each CTA."""
+    test_matmul(1500, 2056, 128 * blocks - 16, 3, kernel)

@@ -388,3 +388,18 @@ def test_refusals():
     gf.gf_plan_set_option(plan, gf.GF_OPT_PDL, 0)
     torch.cuda.synchronize()
     assert bool((o == 77).all()) and bool((rows == 0).all())
+
+
+@pytest.mark.parametrize("tokens,topk,experts,hidden", [
+    (37, 11, 40, 2047), (29, 17, 64, 4999), (16, 2, 8, 9001), (61, 6, 60, 2050), (1, 64, 70, 1241), (3, 5, 9, 249),
+    (130, 6, 16, 1025)])
+@pytest.mark.parametrize("dtype,drop", [(gf.GF_F16, 0.0), (gf.GF_BF16, 0.3)])
+def test_wide_odd_rows(tokens, topk, experts, hidden, dtype, drop):
+    """Odd widths of several turns of a warp, and more slots than are in flight together."""
+    test_back_and_gradients(tokens, topk, experts, hidden, dtype, drop)
+
+
+@pytest.mark.parametrize("tokens,topk,experts,hidden", [(1201, 6, 60, 2047), (700, 8, 64, 4104), (4099, 2, 7, 1030)])
+def test_dispatch_of_many_wide_rows(tokens, topk, experts, hidden):
+    """The sort in a launch of its own before the copies of rows longer than one piece."""
+    test_dispatch(tokens, topk, experts, hidden, gf.GF_BF16, 0.1)
