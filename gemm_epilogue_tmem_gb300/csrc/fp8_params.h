@@ -43,10 +43,12 @@ struct Fp8LaunchArgs {
 };
 
 // What it costs the narrow kernel to join the parts of split tiles, in k-blocks
-// of a CTA's time (6 to 8 us)
+// of a CTA's time (3 to 6 us)
 __host__ __device__ constexpr int fp8_join_blocks(int tile_rows, int dual) {
-  return dual ? 12 : tile_rows == 16 ? 24 : 32;
+  return dual ? 12 : tile_rows == 16 ? 15 : 20;
 }
+// The share of a grid's rounds, in percent, from which on it takes tiles whole
+__host__ __device__ constexpr int fp8_whole_fill(int64_t rounds) { return rounds > 1 ? 65 : 60; }
 
 // the narrow kernel: 128 columns of B x tile_rows (16 or 64) rows per tile
 cudaError_t launch_fp8_narrow(const Fp8LaunchArgs& a);

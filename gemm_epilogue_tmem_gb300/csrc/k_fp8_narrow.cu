@@ -12,12 +12,16 @@
 // another lane by shuffles instead, the shuffles set the pace: 219 against
 // 165 us on 1.07 GB of weights with 64-row tiles).
 //
-// CTA c has the tiles c, c + G, ... whole where splitting them evenly would
-// spare each CTA fewer k-blocks than the join of the parts costs (8 rows, 9000
-// columns, k = 2048, 71 tiles on 152 SMs: 8.2 us whole, 11.7 split; one row,
-// 5120 columns, k = 17408, 40 tiles: 17 split, 35 whole). Otherwise they are split
-// in units of one k-block: CTA c has the units [c W / G, (c + 1) W / G) of the
-// tiles laid end to end. A tile that falls to several CTAs is summed by the last
+// CTA c has the tiles c, c + G, ... whole where those fill most of the grid's
+// rounds: an SM alone takes more than its share of the HBM rate, so that the
+// others make up for an idle one (one row, 12000 columns, k = 16384, 94 tiles on
+// 152 SMs: 38.9 us whole, 40.1 split; 48 rows, 9000 columns, 213 tiles 57 and 72;
+// 96 rows, 4096 columns, 192 tiles 56 and 47). So it has them where splitting them
+// evenly would spare each CTA fewer k-blocks than the join of the parts costs (one
+// row, 4096 columns, 32 tiles: k = 2048 6.9 us whole, 7.1 split; k = 2944 8.7 and
+// 7.4; 5120 columns, k = 17408: 35 and 17). Otherwise they are split in units of
+// one k-block: CTA c has the units [c W / G, (c + 1) W / G) of the tiles laid
+// end to end. A tile that falls to several CTAs is summed by the last
 // of them to finish, over the partial sums in the plan's workspace in k order:
 // no CTA waits for another, and the sum's order does not depend on which is last.
 //
@@ -226,11 +230,16 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
   constexpr int kMinUnits = 4;
   const int cta = static_cast<int>(blockIdx.x), grid = static_cast<int>(gridDim.x);
   const int rounds = (product_tiles + grid - 1) / grid;
-  const bool whole = (static_cast<int64_t>(rounds) * grid - product_tiles) * KB <=
-                     static_cast<int64_t>(fp8_join_blocks(TR, DUAL)) * grid;
+  const int64_t room = static_cast<int64_t>(rounds) * grid;
+  const bool whole =
+      100ll * product_tiles >= fp8_whole_fill(rounds) * room ||
+      (room - product_tiles) * KB <= static_cast<int64_t>(fp8_join_blocks(TR, DUAL)) * grid;
   const int64_t units = static_cast<int64_t>(product_tiles) * KB;
   const int64_t most = units / kMinUnits;
-  const int ctas = most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;
+  int ctas = most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;
+  // (the same number of CTAs for every tile, so that none has parts of two to
+  // join: 1 x 4096 x 8192 10.7 us, otherwise 12.3)
+  if (product_tiles > 0 && ctas >= 2 * product_tiles) ctas -= ctas % product_tiles;
   auto first_unit = [&](int c) { return units * c / ctas; };
   Pieces mine;
   mine.KB = KB;

@@ -34,8 +34,8 @@ enum : int { kNarrow16 = 1, kNarrow64 = 2, kSingle = 3, kPair = 4 };
 // an SM) + round * (tiles one after the other on it). Fitted to the times of all four
 // for 526 products (8 to 51200 rows, 1 to 128 groups, 256 to 17408 columns, k 512
 // to 16384). The kernel that it names is within 1 % of the best of the four on
-// average and 30 % at worst (48 rows, 1000 columns, k = 16384: 64-row tiles 18.5
-// us, 16-row tiles 14.1). Some of them (rows, columns, k; "64 x": groups):
+// average and 37 % at worst (256 rows, 256 columns, k = 16384: 64-row tiles 18.3
+// us, 16-row tiles 13.4). Some of them (rows, columns, k; "64 x": groups):
 //                           16-row  64-row  single  pair
 //   8, 17408, 8192            26      31      52     40
 //   48, 9000, 8192            32      23      32     30
@@ -67,7 +67,10 @@ double expected_time(const gf_plan* p, int kernel) {
   const double rounds = p->groups == 1 ? std::ceil(each) : std::max(1.0, each);
   const double kb = static_cast<double>((p->k + 127) / 128);
   double blocks = rounds * kb;
-  if (kernel <= kNarrow64) blocks = std::min(blocks, each * kb + gf::fp8_join_blocks(static_cast<int>(tile_rows), dual));
+  const double whole = std::ceil(each);
+  if (kernel <= kNarrow64 && 100 * each < gf::fp8_whole_fill(whole > 1 ? 2 : 1) * whole)
+    blocks = std::min(blocks, each * kb +
+                                  gf::fp8_join_blocks(static_cast<int>(tile_rows), dual));
   const Pace& c = kPace[dual][kernel - 1];
   return c.start + c.block * blocks + c.round * rounds;
 }
