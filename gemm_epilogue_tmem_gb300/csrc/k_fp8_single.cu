@@ -51,8 +51,8 @@ constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kStaging = kEpiWarps * 32 * kPad;
 constexpr int kSlot = TR + 4;      // floats of a ring slot: rows, two column blocks
 constexpr int kTable = 2 * (kFp8MaxGroups + 2) * 4;
-constexpr int kFixed = kSmemAlignSlack + kSmemCtrlBytes + kStaging + kRing * kScaleGroup * kSlot * 4 +
-                       2 * TR * 4 + kTable;
+constexpr int kFixed = kSmemAlignSlack + kSmemCtrlBytes + kStaging +
+                       kRing * kScaleGroup * kSlot * 4 + 2 * TR * 4 + kTable;
 constexpr int S = (kSmemPerCta - kFixed) / kStageBytes;
 constexpr int kSmemSingle = kFixed + S * kStageBytes;
 static_assert(S >= 3, "shared memory budget");

@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(32 * kAnyWarps, 7)
 #pragma unroll
         for (int j = 0; j < KS; ++j)
           if (row[j] >= 0 && col < H + 8)
-            w[j] = word_at(rows, 2 * (static_cast<int64_t>(row[j]) * H + col) & ~int64_t(15), total);
+            w[j] = word_at(rows, 2 * (static_cast<int64_t>(row[j]) * H + col) & ~int64_t(15),
+                           total);
       }
       __syncwarp();
 #pragma unroll

@@ -326,10 +326,10 @@ typedef enum gf_fp8_epilog {
  * k % 16 == 0 (16-byte rows for the tensor maps), n % 8 == 0, or n % 16 == 0
  * for SWIGLU_QUANT, and m, groups * n up to 2^31 - 513, at most 2^30 tiles of 16 x
  * 128, else GF_ERR_UNSUPPORTED. dtype: the element type of out
- * (NONE). Options: GF_OPT_KERNEL (0 the plan's choice by the average number of
- * rows a group and the number of tiles; 1 and 2 the kernel for few rows with
- * tiles of 16 and 64 rows; 3 the single-CTA kernel with tiles of 128; 4 the
- * CTA-pair kernel with tiles of 256), GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US,
+ * (NONE). Options: GF_OPT_KERNEL (0 the plan's choice, the one that takes the least
+ * time by a model of the four for groups of about alike numbers of rows; 1 and 2
+ * the kernel for few rows with tiles of 16 and 64 rows; 3 the single-CTA kernel
+ * with tiles of 128; 4 the CTA-pair kernel with tiles of 256), GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US,
  * GF_OPT_FAULT_DROP_LOAD; others give GF_ERR_UNSUPPORTED.
  */
 GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t groups,
