@@ -58,9 +58,8 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   prm.x = x;
   prm.rows = rows;
   prm.scale = scale;
-  // CTAs that share a chunk's copies: as many as have work for their 16 warps
-  // (512 elements of a row at a time), while the grid has fewer than two CTAs
-  // per SM
+  // CTAs that share a chunk's copies: one per 16 pieces of 512 elements of a
+  // row, while the grid has fewer than two CTAs per SM
   const int64_t items = p->chunk_tokens * ((p->k + 511) / 512);
   int64_t seg = (items + 15) / 16;
   const int64_t room = 2 * p->num_sms / p->num_chunks;
