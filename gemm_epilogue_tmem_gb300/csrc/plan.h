@@ -68,7 +68,7 @@ struct gf_plan {
   int64_t topk, experts;
   int chunk_tokens;      // tokens per CTA of the sort
   int num_chunks;
-  int fused;             // few slots: the sort kernel copies the rows too
+  int fused;             // little to copy: the sort kernel does that too
   void* d_work;          // e4m3 products: counters and partial sums of split tiles
   size_t work_bytes;
 };

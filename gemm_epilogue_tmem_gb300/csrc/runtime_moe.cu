@@ -23,10 +23,26 @@ bool given_scale(const void* p) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 }
 
-// Slots up to which every CTA of the sort counts all of them alone and copies
-// its tokens' rows too; above, clusters of CTAs share the counting, and the
-// copies have a kernel of their own (whose CTAs the hardware balances).
-constexpr int64_t kFusedSlots = 4096;
+// Up to these sizes one kernel sorts and copies: every CTA counts all slots alone
+// and copies its own tokens' rows. Above, the copies have a kernel of their own,
+// whose CTAs the hardware balances. us, one kernel and two (16-bit rows; e4m3):
+//   1024 tokens, 8 slots, 1024 columns    7.1  16.5     6.2  12.4
+//   4096, 8, 1024                        18.6  24.6    14.3  15.7
+//   2048, 8, 2048                        17.5  23.9    12.8  15.1
+//   4096, 8, 2048                        32.7  30.1    22.2  19.7
+//   2048, 8, 4096                        31.4  30.0    20.9  19.4
+//   4096, 8, 64                           7.7  11.1     9.1  14.4
+//   16384, 8, 64                         21.7  17.5    25.7  22.0
+constexpr int64_t kFusedSlots = 49152, kFusedElements = 40 << 20;
+
+// Whether clusters of CTAs share the counting of a sort without copies in it: us,
+// each CTA alone and clusters, 32768 slots of 128 experts 6.4 and 8.0, 65536 9.9
+// and 9.5, 65536 of 1024 experts 10.4 and 16.9; with the copies after it (2048
+// tokens, 8 slots, 4096 columns 28.6 and 30.0; 4096 tokens 54.7 and 53.3) from
+// fewer slots on.
+bool clusters_count(int64_t slots, int64_t experts, bool copies) {
+  return slots > (copies ? 16384 : 49152 + 64 * experts);
+}
 
 bool is_moe(const gf_plan* p) { return p != nullptr && p->epi == gf::EPI_MOE; }
 
@@ -49,7 +65,8 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   prm.slots = static_cast<int32_t>(p->m * p->topk);
   prm.chunk_tokens = p->chunk_tokens;
   prm.num_chunks = p->num_chunks;
-  prm.clusters = p->fused ? 0 : 1;
+  const bool copies = copy != gf::MOE_SORT_ONLY;
+  prm.clusters = !(copies && p->fused) && clusters_count(prm.slots, p->experts, copies) ? 1 : 0;
   prm.fused = p->fused;
   prm.expert = expert;
   prm.offsets = offsets;
@@ -59,10 +76,10 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   prm.rows = rows;
   prm.scale = scale;
   // CTAs that share a chunk's copies: one per 16 pieces of 512 elements of a
-  // row, while the grid has fewer than two CTAs per SM
+  // row, as far as there are SMs for them (an SM holds one)
   const int64_t items = p->chunk_tokens * ((p->k + 511) / 512);
   int64_t seg = (items + 15) / 16;
-  const int64_t room = 2 * p->num_sms / p->num_chunks;
+  const int64_t room = p->num_sms / p->num_chunks;
   seg = seg > room ? room : seg;
   prm.segments = static_cast<int32_t>(seg < 1 ? 1 : seg);
   const int bf16 = p->dtype == GF_BF16 ? 1 : 0;
@@ -118,7 +135,8 @@ GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64
   p->experts = experts;
   p->chunk_tokens = static_cast<int>(chunk);
   p->num_chunks = static_cast<int>(chunks);
-  p->fused = tokens * topk <= kFusedSlots ? 1 : 0;
+  p->fused =
+      tokens * topk <= kFusedSlots && tokens * topk * hidden <= kFusedElements ? 1 : 0;
   p->grid = static_cast<int>(chunks);
   return p;
 }

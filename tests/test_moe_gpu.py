@@ -91,7 +91,8 @@ def test_dispatch(tokens, topk, experts, hidden, dtype, drop):
     want = torch.zeros_like(rows)
     want[:kept] = x[dev(slot_of[:kept] // topk)]
     assert torch.equal(rows, want)
-    assert gf.gf_plan_describe(plan)["launches"] == (1 if slots <= 4096 else 2)
+    fused = slots <= 49152 and slots * hidden <= 40 << 20
+    assert gf.gf_plan_describe(plan)["launches"] == (1 if fused else 2)
     plan.free()
 
 
@@ -403,3 +404,27 @@ def test_wide_odd_rows(tokens, topk, experts, hidden, dtype, drop):
 def test_dispatch_of_many_wide_rows(tokens, topk, experts, hidden):
     """The sort in a launch of its own before the copies of rows longer than one piece."""
     test_dispatch(tokens, topk, experts, hidden, gf.GF_BF16, 0.1)
+
+
+@pytest.mark.parametrize("tokens,topk,experts,hidden", [
+    (50001, 1, 600, 8), (12500, 4, 130, 16), (6300, 8, 1024, 24), (52000, 1, 3, 7), (2600, 8, 60, 2047), (700, 8, 64, 7504),
+    (16400, 1, 5, 2563)])
+def test_dispatch_in_two_launches(tokens, topk, experts, hidden):
+    """More slots, or more to copy, than one launch does: counted by clusters, or by each CTA."""
+    test_dispatch(tokens, topk, experts, hidden, gf.GF_BF16, 0.1)
+    if hidden % 16 == 0:
+        test_dispatch_fp8(tokens, topk, experts, hidden, gf.GF_F16, 0.1)
+
+
+@pytest.mark.parametrize("tokens,topk,experts", [(1, 1, 1), (700, 8, 64), (9000, 6, 1024), (12300, 8, 70), (33000, 4, 1024)])
+def test_sort_alone(tokens, topk, experts):
+    """The indexes without any copies, counted by each CTA and by clusters."""
+    e = routing(tokens, topk, experts, 91, 0.1)
+    offsets, row_of, slot_of = sort_reference(e, experts)
+    kept = int(offsets[-1])
+    plan = gf.gf_moe_plan(tokens, topk, experts, 64, gf.GF_F16)
+    o, r, s = int_out(experts + 1), int_out(tokens, topk), int_out(tokens * topk)
+    gf.gf_moe_dispatch_execute(plan, dev(e), None, o, r, s, None)
+    assert np.array_equal(o.cpu().numpy(), offsets) and np.array_equal(r.cpu().numpy(), row_of)
+    assert np.array_equal(s.cpu().numpy()[:kept], slot_of[:kept])
+    plan.free()
