@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   int32_t* rank = mine + p.experts;                     // [kRankWarps][experts]
   int32_t* place = rank + kRankWarps * p.experts;       // [chunk slots]
   __shared__ int32_t warp_sum[kSortThreads / 32];
-  static_assert(kSortThreads >= 1024, "a thread per expert");
+  static_assert(kSortThreads >= kMaxExperts, "a thread per expert");
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t lane = lane_id();
   const int experts = p.experts;
@@ -917,11 +917,14 @@ cudaError_t dispatch_t(const MoeParams& p, int copy, cudaStream_t stream, int pd
                   fused == MOE_SORT_ONLY ? 1 : p.segments, 1);
   const size_t smem =
       ((3 + kRankWarps) * static_cast<size_t>(p.experts) + p.chunk_tokens * p.topk) * 4;
+  // Without asking, a kernel has 48 KB, its static arrays among them (below 1 KB
+  // here). The limit is the kernel's, not the launch's: always raised to the most
+  // that any plan takes, so that no call lowers it between another's two steps.
+  constexpr int kMostSmem = ((3 + kRankWarps) * kMaxExperts + kMaxChunkSlots) * 4;
   auto sort = [&](auto kernel) -> cudaError_t {
-    if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
+    if (smem > 47 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
       if (e != cudaSuccess) return e;
     }
     return launch_clusters(kernel, grid, cluster, kSortThreads, smem, stream, pdl, p);

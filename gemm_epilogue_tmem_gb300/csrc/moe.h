@@ -6,6 +6,8 @@
 
 namespace gf {
 
+constexpr int kMaxExperts = 1024;
+
 struct MoeParams {
   int32_t tokens, topk, experts;
   int32_t hidden;

@@ -109,9 +109,9 @@ extern "C" {
 
 GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64_t hidden,
                             gf_dtype dtype) {
-  if (tokens < 0 || tokens > kMaxDim || topk < 1 || topk > 64 || experts < 1 || experts > 1024 ||
-      hidden < 1 || hidden > kMaxHidden || tokens * topk > kMaxDim ||
-      (dtype != GF_F16 && dtype != GF_BF16)) {
+  if (tokens < 0 || tokens > kMaxDim || topk < 1 || topk > 64 || experts < 1 ||
+      experts > gf::kMaxExperts || hidden < 1 || hidden > kMaxHidden ||
+      tokens * topk > kMaxDim || (dtype != GF_F16 && dtype != GF_BF16)) {
     runtime_fail(GF_ERR_INVALID_VALUE);
     return nullptr;
   }
