@@ -196,10 +196,7 @@ GF_API gf_status gf_noalloc_status(struct CUstream_st* stream) {
     return fail(GF_ERR_CUDA);
   }
   if (word != 0) {
-    if (cudaMemset(scratch, 0, sizeof word) != cudaSuccess) {
-      cudaGetLastError();
-      return fail(GF_ERR_CUDA);
-    }
+    if (gf::runtime_zero(scratch, sizeof word) != GF_OK) return fail(GF_ERR_CUDA);
     return fail(GF_ERR_DEVICE_TIMEOUT);
   }
   return GF_OK;

@@ -326,8 +326,7 @@ gf_status ensure_splitk(gf_plan* p) {
   }
   if (st == GF_OK) {
     p->splitk_cnt_offset = ws;
-    if (cudaMemset(static_cast<char*>(p->d_splitk) + ws, 0, parts * 4) != cudaSuccess)
-      st = GF_ERR_CUDA;
+    st = gf::runtime_zero(static_cast<char*>(p->d_splitk) + ws, parts * 4);
   }
   if (st != GF_OK) {
     cudaGetLastError();
@@ -446,7 +445,7 @@ gf_plan* plan_create(int64_t m, int64_t n, int64_t k, gf_dtype dtype, int epi,
     fail(GF_ERR_OUT_OF_MEMORY);
     return nullptr;
   }
-  if (cudaMemset(p->d_status, 0, 256) != cudaSuccess) {
+  if (gf::runtime_zero(p->d_status, 256) != GF_OK) {
     cudaFree(p->d_status);
     delete p;
     fail(GF_ERR_CUDA);
@@ -688,6 +687,19 @@ CUcontext runtime_current_context() {
 
 gf_status runtime_fail(gf_status s) { return fail(s); }
 
+gf_status runtime_zero(void* ptr, size_t bytes) {
+  cudaStream_t own;
+  if (cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) != cudaSuccess) {
+    cudaGetLastError();
+    return GF_ERR_CUDA;
+  }
+  const bool ok = cudaMemsetAsync(ptr, 0, bytes, own) == cudaSuccess &&
+                  cudaStreamSynchronize(own) == cudaSuccess;
+  cudaStreamDestroy(own);
+  if (!ok) cudaGetLastError();
+  return ok ? GF_OK : GF_ERR_CUDA;
+}
+
 bool runtime_encode_2d(CUtensorMap* map, const void* ptr, gf_dtype dt, uint64_t inner,
                        uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
   load_driver_entry_points();
@@ -753,8 +765,8 @@ gf_plan* runtime_new_plan(int epi, gf_dtype dtype) {
   gf_status got = GF_OK;
   if (cudaMalloc(&p->d_status, 256) != cudaSuccess)
     got = GF_ERR_OUT_OF_MEMORY;
-  else if (cudaMemset(p->d_status, 0, 256) != cudaSuccess)
-    got = GF_ERR_CUDA;
+  else
+    got = runtime_zero(p->d_status, 256);
   if (got != GF_OK) {
     cudaGetLastError();
     gf_plan_free(p);
@@ -1034,9 +1046,11 @@ GF_API gf_status gf_plan_status(const gf_plan* p, struct CUstream_st* stream) {
     // which waits gave up: 1 producer, 2 MMA on a stage, 4 MMA on an
     // accumulator buffer, 8 epilogue, 16 teardown drain
     if (getenv("GF_DEBUG")) fprintf(stderr, "gf: device status word 0x%x\n", word);
+    // nothing of the plan may be running while its words are set back
+    if (cudaDeviceSynchronize() != cudaSuccess) return fail(GF_ERR_CUDA);
     // the status word, and the dynamic schedule's tile counters that a launch
     // which gave up may leave part-way
-    if (cudaMemset(p->d_status, 0, 256) != cudaSuccess) return fail(GF_ERR_CUDA);
+    if (gf::runtime_zero(p->d_status, 256) != GF_OK) return fail(GF_ERR_CUDA);
     if (gf::epi_fp8(p->epi) &&
         gf::runtime_fp8_clear_counters(const_cast<gf_plan*>(p)) != GF_OK)
       return fail(GF_ERR_CUDA);
@@ -1044,8 +1058,8 @@ GF_API gf_status gf_plan_status(const gf_plan* p, struct CUstream_st* stream) {
     const size_t counters = p->pair ? 2 * static_cast<size_t>(p->num_tiles - p->split_from)
                                     : static_cast<size_t>(p->num_tiles);
     if (p->k_splits > 1 &&
-        cudaMemset(static_cast<char*>(p->d_splitk) + p->splitk_cnt_offset, 0, counters * 4) !=
-            cudaSuccess)
+        gf::runtime_zero(static_cast<char*>(p->d_splitk) + p->splitk_cnt_offset, counters * 4) !=
+            GF_OK)
       return fail(GF_ERR_CUDA);
     return fail(GF_ERR_DEVICE_TIMEOUT);
   }

@@ -96,12 +96,14 @@ void plan_tiles(gf_plan* p) {
 }
 
 // The workspace of the plan's tiling: the narrow kernel's counters (zeroed),
-// then its partial sums. Grown when too small.
+// then its partial sums. Grown when too small; one that the plan has already
+// had may be in use, by launches that have to end first.
 size_t counter_bytes(const gf_plan* p) { return (static_cast<size_t>(p->grid) * 4 + 255) / 256 * 256; }
 
 gf_status ensure_work(gf_plan* p) {
   if (p->kernel > kNarrow64) return GF_OK;
   const int dual = p->epi == gf::EPI_FP8_SWIGLU_QUANT ? 1 : 0;
+  if (p->d_work && cudaDeviceSynchronize() != cudaSuccess) return GF_ERR_CUDA;
   const size_t need =
       counter_bytes(p) + gf::fp8_narrow_partial_bytes(p->tile_rows, dual, p->grid);
   if (need > p->work_bytes) {
@@ -114,7 +116,7 @@ gf_status ensure_work(gf_plan* p) {
     p->d_work = grown;
     p->work_bytes = need;
   }
-  return cudaMemset(p->d_work, 0, counter_bytes(p)) == cudaSuccess ? GF_OK : GF_ERR_CUDA;
+  return gf::runtime_zero(p->d_work, counter_bytes(p));
 }
 
 }  // namespace
@@ -138,7 +140,7 @@ gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value) {
 
 gf_status runtime_fp8_clear_counters(gf_plan* p) {
   if (p->kernel > kNarrow64) return GF_OK;
-  return cudaMemset(p->d_work, 0, counter_bytes(p)) == cudaSuccess ? GF_OK : GF_ERR_CUDA;
+  return gf::runtime_zero(p->d_work, counter_bytes(p));
 }
 
 }  // namespace gf

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "gf.h"
@@ -17,6 +18,11 @@ CUcontext runtime_current_context();
 
 // Records `s` as the calling thread's last error (gf_last_error) and returns it.
 gf_status runtime_fail(gf_status s);
+
+// Zeroes device memory and returns once that is done. A memset on the default
+// stream would still be to come when the caller goes on, and a launch on a
+// non-blocking stream does not wait for it.
+gf_status runtime_zero(void* ptr, size_t bytes);
 
 // 2-D TMA map over a row-major [outer, inner] matrix of 16-bit elements with
 // box_inner x box_outer boxes, 128-byte swizzle, zero fill out of bounds.
