@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kRankWarps = 8;        // warps that rank the slots of a chunk
-constexpr int kMaxChunkSlots = 4096;
 constexpr uint32_t kSortCluster = 8;
 
 template <typename K, typename... A>
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   int32_t* before = total + p.experts;                  // [experts]
   int32_t* mine = before + p.experts;                   // [experts], of this chunk
   int32_t* rank = mine + p.experts;                     // [kRankWarps][experts]
-  int32_t* place = rank + kRankWarps * p.experts;       // [chunk slots]
+  int32_t* place = rank + kRankWarps * p.experts;       // [chunk slots] (with copies)
   __shared__ int32_t warp_sum[kSortThreads / 32];
   static_assert(kSortThreads >= kMaxExperts, "a thread per expert");
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
         rank[warp * experts + e] += __popc(same);
       __syncwarp();
       if (i < n) {
-        place[i] = row;
+        if constexpr (COPY != MOE_SORT_ONLY) place[i] = row;
         if (writer) {
           p.row_of[first + i] = row;
           if (row >= 0) p.slot_of[row] = first + i;
@@ -915,12 +914,12 @@ cudaError_t dispatch_t(const MoeParams& p, int copy, cudaStream_t stream, int pd
   const unsigned cluster = p.clusters ? kSortCluster : 1;
   const dim3 grid((p.num_chunks + cluster - 1) / cluster * cluster,
                   fused == MOE_SORT_ONLY ? 1 : p.segments, 1);
-  const size_t smem =
-      ((3 + kRankWarps) * static_cast<size_t>(p.experts) + p.chunk_tokens * p.topk) * 4;
+  const size_t places = fused == MOE_SORT_ONLY ? 0 : size_t(p.chunk_tokens) * p.topk;
+  const size_t smem = ((3 + kRankWarps) * static_cast<size_t>(p.experts) + places) * 4;
   // Without asking, a kernel has 48 KB, its static arrays among them (below 1 KB
   // here). The limit is the kernel's, not the launch's: always raised to the most
   // that any plan takes, so that no call lowers it between another's two steps.
-  constexpr int kMostSmem = ((3 + kRankWarps) * kMaxExperts + kMaxChunkSlots) * 4;
+  constexpr int kMostSmem = ((3 + kRankWarps) * kMaxExperts + kMoeChunkSlots) * 4;
   auto sort = [&](auto kernel) -> cudaError_t {
     if (smem > 47 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(
@@ -1000,8 +999,6 @@ cudaError_t grad_t(const GatherParams& p, cudaStream_t stream, int pdl) {
 }
 
 }  // namespace
-
-int moe_max_chunk_slots() { return kMaxChunkSlots; }
 
 cudaError_t launch_moe_dispatch(const MoeParams& p, int copy, int bf16, cudaStream_t stream,
                                 int pdl) {

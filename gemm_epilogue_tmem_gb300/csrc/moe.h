@@ -7,6 +7,9 @@
 namespace gf {
 
 constexpr int kMaxExperts = 1024;
+// most slots of a chunk that is sorted and copied in one launch: their rows are held
+// in shared memory
+constexpr int kMoeChunkSlots = 4096;
 
 struct MoeParams {
   int32_t tokens, topk, experts;
@@ -28,8 +31,6 @@ struct MoeParams {
 
 enum MoeCopy : int { MOE_SORT_ONLY = 0, MOE_COPY = 1, MOE_COPY_FP8 = 2 };
 
-// most tokens of a chunk: its slots' rows are held in shared memory
-int moe_max_chunk_slots();
 cudaError_t launch_moe_dispatch(const MoeParams& p, int copy, int bf16, cudaStream_t stream,
                                 int pdl);
 

@@ -44,6 +44,20 @@ bool clusters_count(int64_t slots, int64_t experts, bool copies) {
   return slots > (copies ? 16384 : 49152 + 64 * experts);
 }
 
+// Tokens of a chunk. One chunk per SM; smaller ones of kMoeChunkSlots slots where those
+// are at most two an SM, of which one ranks its slots while the other still counts.
+// More must not be: every CTA, or every cluster of them, counts all slots, and the
+// sort would be quadratic. us, chunks of 4096 slots and one per SM: 800000 slots of
+// 128 experts 32.7 and 36.4, 1 Mi 37.6 and 45.1, 1600000 76 and 65, 8 Mi of 256
+// experts 1169 and 325. Where the copies are in the same launch the kernel's table
+// holds kMoeChunkSlots rows.
+int64_t chunk_of(int64_t tokens, int64_t topk, int sms, bool fused) {
+  const int64_t per_sm = (tokens + sms - 1) / sms, small = gf::kMoeChunkSlots / topk;
+  const bool few = fused || (tokens + small - 1) / small <= 2 * sms;
+  const int64_t chunk = few && small < per_sm ? small : per_sm;
+  return chunk < 1 ? 1 : chunk;
+}
+
 bool is_moe(const gf_plan* p) { return p != nullptr && p->epi == gf::EPI_MOE; }
 
 gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32_t* offsets,
@@ -121,10 +135,8 @@ GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64
     runtime_fail(st);
     return nullptr;
   }
-  // one chunk of tokens per SM, as far as its slots fit the kernel's table
-  int64_t chunk = (tokens + sms - 1) / sms;
-  const int64_t most = gf::moe_max_chunk_slots() / topk;
-  chunk = chunk > most ? most : chunk < 1 ? 1 : chunk;
+  const int fused = tokens * topk <= kFusedSlots && tokens * topk * hidden <= kFusedElements ? 1 : 0;
+  const int64_t chunk = chunk_of(tokens, topk, sms, fused != 0);
   const int64_t chunks = tokens == 0 ? 1 : (tokens + chunk - 1) / chunk;
   gf_plan* p = gf::runtime_new_plan(gf::EPI_MOE, dtype);
   if (!p) return nullptr;
@@ -135,8 +147,7 @@ GF_API gf_plan* gf_moe_plan(int64_t tokens, int64_t topk, int64_t experts, int64
   p->experts = experts;
   p->chunk_tokens = static_cast<int>(chunk);
   p->num_chunks = static_cast<int>(chunks);
-  p->fused =
-      tokens * topk <= kFusedSlots && tokens * topk * hidden <= kFusedElements ? 1 : 0;
+  p->fused = fused;
   p->grid = static_cast<int>(chunks);
   return p;
 }

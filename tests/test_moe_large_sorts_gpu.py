@@ -14,38 +14,49 @@ import gemm_epilogue_tmem_gb300 as gf  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
-IN_A_PROCESS_OF_ITS_OWN = """
-import sys
-import torch
-import gemm_epilogue_tmem_gb300 as gf
-tokens, topk, experts, hidden, copies = (int(a) for a in sys.argv[1:])
-expert = torch.randint(-1, experts, (tokens, topk), dtype=torch.int32, device="cuda")
-flat = expert.flatten().long()
-kept = int((flat >= 0).sum())
-order = torch.argsort(torch.where(flat < 0, experts, flat), stable=True)[:kept]
-i32 = dict(dtype=torch.int32, device="cuda")
-offsets, row_of, slot_of = torch.empty(experts + 1, **i32), torch.empty(tokens, topk, **i32), torch.empty(tokens * topk, **i32)
-x = torch.randn(tokens, hidden, device="cuda").half() if copies else None
-rows = torch.empty(tokens * topk, hidden, dtype=torch.half, device="cuda") if copies else None
-plan = gf.gf_moe_plan(tokens, topk, experts, hidden, gf.GF_F16)
-gf.gf_moe_dispatch_execute(plan, expert, x, offsets, row_of, slot_of, rows)
-assert gf.gf_plan_status(plan) == gf.GF_OK
-assert torch.equal(slot_of[:kept].long(), order) and bool((slot_of[kept:] == -1).all())
-want = torch.full_like(flat, -1)
-want[order] = torch.arange(kept, device="cuda")
-assert torch.equal(row_of.flatten().long(), want)
-assert torch.equal(offsets[1:].long(), torch.cumsum(torch.bincount(flat[flat >= 0], minlength=experts), 0))
-if copies:
-    assert torch.equal(rows[:kept], x[order // topk]) and not bool(rows[kept:].any())
-print("right")
-"""
+
+def check_dispatch(tokens, topk, experts, hidden, copies):
+    """The indexes, and the rows where `copies`, against torch's stable sort; some slots are dropped."""
+    expert = torch.randint(-1, experts, (tokens, topk), dtype=torch.int32, device="cuda")
+    flat = expert.flatten().long()
+    kept = int((flat >= 0).sum())
+    order = torch.argsort(torch.where(flat < 0, experts, flat), stable=True)[:kept]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    offsets, row_of, slot_of = torch.empty(experts + 1, **i32), torch.empty(tokens, topk, **i32), torch.empty(tokens * topk, **i32)
+    x = torch.randn(tokens, hidden, device="cuda").half() if copies else None
+    rows = torch.empty(tokens * topk, hidden, dtype=torch.half, device="cuda") if copies else None
+    plan = gf.gf_moe_plan(tokens, topk, experts, hidden, gf.GF_F16)
+    gf.gf_moe_dispatch_execute(plan, expert, x, offsets, row_of, slot_of, rows)
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    assert torch.equal(slot_of[:kept].long(), order) and bool((slot_of[kept:] == -1).all())
+    want = torch.full_like(flat, -1)
+    want[order] = torch.arange(kept, device="cuda")
+    assert torch.equal(row_of.flatten().long(), want)
+    assert int(offsets[0]) == 0
+    assert torch.equal(offsets[1:].long(), torch.cumsum(torch.bincount(flat[flat >= 0], minlength=experts), 0))
+    if copies:
+        assert torch.equal(rows[:kept], x[order // topk]) and not bool(rows[kept:].any())
+    described = gf.gf_plan_describe(plan)
+    plan.free()
+    return described
 
 
 @pytest.mark.parametrize("tokens,topk,experts,hidden,copies", [
     (19000, 8, 1024, 8, 0), (18900, 8, 1024, 16, 1), (48032, 4, 1002, 8, 0), (361700, 1, 900, 8, 1), (24320, 8, 1000, 8, 0)])
 def test_first_call_of_a_process(tokens, topk, experts, hidden, copies):
-    """Tables of a few bytes less than 48 KB: with what the kernel holds besides they need the larger limit, which no
-    earlier call has asked for."""
-    r = subprocess.run([sys.executable, "-c", IN_A_PROCESS_OF_ITS_OWN, *map(str, (tokens, topk, experts, hidden, copies))],
-                       cwd=ROOT, capture_output=True, text=True, timeout=300)
+    """Tables of a few bytes less than 48 KB, with the rows of a chunk's slots among them: with what the kernel holds
+    besides they need the larger limit, which no earlier call has asked for."""
+    call = f"import test_moe_large_sorts_gpu as t; t.check_dispatch({tokens}, {topk}, {experts}, {hidden}, {copies}); print('right')"
+    path = os.pathsep.join([ROOT, os.path.join(ROOT, "tests"), os.environ.get("PYTHONPATH", "")])
+    r = subprocess.run([sys.executable, "-c", call], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": path})
     assert r.returncode == 0 and r.stdout.strip() == "right", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("tokens,topk,experts,hidden,copies", [
+    (700001, 1, 1024, 8, 1), (1300001, 1, 3, 8, 0), (1300001, 1, 1024, 8, 1), (80000, 17, 60, 8, 1), (22000, 64, 70, 16, 0),
+    (1 << 20, 8, 256, 8, 0)])
+def test_chunks_do_not_grow_in_number(tokens, topk, experts, hidden, copies):
+    """However many slots: every CTA or cluster counts them all, so that their number must not grow with the slots."""
+    described = check_dispatch(tokens, topk, experts, hidden, copies)
+    assert described["grid"] <= 2 * torch.cuda.get_device_properties(0).multi_processor_count
