@@ -509,8 +509,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   }
   // rows without a slot
   if (writer)
-    for (int r = kept + blockIdx.x * kSortThreads + tid; r < p.slots;
-         r += gridDim.x * kSortThreads)
+    for (int64_t r = kept + static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; r < p.slots;
+         r += static_cast<int64_t>(gridDim.x) * kSortThreads)  // passes 2^31 with many slots
       p.slot_of[r] = -1;
   if (p.clusters) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   if constexpr (COPY == MOE_SORT_ONLY) return;

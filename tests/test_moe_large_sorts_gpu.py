@@ -60,3 +60,32 @@ def test_chunks_do_not_grow_in_number(tokens, topk, experts, hidden, copies):
     """However many slots: every CTA or cluster counts them all, so that their number must not grow with the slots."""
     described = check_dispatch(tokens, topk, experts, hidden, copies)
     assert described["grid"] <= 2 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("experts,period", [(3, 3), (3, 4), (5, 64)])
+def test_most_slots(experts, period):
+    """2^31 - 1 slots, none dropped, a quarter and nearly all: indexes that pass 32 bits with the threads' stride. Slot i
+    has expert i % period. The array before slot_of, as far as a negative 32-bit index reaches, stays as it is."""
+    slots = 2 ** 31 - 1
+    expert = torch.arange(slots, dtype=torch.int32, device="cuda").remainder_(period)
+    offsets = torch.full((experts + 1,), 77, dtype=torch.int32, device="cuda")
+    row_of = torch.full((slots,), 77, dtype=torch.int32, device="cuda")
+    flat = torch.full((2 ** 31 + slots,), 77, dtype=torch.int32, device="cuda")
+    slot_of = flat[2 ** 31:]
+    plan = gf.gf_moe_plan(slots, 1, experts, 8, gf.GF_F16)
+    gf.gf_moe_dispatch_execute(plan, expert, None, offsets, row_of, slot_of, None)
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    plan.free()
+    del expert
+    counts = [(slots - e + period - 1) // period for e in range(experts)]
+    starts = [sum(counts[:e]) for e in range(experts + 1)]
+    assert offsets.tolist() == starts
+    for e in range(period):
+        if e < experts:
+            rows = torch.arange(starts[e], starts[e + 1], dtype=torch.int32, device="cuda")
+            assert torch.equal(row_of[e::period], rows)
+            assert torch.equal(slot_of[starts[e]:starts[e + 1]], rows.sub_(starts[e]).mul_(period).add_(e))
+        else:
+            assert bool((row_of[e::period] == -1).all())
+    assert bool((slot_of[starts[-1]:] == -1).all())
+    assert bool((flat[:2 ** 31] == 77).all())
