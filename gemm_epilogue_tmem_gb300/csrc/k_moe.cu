@@ -12,6 +12,10 @@
 // element), and what they need of another row is shifted out of the two
 // aligned words that hold it (5003 tokens, 6 slots, 2047 columns of fp16: the
 // gradient of dispatch took 87 us with 2-byte accesses).
+//
+// The kernels begin while the one before them, which may write what they read,
+// still runs. So no load goes through the read-only path (__ldg, or const and
+// __restrict__ pointers), which is for data that nobody writes while a kernel lives.
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -69,6 +73,18 @@ __device__ __forceinline__ int ld_cluster(uint32_t cluster_addr) {
 }
 
 // --------------------------------------------------------- rows of any length
+// A coherent load that the compiler may move over stores, which go to other arrays
+// (a plain one stays behind them: gradient of combine, 5003 tokens, 6 slots, 2047
+// columns, 57 us, with this one 54.5). Not over grid_dep_wait as long as the address
+// depends on an index that was loaded after it, as the row of a slot does.
+__device__ __forceinline__ uint4 load_early(const uint4* p) {
+  uint4 v;
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p));
+  return v;
+}
+
 // The aligned 16-byte word at byte `at` of an array of `total` bytes; bytes
 // outside it are zero and are not read.
 __device__ __forceinline__ uint4 word_at(const uint8_t* array, int64_t at, int64_t total) {
@@ -247,8 +263,8 @@ __device__ __forceinline__ void copy_item(const MoeParams& p, int token, int par
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (col0 + 256 * u >= H) continue;
-          a[u] = __ldg(src + 32 * u);
-          b[u] = __ldg(src + 32 * u + 1);
+          a[u] = load_early(src + 32 * u);
+          b[u] = load_early(src + 32 * u + 1);
         }
       } else {
 #pragma unroll
@@ -767,7 +783,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas(KS))
           if (inside) {
             const uint32_t shift = static_cast<uint32_t>(at) & 15u;
             const uint4* src = reinterpret_cast<const uint4*>(d_out + at - shift);
-            d = shift_out(__ldg(src), __ldg(src + 1), shift);
+            d = shift_out(load_early(src), load_early(src + 1), shift);
           } else {
             d = bytes_at(d_out, at, total);
           }
