@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_dispatch_kernel(const MoePar
   const int parts = copy_parts<COPY, ANY>(p.hidden);
   const int64_t items = static_cast<int64_t>(n / p.topk) * parts;
   constexpr int kWarps = kSortThreads / 32;
-  for (int64_t it = static_cast<int64_t>(blockIdx.y) * kWarps + warp; it < items;
+  // (the first pieces to every one of the chunk's CTAs, then the next)
+  for (int64_t it = static_cast<int64_t>(warp) * gridDim.y + blockIdx.y; it < items;
        it += static_cast<int64_t>(gridDim.y) * kWarps) {
     const int t = static_cast<int>(it / parts);
     const int part = static_cast<int>(it - static_cast<int64_t>(t) * parts);

@@ -89,8 +89,9 @@ gf_status dispatch(const gf_plan* p, const int32_t* expert, const void* x, int32
   prm.x = x;
   prm.rows = rows;
   prm.scale = scale;
-  // CTAs that share a chunk's copies: one per 16 pieces of 512 elements of a
-  // row, as far as there are SMs for them (an SM holds one)
+  // CTAs that share a chunk's copies: one per 8 Ki elements of its rows, as far as
+  // there are SMs for them (an SM holds one). One token, 8 slots, 16384 columns 6.2
+  // us, with one CTA 8.3; 65536 columns 6.3 and 20.6
   const int64_t items = p->chunk_tokens * ((p->k + 511) / 512);
   int64_t seg = (items + 15) / 16;
   const int64_t room = p->num_sms / p->num_chunks;

@@ -1,4 +1,4 @@
-"""The sort of expert routing at the sizes where its launch or its indexes change."""
+"""Expert routing at the sizes where the sort's launch or its indexes change."""
 import os
 import subprocess
 import sys
@@ -11,6 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import gemm_epilogue_tmem_gb300 as gf  # noqa: E402
+import test_moe_gpu as moe  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -89,3 +90,13 @@ def test_most_slots(experts, period):
             assert bool((row_of[e::period] == -1).all())
     assert bool((slot_of[starts[-1]:] == -1).all())
     assert bool((flat[:2 ** 31] == 77).all())
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 7, 20, 76])
+@pytest.mark.parametrize("hidden", [9216, 16400, 16383, 32784, 33001, 65536])
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+def test_long_rows_of_few_tokens(tokens, hidden, drop):
+    """Several CTAs share the copies of a token's row, and what is cleared behind the last."""
+    moe.test_dispatch(tokens, 3, 9, hidden, gf.GF_BF16, drop)
+    if hidden % 16 == 0:
+        moe.test_dispatch_fp8(tokens, 3, 9, hidden, gf.GF_F16, drop)
