@@ -35,13 +35,18 @@ bool given_scale(const void* p) {
 //   16384, 8, 64                         21.7  17.5    25.7  22.0
 constexpr int64_t kFusedSlots = 49152, kFusedElements = 40 << 20;
 
-// Whether clusters of CTAs share the counting of a sort without copies in it: us,
-// each CTA alone and clusters, 32768 slots of 128 experts 6.4 and 8.0, 65536 9.9
-// and 9.5, 65536 of 1024 experts 10.4 and 16.9; with the copies after it (2048
-// tokens, 8 slots, 4096 columns 28.6 and 30.0; 4096 tokens 54.7 and 53.3) from
-// fewer slots on.
+// Whether clusters of CTAs share the counting of a sort without copies in it, which
+// is worth the more the more slots there are, and the less the more experts. us, each
+// CTA alone and clusters: 32768 slots of 128 experts 6.4 and 8.0, 65536 9.9 and 9.5,
+// 65536 of 1024 experts 10.4 and 16.9. With the copies after it, which wait for the
+// sort's last CTA, from fewer slots on (8 slots a token, 4096 columns):
+//   experts   20480 slots    32768          49152          65536
+//   128       35.0  35.0     52.6  53.0     76.8  74.5     102.7  96.7
+//   256       35.1  35.3     53.0  54.0     78.0  75.1     103.2  97.3
+//   512       35.2  37.1     52.2  52.7     76.4  76.2     101.8  98.6
+//   1024      35.2  40.4     52.4  55.6     77.9  76.9     102.3 100.2
 bool clusters_count(int64_t slots, int64_t experts, bool copies) {
-  return slots > (copies ? 16384 : 49152 + 64 * experts);
+  return slots > (copies ? 24576 + 32 * experts : 49152 + 64 * experts);
 }
 
 // Tokens of a chunk. One chunk per SM; smaller ones of kMoeChunkSlots slots where those

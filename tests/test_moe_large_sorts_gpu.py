@@ -100,3 +100,12 @@ def test_long_rows_of_few_tokens(tokens, hidden, drop):
     moe.test_dispatch(tokens, 3, 9, hidden, gf.GF_BF16, drop)
     if hidden % 16 == 0:
         moe.test_dispatch_fp8(tokens, 3, 9, hidden, gf.GF_F16, drop)
+
+
+@pytest.mark.parametrize("experts", [3, 128, 512, 1024])
+@pytest.mark.parametrize("copies", [0, 1])
+@pytest.mark.parametrize("more", [0, 1])
+def test_either_way_of_counting(experts, copies, more):
+    """On both sides of the number of slots from which on clusters of CTAs share the counting."""
+    slots = (24576 + 32 * experts if copies else 49152 + 64 * experts) + more
+    check_dispatch(slots, 1, experts, 2048 if copies else 8, copies)
