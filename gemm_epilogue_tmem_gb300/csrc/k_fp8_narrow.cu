@@ -225,21 +225,10 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
   const int product_tiles = KB > 0 ? table.tile0[p.groups] : 0;  // the others are zeros
   bool aborted = false;
 
-  // whole tiles, or split ones over the CTAs that then have at least
-  // kMinUnits k-blocks each
-  constexpr int kMinUnits = 4;
   const int cta = static_cast<int>(blockIdx.x), grid = static_cast<int>(gridDim.x);
-  const int rounds = (product_tiles + grid - 1) / grid;
-  const int64_t room = static_cast<int64_t>(rounds) * grid;
-  const bool whole =
-      100ll * product_tiles >= fp8_whole_fill(rounds) * room ||
-      (room - product_tiles) * KB <= static_cast<int64_t>(fp8_join_blocks(TR, DUAL)) * grid;
+  const int ctas = fp8_split_ctas(product_tiles, KB, grid, TR, DUAL);
+  const bool whole = ctas == 0;
   const int64_t units = static_cast<int64_t>(product_tiles) * KB;
-  const int64_t most = units / kMinUnits;
-  int ctas = most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;
-  // (the same number of CTAs for every tile, so that none has parts of two to
-  // join: 1 x 4096 x 8192 10.7 us, otherwise 12.3)
-  if (product_tiles > 0 && ctas >= 2 * product_tiles) ctas -= ctas % product_tiles;
   auto first_unit = [&](int c) { return units * c / ctas; };
   Pieces mine;
   mine.KB = KB;
@@ -507,10 +496,8 @@ __global__ void __launch_bounds__(kThreadsNarrow, TR == 16 ? 2 : 1)
         // consecutive CTAs, from the one with the tile's first unit; the last
         // to count adds them in order
         const int64_t first = static_cast<int64_t>(u.tile) * KB;
-        auto owner = [&](int64_t unit) {  // the CTA c with first_unit(c) <= unit < first_unit(c + 1)
-          return static_cast<int>(((unit + 1) * ctas - 1) / units);
-        };
-        const int c0 = owner(first), c1 = owner(first + KB - 1);
+        const int c0 = fp8_unit_owner(first, units, ctas);
+        const int c1 = fp8_unit_owner(first + KB - 1, units, ctas);
         float2* ws = reinterpret_cast<float2*>(p.partials);
         float2* dst = ws + (static_cast<int64_t>(2 * cta + (u.kb0 == 0 ? 1 : 0)) * NACC) * 128 + col;
 #pragma unroll

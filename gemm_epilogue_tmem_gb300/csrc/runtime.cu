@@ -1006,7 +1006,7 @@ GF_API gf_status gf_plan_launches(const gf_plan* p, int32_t* launches) {
 
 GF_API gf_status gf_plan_k_splits(const gf_plan* p, int32_t* k_splits) {
   if (!p || !k_splits) return fail(GF_ERR_INVALID_VALUE);
-  *k_splits = p->k_splits;
+  *k_splits = gf::epi_fp8(p->epi) ? gf::runtime_fp8_k_splits(p) : p->k_splits;
   return GF_OK;
 }
 

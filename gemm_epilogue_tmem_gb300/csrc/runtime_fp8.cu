@@ -138,6 +138,21 @@ gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value) {
   return st;
 }
 
+int runtime_fp8_k_splits(const gf_plan* p) {
+  if (p->kernel > kNarrow64) return 1;
+  if (p->groups > 1) return 0;
+  const int kb = static_cast<int>((p->k + 127) / 128);
+  const int64_t tiles =
+      kb == 0 ? 0 : (p->m + p->tile_rows - 1) / p->tile_rows * ((p->n + 127) / 128);
+  const int ctas = fp8_split_ctas(static_cast<int>(tiles), kb, p->grid, p->tile_rows,
+                                  p->epi == EPI_FP8_SWIGLU_QUANT ? 1 : 0);
+  int most = 1;
+  for (int64_t t = 0; ctas > 0 && t < tiles; ++t)
+    most = std::max(most, fp8_unit_owner((t + 1) * kb - 1, tiles * kb, ctas) -
+                              fp8_unit_owner(t * kb, tiles * kb, ctas) + 1);
+  return most;
+}
+
 gf_status runtime_fp8_clear_counters(gf_plan* p) {
   if (p->kernel > kNarrow64) return GF_OK;
   return gf::runtime_zero(p->d_work, counter_bytes(p));

@@ -41,6 +41,9 @@ gf_plan* runtime_new_plan(int epi, gf_dtype dtype);
 // GF_OPT_KERNEL of an e4m3 product's plan.
 gf_status runtime_fp8_set_kernel(gf_plan* p, int64_t value);
 
+// The most CTAs that share a tile of such a plan; 0 where the offsets decide.
+int runtime_fp8_k_splits(const gf_plan* p);
+
 // After a launch of such a plan that gave up: its counters back to zero.
 gf_status runtime_fp8_clear_counters(gf_plan* p);
 

@@ -480,8 +480,10 @@ GF_API gf_status gf_plan_describe(const gf_plan* plan, int32_t* tile_m, int32_t*
                                   int32_t* stages, int32_t* grid, int64_t* workspace_bytes);
 
 /* The number of CTAs that share the k-blocks of one output tile in the
- * plan's current configuration (1: no split). GF_ERR_INVALID_VALUE for a
- * NULL argument. */
+ * plan's current configuration (1: no split). For an e4m3 product of one group
+ * the most for any tile, with all m rows the group's; 0 for several groups on the
+ * kernel for few rows, whose offsets decide it on the device.
+ * GF_ERR_INVALID_VALUE for a NULL argument. */
 GF_API gf_status gf_plan_k_splits(const gf_plan* plan, int32_t* k_splits);
 
 /* The number of kernels one execute of the plan enqueues in its current
