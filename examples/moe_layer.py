@@ -5,10 +5,12 @@ Serving (``MoeLayer.serve``): the router's logits by ``gf_matmul``, its choice,
 with SwiGLU and quantisation and their down product (``gf_fp8_matmul``), and
 ``gf_moe_combine``. Nothing is read back to the host.
 
-Training (``MoeLayer.train``): the same routing on 16-bit rows, each expert's
+The gradients (``MoeLayer.train``): the same routing on 16-bit rows, each expert's
 SwiGLU through ``gf_swiglu`` / ``gf_dswiglu``, and the gradients of the input
 and of the router's weights through ``gf_moe_combine_grad`` and
-``gf_moe_dispatch_grad``.
+``gf_moe_dispatch_grad``. The experts' weights are held: their gradients, and 16-bit
+products over groups of rows, are not among the library's operators, so that the
+experts' numbers of rows are read back and each has products of its own.
 
     python examples/moe_layer.py [tokens]
 """
@@ -43,6 +45,7 @@ class MoeLayer:
         self.down = weight(experts, hidden, inner)
         self.fp8 = {name: self._quantized(getattr(self, name)) for name in ("gate", "up", "down")}
         self.plans = {}  # by number of tokens: a serving program keeps a plan for each batch size
+        self.expert_plans = {}  # by product and number of rows
 
     def _quantized(self, w):
         """The experts' weights in e4m3, a scale for each 128 x 128 block."""
@@ -73,6 +76,19 @@ class MoeLayer:
         self.plans[tokens] = p
         return p
 
+    def _expert_plan(self, product, rows):
+        """The plan of one expert's 16-bit product. Kept: a plan may be freed only when its work is done."""
+        key = product, rows
+        if key not in self.expert_plans:
+            h, i, bf16 = self.hidden, self.inner, gf.GF_BF16
+            self.expert_plans[key] = {
+                "gate_up": lambda: gf.gf_swiglu_plan(rows, i, h, bf16, save_gu=True),
+                "down": lambda: gf.gf_matmul_plan_ex(rows, h, i, bf16, gf.GF_EPILOG_NONE, gf.GF_BIAS_COL, gf.GF_B_NK),
+                "d_hid": lambda: gf.gf_dswiglu_plan(rows, i, h, bf16),
+                "d_rows": lambda: gf.gf_matmul_plan(rows, h, i, bf16, gf.GF_EPILOG_NONE),
+            }[product]()
+        return self.expert_plans[key]
+
     def route(self, x, p):
         """The router's choice: experts and weights of each token."""
         gf.gf_matmul_execute(p["router"], x, self.router, out=p["logits"])
@@ -95,7 +111,7 @@ class MoeLayer:
         """(out, d_x, d_weight): forward, and the gradients of the input (through
         the experts, the router's choice held) and of the router's weights."""
         p = self._kept(x.shape[0])
-        h, i, bf16, nk = self.hidden, self.inner, gf.GF_BF16, gf.GF_B_NK
+        h, i = self.hidden, self.inner
         expert, weight = self.route(x, p)
         rows, d_rows = p["rows"], torch.empty_like(p["rows"])
         gf.gf_moe_dispatch_execute(p["moe"], expert, x, p["offsets"], p["row_of"], p["slot_of"], rows)
@@ -105,11 +121,9 @@ class MoeLayer:
             part = slice(ends[e], ends[e + 1])
             n = ends[e + 1] - ends[e]
             hid, g, u = _empty(n, i), _empty(n, i), _empty(n, i)
-            fwd = gf.gf_swiglu_plan(n, i, h, bf16, save_gu=True)
-            gf.gf_swiglu_execute(fwd, rows[part].contiguous(), self.gate[e], self.up[e], hid, g, u)
-            down = gf.gf_matmul_plan_ex(n, h, i, bf16, gf.GF_EPILOG_NONE, gf.GF_BIAS_COL, nk)
+            gf.gf_swiglu_execute(self._expert_plan("gate_up", n), rows[part].contiguous(), self.gate[e], self.up[e], hid, g, u)
             out = _empty(n, h)
-            gf.gf_matmul_execute(down, hid, self.down[e], out=out)
+            gf.gf_matmul_execute(self._expert_plan("down", n), hid, self.down[e], out=out)
             y[part] = out
             saved.append((part, n, g, u))
         gf.gf_moe_combine_execute(p["moe"], p["row_of"], weight, y, p["out"])
@@ -118,10 +132,8 @@ class MoeLayer:
         gf.gf_moe_combine_grad_execute(p["moe"], p["offsets"], p["row_of"], weight, y, d_out, d_y, d_weight)
         for e, (part, n, g, u) in enumerate(saved):
             d_gate, d_up = _empty(n, i), _empty(n, i)
-            back = gf.gf_dswiglu_plan(n, i, h, bf16)
-            gf.gf_dswiglu_execute(back, d_y[part].contiguous(), self.down[e], g, u, d_gate, d_up)
-            plan = gf.gf_matmul_plan(n, h, i, bf16, gf.GF_EPILOG_NONE)
-            a, b = _empty(n, h), _empty(n, h)
+            gf.gf_dswiglu_execute(self._expert_plan("d_hid", n), d_y[part].contiguous(), self.down[e], g, u, d_gate, d_up)
+            plan, a, b = self._expert_plan("d_rows", n), _empty(n, h), _empty(n, h)
             gf.gf_matmul_execute(plan, d_gate, self.gate[e], out=a)
             gf.gf_matmul_execute(plan, d_up, self.up[e], out=b)
             d_rows[part] = a + b
