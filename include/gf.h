@@ -338,7 +338,9 @@ GF_API gf_plan* gf_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t grou
 /*
  * A: device e4m3 [m, k]; a_scale: device fp32 [m, ceil(k / 128)]. B, B2: device
  * e4m3 [groups, n, k]; b_scale, b2_scale: device fp32 [groups, ceil(n / 128),
- * ceil(k / 128)]; B2 and b2_scale: SWIGLU_QUANT only. Scales are any fp32 values.
+ * ceil(k / 128)]; B2 and b2_scale: SWIGLU_QUANT only. Scales are any fp32 values;
+ * some kernels form a_scale * b_scale first, so that a product of the two which
+ * overflows fp32 or falls below 2^-126 gives what fp32 makes of it.
  * offsets: device int32 [groups + 1], group g is rows offsets[g] ..
  * offsets[g + 1] - 1 (offsets[0] is taken as 0 and each other one bounded to
  * [the one before, m] by the kernel); NULL with groups == 1: all rows. Rows of
