@@ -17,7 +17,7 @@
 // 512: 713 cycles a block (0.375 us, from k = 1024 against k = 4096). Tensor
 // memory has no room for a third accumulator of this width, and with four of 128
 // columns the N = 128 instructions (365 cycles a half) are the slower choice.
-// Measured at m = 8192, n = 16384, k = 4096: 378 us, 2.9 PFLOP/s; 390-420 us in a
+// Measured at m = 8192, n = 16384, k = 4096: 378 us, 2.9 PFLOP/s; 419-436 us in a
 // steady loop at the power cap.
 //
 // The rows' scales lie a row apart in memory, so that a warp's load of one block

@@ -37,10 +37,10 @@ enum : int { kNarrow16 = 1, kNarrow64 = 2, kSingle = 3, kPair = 4 };
 // average and 37 % at worst (256 rows, 256 columns, k = 16384: 64-row tiles 18.3
 // us, 16-row tiles 13.4). Some of them (rows, columns, k; "64 x": groups):
 //                           16-row  64-row  single  pair
-//   8, 17408, 8192            26      31      52     40
-//   48, 9000, 8192            32      23      32     30
-//   256, 4096, 8192           59      24      32     30
-//   256, 17408, 8192         294      87      38     36
+//   8, 17408, 8192            26      32      40     45
+//   48, 9000, 8192            30      20      32     29
+//   256, 4096, 8192           55      22      31     28
+//   256, 17408, 8192         196      77      38     36
 //   64 x 64, 4096, 2048        -     119      90    130
 //   64 x 256, 4096, 2048       -     353     161    181
 //   8 x 1024, 4096, 16384      -       -     482    425
