@@ -34,13 +34,19 @@ __all__ = [
     "gf_moe_plan", "gf_moe_dispatch_execute", "gf_moe_dispatch_fp8_execute",
     "gf_moe_dispatch_grad_execute", "gf_moe_combine_execute", "gf_moe_combine_grad_execute",
     "gf_fp8_quantize", "gf_fp8_matmul_plan", "gf_fp8_matmul_execute",
+    "GF_F32", "GF_ACT_NONE", "GF_ACT_RELU", "GF_ACT_GELU", "GF_ACT_SILU",
+    "GF_SCORE_SOFTMAX", "GF_SCORE_SIGMOID",
+    "gf_matmul_residual_plan", "gf_matmul_residual_execute",
+    "gf_dact_bgrad_plan", "gf_dact_bgrad_execute",
+    "gf_rmsnorm_plan", "gf_rmsnorm_execute", "gf_rmsnorm_grad_execute",
+    "gf_route_plan", "gf_route_execute", "gf_route_grad_execute",
 ]
 
 # gf_status
 GF_OK, GF_ERR_INVALID_VALUE, GF_ERR_UNSUPPORTED, GF_ERR_NO_DEVICE = 0, 1, 2, 3
 GF_ERR_CUDA, GF_ERR_OUT_OF_MEMORY, GF_ERR_DEVICE_TIMEOUT = 4, 5, 6
 # gf_dtype
-GF_F16, GF_BF16 = 0, 1
+GF_F16, GF_BF16, GF_F32 = 0, 1, 2
 # gf_epilog
 GF_EPILOG_NONE, GF_EPILOG_RELU_BIAS, GF_EPILOG_RELU_AUX_BIAS = 0, 1, 2
 GF_EPILOG_DRELU_BGRAD, GF_EPILOG_BIAS = 3, 4
@@ -55,6 +61,9 @@ GF_OPT_KERNEL, GF_OPT_GROUP_M, GF_OPT_L2_HINTS, GF_OPT_SCHEDULE = 4, 5, 6, 7
 GF_OPT_SPLIT_K, GF_OPT_PDL, GF_OPT_RASTER = 8, 9, 10
 # gf_fp8_epilog
 GF_FP8_EPILOG_NONE, GF_FP8_EPILOG_SWIGLU_QUANT = 0, 1
+# gf_activation, gf_score
+GF_ACT_NONE, GF_ACT_RELU, GF_ACT_GELU, GF_ACT_SILU = 0, 1, 2, 3
+GF_SCORE_SOFTMAX, GF_SCORE_SIGMOID = 0, 1
 # fp32 partial sums the allocation-free DRELU_BGRAD entry point can hold
 GF_NOALLOC_MAX_PARTIALS = 2097152
 
@@ -69,6 +78,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int
+_F32 = ctypes.c_float
 
 
 def lib(path: str | None = None):
@@ -134,6 +144,26 @@ def lib(path: str | None = None):
         L.gf_fp8_matmul_plan.argtypes = [_I64, _I64, _I64, _I64, _I32, _I32]
         L.gf_fp8_matmul_execute.restype = _I32
         L.gf_fp8_matmul_execute.argtypes = [_P] * 11
+        L.gf_matmul_residual_plan.restype = _P
+        L.gf_matmul_residual_plan.argtypes = [_I64, _I64, _I64, _I32, _I32, _I32]
+        L.gf_matmul_residual_execute.restype = _I32
+        L.gf_matmul_residual_execute.argtypes = [_P] * 8
+        L.gf_dact_bgrad_plan.restype = _P
+        L.gf_dact_bgrad_plan.argtypes = [_I64, _I64, _I32, _I32]
+        L.gf_dact_bgrad_execute.restype = _I32
+        L.gf_dact_bgrad_execute.argtypes = [_P] * 6
+        L.gf_rmsnorm_plan.restype = _P
+        L.gf_rmsnorm_plan.argtypes = [_I64, _I64, _I32, _F32]
+        L.gf_rmsnorm_execute.restype = _I32
+        L.gf_rmsnorm_execute.argtypes = [_P] * 9
+        L.gf_rmsnorm_grad_execute.restype = _I32
+        L.gf_rmsnorm_grad_execute.argtypes = [_P] * 8
+        L.gf_route_plan.restype = _P
+        L.gf_route_plan.argtypes = [_I64, _I64, _I64, _I32, _I32, _I32, _F32, _I64, _I64, _I32, _I64]
+        L.gf_route_execute.restype = _I32
+        L.gf_route_execute.argtypes = [_P] * 6
+        L.gf_route_grad_execute.restype = _I32
+        L.gf_route_grad_execute.argtypes = [_P] * 6
         _lib = L
     return _lib
 
@@ -325,7 +355,7 @@ _I32_KIND, _F32_KIND, _E4M3_KIND = "i32", "f32", "e4m3"
 _TENSOR_KINDS = {
     _I32_KIND: ("torch.int32",), _F32_KIND: ("torch.float32",),
     _E4M3_KIND: ("torch.float8_e4m3fn", "torch.uint8"),
-    GF_F16: ("torch.float16",), GF_BF16: ("torch.bfloat16",),
+    GF_F16: ("torch.float16",), GF_BF16: ("torch.bfloat16",), GF_F32: ("torch.float32",),
 }
 _kinds = {}  # kind -> its torch dtypes
 
@@ -463,3 +493,116 @@ def gf_fp8_matmul_execute(plan: Plan, A, a_scale, B, b_scale, B2=None, b2_scale=
         _arg(offsets, _I32_KIND, groups + 1, what),
         _arg(out, _E4M3_KIND if plan.quant else plan.dtype, m * n, what),
         _arg(out_scale, _F32_KIND, m * plan.nb, what), _stream(stream)), what)
+
+
+# ------------------------------------------- a block's norm, router, residual
+def _of(plan: Plan, kind: str, what: str) -> None:
+    if getattr(plan, "block", None) != kind:
+        raise GfError(GF_ERR_INVALID_VALUE, f"{what}: not a plan of gf_{kind}_plan")
+
+
+def _block_plan(handle, kind: str, m: int, n: int, k: int, dtype: int) -> Plan:
+    if not handle:
+        raise GfError(gf_last_error(), f"gf_{kind}_plan")
+    plan = Plan(handle, m, n, k, dtype, -5, GF_BIAS_COL, GF_B_KN)
+    plan.block = kind
+    return plan
+
+
+def gf_matmul_residual_plan(m: int, n: int, k: int, dtype: int, act: int = GF_ACT_NONE,
+                            b_layout: int = GF_B_KN) -> Plan:
+    """out = act(A B + bias) + residual plan."""
+    plan = _block_plan(lib().gf_matmul_residual_plan(m, n, k, dtype, act, b_layout),
+                       "matmul_residual", m, n, k, dtype)
+    plan.b_layout = b_layout
+    return plan
+
+
+def gf_matmul_residual_execute(plan: Plan, A, B, residual, out, bias=None, z_out=None,
+                               stream=None) -> None:
+    """out = act(A B + bias) + residual; z_out keeps what the activation takes."""
+    what = "gf_matmul_residual_execute"
+    _of(plan, "matmul_residual", what)
+    m, n, k, dtype = plan.m, plan.n, plan.k, plan.dtype
+    _check(lib().gf_matmul_residual_execute(
+        plan.handle, _arg(A, dtype, m * k, what), _arg(B, dtype, n * k, what),
+        _arg(bias, dtype, n, what), _arg(residual, dtype, m * n, what),
+        _arg(out, dtype, m * n, what), _arg(z_out, dtype, m * n, what), _stream(stream)), what)
+
+
+def gf_dact_bgrad_plan(m: int, n: int, dtype: int, act: int) -> Plan:
+    """Plan of the gradients of an activation's argument and of the bias in it."""
+    return _block_plan(lib().gf_dact_bgrad_plan(m, n, dtype, act), "dact_bgrad", m, n, 0, dtype)
+
+
+def gf_dact_bgrad_execute(plan: Plan, d_out, z=None, d_z=None, bgrad=None, stream=None) -> None:
+    """d_z = d_out * act'(z) and bgrad, its column sums (GF_ACT_NONE: bgrad alone)."""
+    what = "gf_dact_bgrad_execute"
+    _of(plan, "dact_bgrad", what)
+    count, dtype = plan.m * plan.n, plan.dtype
+    _check(lib().gf_dact_bgrad_execute(
+        plan.handle, _arg(d_out, dtype, count, what), _arg(z, dtype, count, what),
+        _arg(d_z, dtype, count, what), _arg(bgrad, _F32_KIND, plan.n, what), _stream(stream)), what)
+
+
+def gf_rmsnorm_plan(rows: int, hidden: int, dtype: int, eps: float = 1e-6) -> Plan:
+    """Root-mean-square norm plan: `rows` rows of `hidden` elements."""
+    return _block_plan(lib().gf_rmsnorm_plan(rows, hidden, dtype, eps), "rmsnorm", rows, hidden,
+                       hidden, dtype)
+
+
+def gf_rmsnorm_execute(plan: Plan, x, weight, residual=None, residual_out=None, out=None, out8=None,
+                       out_scale=None, stream=None) -> None:
+    """r = x + residual, and its norm in 16 bits (out) and / or e4m3 (out8, out_scale)."""
+    what = "gf_rmsnorm_execute"
+    _of(plan, "rmsnorm", what)
+    count, dtype = plan.m * plan.n, plan.dtype
+    _check(lib().gf_rmsnorm_execute(
+        plan.handle, _arg(x, dtype, count, what), _arg(residual, dtype, count, what),
+        _arg(weight, dtype, plan.n, what), _arg(residual_out, dtype, count, what),
+        _arg(out, dtype, count, what), _arg(out8, _E4M3_KIND, count, what),
+        _arg(out_scale, _F32_KIND, plan.m * -(-plan.n // 128), what), _stream(stream)), what)
+
+
+def gf_rmsnorm_grad_execute(plan: Plan, d_out, r, weight, d_x, d_weight=None, d_residual=None,
+                            stream=None) -> None:
+    """Gradients of the norm: d_x (of x and of the residual) and d_weight."""
+    what = "gf_rmsnorm_grad_execute"
+    _of(plan, "rmsnorm", what)
+    count, dtype = plan.m * plan.n, plan.dtype
+    _check(lib().gf_rmsnorm_grad_execute(
+        plan.handle, _arg(d_out, dtype, count, what), _arg(r, dtype, count, what),
+        _arg(weight, dtype, plan.n, what), _arg(d_residual, dtype, count, what),
+        _arg(d_x, dtype, count, what), _arg(d_weight, _F32_KIND, plan.n, what), _stream(stream)), what)
+
+
+def gf_route_plan(tokens: int, experts: int, topk: int, dtype: int, score: int = GF_SCORE_SOFTMAX,
+                  renorm: bool = True, scale: float = 1.0, groups: int = 1, topk_groups: int = 1,
+                  group_best: int = 2, ld: int | None = None) -> Plan:
+    """Router plan: `topk` of `experts` for each token, from logits with rows `ld` elements apart."""
+    ld = experts if ld is None else ld
+    plan = _block_plan(lib().gf_route_plan(tokens, experts, topk, dtype, score, 1 if renorm else 0,
+                                           scale, groups, topk_groups, group_best, ld),
+                       "route", tokens, experts, topk, dtype)
+    plan.ld, plan.choices = ld, tokens * topk
+    return plan
+
+
+def gf_route_execute(plan: Plan, logits, expert, weight, bias=None, stream=None) -> None:
+    """The tokens' experts and weights; the bias takes part in the choice alone."""
+    what = "gf_route_execute"
+    _of(plan, "route", what)
+    _check(lib().gf_route_execute(
+        plan.handle, _arg(logits, plan.dtype, plan.m * plan.ld, what), _arg(bias, _F32_KIND, plan.n, what),
+        _arg(expert, _I32_KIND, plan.choices, what), _arg(weight, _F32_KIND, plan.choices, what),
+        _stream(stream)), what)
+
+
+def gf_route_grad_execute(plan: Plan, logits, expert, d_weight, d_logits, stream=None) -> None:
+    """The gradient of the logits from that of the weights."""
+    what = "gf_route_grad_execute"
+    _of(plan, "route", what)
+    _check(lib().gf_route_grad_execute(
+        plan.handle, _arg(logits, plan.dtype, plan.m * plan.ld, what),
+        _arg(expert, _I32_KIND, plan.choices, what), _arg(d_weight, _F32_KIND, plan.choices, what),
+        _arg(d_logits, plan.dtype, plan.m * plan.ld, what), _stream(stream)), what)

@@ -113,8 +113,8 @@ cudaError_t launch_dual(const LaunchArgs& a) {
 
 template <int EPI>
 cudaError_t launch_epi(const LaunchArgs& a) {
-  if (a.pair && a.split) {  // split-k units: EPILOG_NONE only
-    if constexpr (EPI == EPI_NONE) {
+  if (a.pair && a.split) {  // split-k units: EPILOG_NONE and RESIDUAL only
+    if constexpr (EPI == EPI_NONE || EPI == EPI_RESIDUAL) {
       if (a.wide) {
         if (a.bf16)
           return a.b_mn ? launch_pair_instance<EPI, __nv_bfloat16, true, true, true>(a)

@@ -23,6 +23,8 @@
 //                 column sums of dz are reduced in the CTA (warp shuffles,
 //                 then the four warps in a fixed order) and written as one
 //                 partial per tile, or added with one atomicAdd per column.
+//   RESIDUAL      out = act(acc + bias) + residual, act and the bias chosen at
+//                 run time (one instance for all: the branches are uniform).
 //
 // Every mbarrier wait is bounded; on time-out the kernel records an error in
 // the plan's status word, tells the other roles to stop, waits for its own
@@ -134,6 +136,20 @@ __device__ __forceinline__ float dgelu_tanh(float z) {
 __device__ __forceinline__ float sigmoid_f(float g) { return fmaf(0.5f, tanh_fast(0.5f * g), 0.5f); }
 
 __device__ __forceinline__ float silu_f(float g) { return g * sigmoid_f(g); }
+
+// The activations of the RESIDUAL epilogue and of their gradient, z / (1 + e^-u)
+// with u = z (SiLU) or 2 c (z + k z^3) (GELU's tanh form: (1 + tanh v) / 2 =
+// 1 / (1 + e^-2v)), by the hardware exponential and reciprocal: errors of a few
+// 2^-24 relative to the value. Their sum with the residual is what is rounded, and
+// fp16 keeps 2^-11 of it, which the error of tanh.approx would reach.
+__device__ __forceinline__ float logistic_f(float u) { return __fdividef(1.f, 1.f + __expf(-u)); }
+
+__device__ __forceinline__ float act_value(int act, float z) {
+  if (act == kActRelu) return z > 0.f ? z : 0.f;
+  if (act == kActNone) return z;
+  const float u = act == kActGelu ? z * fmaf(2.f * kGeluCK, z * z, 2.f * kGeluC) : z;
+  return __fdividef(z, 1.f + __expf(-u));
+}
 
 // 32 consecutive values of one row -> 4 x 16-byte stores of T (columns at or
 // past N are skipped; N is a multiple of 8)
@@ -292,8 +308,8 @@ __device__ __forceinline__ void prefetch_side(const GemmParams& p, int row0w, in
       const uint32_t w = wrow_ok && col < p.N ? __ldg(p.aux_in + (size_t)wrow * p.N + col) : 0u;
       st_shared_u32(side + 4u * (uint32_t)(32 * i + (int)lane), w);
     }
-  } else if constexpr (epi_has_bias(EPI)) {
-    if (p.bias_axis == 0) {
+  } else if constexpr (epi_has_bias(EPI) || EPI == EPI_RESIDUAL) {
+    if (p.bias_axis == 0 && (EPI != EPI_RESIDUAL || p.bias != nullptr)) {
       const T* bias = reinterpret_cast<const T*>(p.bias);
       // NC columns of 2 bytes: 16-byte pieces, lane-strided
 #pragma unroll
@@ -406,9 +422,10 @@ __device__ __forceinline__ bool epilogue_drain(const GemmParams& p, uint32_t t_r
                 "preloaded drains: TMA stores, one operand, 4 chunks");
   constexpr bool kDual = epi_dual(EPI);
   // 16-byte side inputs per chunk: g and u (DSWIGLU), the pre-activation
-  // (DGELU_BGRAD), the column bias (bias epilogs), the mask word (DRELU_BGRAD)
+  // (DGELU_BGRAD), the residual (RESIDUAL), the column bias (bias epilogs), the
+  // mask word (DRELU_BGRAD)
   constexpr int kSide = EPI == EPI_DSWIGLU ? 8
-                        : (EPI == EPI_DGELU_BGRAD || epi_has_bias(EPI)) ? 4
+                        : (EPI == EPI_DGELU_BGRAD || EPI == EPI_RESIDUAL || epi_has_bias(EPI)) ? 4
                         : EPI == EPI_DRELU_BGRAD ? 1
                                                  : 0;
   constexpr int kSideN = kSide > 0 ? kSide : 1;
@@ -455,7 +472,8 @@ __device__ __forceinline__ bool epilogue_drain(const GemmParams& p, uint32_t t_r
   // the saved 16-bit activations are read coalesced when the staging buffer
   // is there: lane l loads 16 bytes of row 8g + l/4 (4 lanes per 64-byte row
   // segment), and transpose_side() hands each lane its own row afterwards
-  constexpr bool kCoalesced = STG && (EPI == EPI_DSWIGLU || EPI == EPI_DGELU_BGRAD);
+  constexpr bool kCoalesced =
+      STG && (EPI == EPI_DSWIGLU || EPI == EPI_DGELU_BGRAD || EPI == EPI_RESIDUAL);
   auto load_side = [&](int col0, uint4 (&sd)[kSideN]) {
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (kCoalesced) {
@@ -463,13 +481,18 @@ __device__ __forceinline__ bool epilogue_drain(const GemmParams& p, uint32_t t_r
       const int col = col0 + 8 * (int)pc;
 #pragma unroll
       for (int in = 0; in < (EPI == EPI_DSWIGLU ? 2 : 1); ++in) {
-        const T* base = reinterpret_cast<const T*>(in == 0 ? p.aux_in : p.aux_in2);
+        const T* base = reinterpret_cast<const T*>(
+            EPI == EPI_RESIDUAL ? p.residual
+                                : static_cast<const void*>(in == 0 ? p.aux_in : p.aux_in2));
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int r = row0w + 8 * g + (int)(lane >> 2);
-          sd[4 * in + g] = r < p.M && col < p.N
-                               ? __ldg(reinterpret_cast<const uint4*>(base + (size_t)r * p.N + col))
-                               : zero;
+          const uint4* at = reinterpret_cast<const uint4*>(base + (size_t)r * p.N + col);
+          // (the residual may be out: no load that takes it for constant)
+          if (r < p.M && col < p.N)
+            sd[4 * in + g] = EPI == EPI_RESIDUAL ? *at : __ldg(at);
+          else
+            sd[4 * in + g] = zero;
         }
       }
     } else if constexpr (EPI == EPI_DSWIGLU || EPI == EPI_DGELU_BGRAD) {
@@ -486,6 +509,11 @@ __device__ __forceinline__ bool epilogue_drain(const GemmParams& p, uint32_t t_r
                           ? __ldg(reinterpret_cast<const uint4*>(up + 8 * g))
                           : zero;
       }
+    } else if constexpr (EPI == EPI_RESIDUAL) {
+      const T* rp = reinterpret_cast<const T*>(p.residual) + (size_t)row * p.N + col0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        sd[g] = row_ok && col0 + 8 * g < p.N ? *reinterpret_cast<const uint4*>(rp + 8 * g) : zero;
     } else if constexpr (EPI == EPI_DRELU_BGRAD) {
       sd[0] = zero;
       if constexpr (SIDE) {
@@ -583,6 +611,33 @@ __device__ __forceinline__ bool epilogue_drain(const GemmParams& p, uint32_t t_r
         unpack8<T>(cur[g], z8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * g + i] = v[8 * g + i] * dgelu_tanh(z8[i]);
+      }
+    } else if constexpr (EPI == EPI_RESIDUAL) {
+      if (bias != nullptr) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint4 b = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (SIDE)
+            b = ld_shared_v4(side + 2u * (uint32_t)(col0 - n0) + 16u * g);
+          else if (col0 + 8 * g < p.N)
+            b = *reinterpret_cast<const uint4*>(bias + col0 + 8 * g);
+          float b8[8];
+          unpack8<T>(b, b8);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[8 * g + i] += b8[i];
+        }
+      }
+      if (p.aux_out != nullptr) emit(true, col0, v);  // what the activation takes, rounded to T
+      if (p.act != kActNone) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = act_value(p.act, v[j]);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float r8[8];
+        unpack8<T>(cur[g], r8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * g + i] += r8[i];
       }
     } else if constexpr (EPI == EPI_DRELU_BGRAD) {
       // lane j holds the mask word of column col0 + j; transposed, lane i

@@ -57,11 +57,11 @@ GF_HD constexpr bool pair_epi8(int epi, bool wide) { return wide && epi >= 0; }
 // A 2 KB shared-memory staging buffer per epilogue warp: 64-byte row-segment
 // output stores, and coalesced loads of saved 16-bit activations. The wide
 // tiles, and on 256 x 256 tiles the epilogs that store two or three 16-bit
-// outputs per element or read saved activations (one ring stage makes room
+// outputs per element or read saved activations or a residual (one ring stage makes room
 // for it where the bias-gradient scratch has not already).
 GF_HD constexpr bool pair_stg(int epi, bool wide) {
   return wide || epi == EPI_GELU_AUX_BIAS || epi == EPI_SWIGLU_SAVE || epi == EPI_DSWIGLU ||
-         epi == EPI_DGELU_BGRAD;
+         epi == EPI_DGELU_BGRAD || epi == EPI_RESIDUAL;
 }
 
 // Chunk slots of the dSwiGLU side-input ring per epilogue warp (256 x 256
@@ -621,7 +621,8 @@ __global__ void __launch_bounds__(PairCfg<epi_dual(EPI) ? 2 : 1, epi_has_bgrad(E
       const int n0 = nb * BN;
       // wide: this warp's 128 columns of each accumulator half, their side
       // inputs (bias or mask words) prefetched while the mainloop runs
-      constexpr bool kSide = WIDE && (EPI == EPI_DRELU_BGRAD || epi_has_bias(EPI));
+      constexpr bool kSide =
+          WIDE && (EPI == EPI_DRELU_BGRAD || EPI == EPI_RESIDUAL || epi_has_bias(EPI));
       constexpr uint32_t kSideHalf = EPI == EPI_DRELU_BGRAD ? 512u : 256u;  // 128 columns
       const int c_sub = 128 * sub;
       const uint32_t side = side0 + 1024u * (uint32_t)ew;

@@ -1,0 +1,519 @@
+// Root-mean-square norm with the residual's addition before it.
+//
+//   r = round(x + residual),  y = r w rstd,  rstd = 1 / sqrt(mean(r^2) + eps)
+//   g = d_y w,  d = rstd (g - r rstd^2 mean(g r)) + d_r,  d_w = sum of d_y r rstd
+//
+// A row is read once: it stays in registers, in 16 bits, between its sum and its
+// output. 16-byte accesses for rows of any length: where rows do not start on
+// 16 bytes, the row's words are those it would have in an aligned array, the ones
+// at its two ends are read and written one element at a time. HBM bounds both
+// directions; nothing is kept from the forward but r itself, whose sum of squares
+// the backward forms along with the other one that it needs.
+//
+// e4m3 output: the scale of 128 elements is a power of two that the block's
+// largest magnitude decides, so that a last bit of rstd could turn the whole block's
+// scale. That magnitude is max|r w| rstd; the products r w of 16-bit values are exact
+// in fp32, and rstd is held as the sum of two fp32, from a sum of squares held the
+// same way (error-free addition: Knuth, The Art of Computer Programming 2, 4.2.2,
+// and one Newton step), so that the scale is the one of 64-bit arithmetic.
+#include <math.h>
+
+#include "block.h"
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace gf {
+namespace {
+
+// a + b = s + e exactly
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float z = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
+}
+
+// a sum of squares: fp32, or (EXACT) two fp32
+template <bool EXACT>
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {
+    if constexpr (EXACT) {
+      float e;
+      two_sum(hi, v, hi, e);
+      lo += e;
+    } else {
+      hi += v;
+    }
+  }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.hi);
+    if constexpr (EXACT) lo += o.lo;
+  }
+  __device__ __forceinline__ Sum other(int lane_mask) const {
+    Sum o = {0.f, 0.f};
+    o.hi = __shfl_xor_sync(0xFFFFFFFFu, hi, lane_mask);
+    if constexpr (EXACT) o.lo = __shfl_xor_sync(0xFFFFFFFFu, lo, lane_mask);
+    return o;
+  }
+};
+
+// 1 / sqrt(sum / n + eps), as hi + lo (EXACT)
+template <bool EXACT>
+__device__ __forceinline__ float inv_rms(const Sum<EXACT>& sum, int n, float eps, float& lo) {
+  lo = 0.f;
+  const float nf = static_cast<float>(n);
+  if constexpr (!EXACT) {
+    return rsqrtf(sum.hi / nf + eps);
+  } else {
+    float sh, sl;
+    two_sum(sum.hi, sum.lo, sh, sl);
+    if (!isfinite(sum.hi)) return rsqrtf(sum.hi);
+    const float q = __fdiv_rn(sh, nf);
+    const float ql = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, nf, sh), sl), nf);
+    float v, vl;
+    two_sum(q, eps, v, vl);
+    vl = __fadd_rn(vl, ql);
+    const float r = rsqrtf(v);
+    if (!isfinite(r)) return r;
+    // r^2 and v r^2 with their rounding errors; 1 - v r^2 is small
+    const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
+    const float t = __fmul_rn(v, p), te = __fmaf_rn(v, p, -t);
+    float e = __fsub_rn(__fsub_rn(1.f, t), te);
+    e = __fsub_rn(e, __fmul_rn(v, pe));
+    e = __fsub_rn(e, __fmul_rn(vl, p));
+    lo = __fmul_rn(__fmul_rn(0.5f, r), e);
+    return r;
+  }
+}
+
+// A row of a dense [rows, n] matrix of 16-bit elements as 16-byte words. ALIGNED:
+// n is a multiple of 8; else the row begins at element `o` of its first word.
+template <typename T, bool ALIGNED>
+struct Row {
+  int64_t word0;  // index of the first word
+  int o, n, words;
+  __device__ __forceinline__ Row(int64_t row, int n_) : n(n_) {
+    const int64_t first = row * n_;
+    o = ALIGNED ? 0 : static_cast<int>(first & 7);
+    word0 = (first - o) >> 3;
+    words = (o + n + 7) >> 3;
+  }
+  __device__ __forceinline__ bool whole(int w) const {
+    return ALIGNED || ((w > 0 || o == 0) && 8 * w + 8 <= o + n);
+  }
+  __device__ __forceinline__ uint4 load(const void* base, int w) const {
+    const uint4* at = static_cast<const uint4*>(base) + word0 + w;
+    if (whole(w)) return *at;
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = 8 * w + j - o;
+      if (col >= 0 && col < n) v[j / 2] |= static_cast<uint32_t>(e[j]) << (16 * (j & 1));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  __device__ __forceinline__ void store(void* base, int w, const uint4& u) const {
+    uint4* at = static_cast<uint4*>(base) + word0 + w;
+    if (whole(w)) {
+      *at = u;
+      return;
+    }
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+    uint16_t* e = reinterpret_cast<uint16_t*>(at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = 8 * w + j - o;
+      if (col >= 0 && col < n) e[j] = static_cast<uint16_t>(v[j / 2] >> (16 * (j & 1)));
+    }
+  }
+  // a vector over the columns (the norm's weight), at this row's words
+  __device__ __forceinline__ uint4 load_cols(const void* base, int w) const {
+    if (ALIGNED) return static_cast<const uint4*>(base)[w];
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    const uint16_t* e = static_cast<const uint16_t*>(base);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = 8 * w + j - o;
+      if (col >= 0 && col < n) v[j / 2] |= static_cast<uint32_t>(e[col]) << (16 * (j & 1));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = Pair16<T>::unpack(w[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  return make_uint4(Pair16<T>::pack(f[0], f[1]), Pair16<T>::pack(f[2], f[3]),
+                    Pair16<T>::pack(f[4], f[5]), Pair16<T>::pack(f[6], f[7]));
+}
+
+// the sum over the blockDim.x threads of a row, in the same order in each of them
+template <typename S>
+__device__ __forceinline__ S row_sum(S s, S* red) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s.add(s.other(d));
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return s;
+  S* mine = red + threadIdx.y * warps;
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = mine[0];
+  for (int i = 1; i < warps; ++i) s.add(mine[i]);
+  return s;
+}
+
+// Threads (x: the words of a row, y: rows). V words a thread.
+template <typename T, int V, bool ALIGNED, bool FP8>
+__global__ void __launch_bounds__(544) norm_kernel(const NormParams p) {
+  __shared__ Sum<FP8> red[32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const Row<T, ALIGNED> row(at, p.hidden);
+  const int words = at < p.rows ? row.words : 0;
+  const int step = blockDim.x, w0 = threadIdx.x;
+  uint4 r[V], wt[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int w = w0 + i * step;
+    r[i] = w < words ? row.load(p.x, w) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (p.residual != nullptr) {
+    uint4 add[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      add[i] = w < words ? row.load(p.residual, w) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float a[8], b[8];
+      unpack<T>(r[i], a);
+      unpack<T>(add[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+      r[i] = pack<T>(a);  // the residual stream is kept in 16 bits, and normed as it is kept
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int w = w0 + i * step;
+    wt[i] = w < words ? row.load_cols(p.weight, w) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (p.residual_out != nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      if (w < words) row.store(p.residual_out, w, r[i]);
+    }
+  }
+  Sum<FP8> s = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float f[8];
+    unpack<T>(r[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.add(__fmul_rn(f[j], f[j]));
+  }
+  s = row_sum(s, red);
+  float lo;
+  const float rstd = inv_rms<FP8>(s, p.hidden, p.eps, lo);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int w = w0 + i * step;
+    float f[8], g[8];
+    unpack<T>(r[i], f);
+    unpack<T>(wt[i], g);
+    uint32_t mag = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] *= g[j];
+      if (FP8) mag = max(mag, finite_mag_bits(f[j]));
+      f[j] *= rstd;
+    }
+    if ((!FP8 || p.out != nullptr) && w < words) row.store(p.out, w, pack<T>(f));
+    if constexpr (FP8) {
+      // 16 lanes hold a block of 128
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d));
+      const float m = __uint_as_float(mag);
+      const float top = __fmul_rn(m, rstd);
+      const float err = __fmaf_rn(m, lo, __fmaf_rn(m, rstd, -top));
+      uint32_t bits = finite_mag_bits(top);
+      // the rounded product lies on the border of two scales, the product above it
+      if ((bits & 0x7FFFFFu) == 0x600000u && err > 0.f) ++bits;
+      float inv;
+      const float scale = e4m3_scale(bits, inv);
+      if (w < words) {
+        reinterpret_cast<uint2*>(p.out8)[row.word0 + w] =
+            make_uint2(e4m3x4(f[0], f[1], f[2], f[3], inv), e4m3x4(f[4], f[5], f[6], f[7], inv));
+        if ((threadIdx.x & 15) == 0) p.scale[at * ((p.hidden + 127) >> 7) + (w >> 4)] = scale;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- backward
+struct Sum2 {
+  float rr, gr;
+  __device__ __forceinline__ void add(const Sum2& o) {
+    rr += o.rr;
+    gr += o.gr;
+  }
+  __device__ __forceinline__ Sum2 other(int lane_mask) const {
+    Sum2 o;
+    o.rr = __shfl_xor_sync(0xFFFFFFFFu, rr, lane_mask);
+    o.gr = __shfl_xor_sync(0xFFFFFFFFu, gr, lane_mask);
+    return o;
+  }
+};
+
+// CTAs walk over the rows, a thread keeping the same columns from row to row for
+// the weight's gradient (in registers; from V = 8 on in shared memory). Rows whose
+// words do not begin on the row begin elsewhere in their first word each time,
+// with a period of 8: there the thread rows of the grid are a multiple of 8.
+template <typename T, int V, bool ALIGNED>
+__global__ void __launch_bounds__(544) norm_grad_kernel(const NormParams p) {
+  constexpr bool kSmemAcc = V >= 8;
+  extern __shared__ float cols[];  // [hidden]
+  __shared__ Sum2 red[2][32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = blockIdx.x * blockDim.y + threadIdx.y;  // thread row
+  const int step = blockDim.x, w0 = threadIdx.x;
+  const bool sums = p.partials != nullptr;
+  if (sums) {
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < p.hidden; c += blockDim.x * blockDim.y)
+      cols[c] = 0.f;
+  }
+  __syncthreads();
+  float acc[kSmemAcc ? 1 : V][8];
+#pragma unroll
+  for (int i = 0; i < (kSmemAcc ? 1 : V); ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  const int o0 = ALIGNED ? 0 : static_cast<int>((static_cast<int64_t>(lane) * p.hidden) & 7);
+  int turn = 0;
+  // every thread row of a CTA goes through as many rows (barriers), the last past the end
+  const int64_t cta_first = static_cast<int64_t>(blockIdx.x) * blockDim.y;
+  for (int64_t skip = 0; cta_first + skip < p.rows; skip += p.lanes, turn ^= 1) {
+    const int64_t at = lane + skip;
+    const Row<T, ALIGNED> row(at, p.hidden);
+    const int words = at < p.rows ? row.words : 0;
+    uint4 r[V], dy[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      r[i] = dy[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (w < words) {
+        r[i] = row.load(p.x, w);
+        dy[i] = row.load(p.d_out, w);
+      }
+    }
+    Sum2 s = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      float f[8], g[8], wt[8];
+      unpack<T>(r[i], f);
+      unpack<T>(dy[i], g);
+      unpack<T>(w < words ? row.load_cols(p.weight, w) : make_uint4(0u, 0u, 0u, 0u), wt);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s.rr += f[j] * f[j];
+        s.gr += g[j] * wt[j] * f[j];
+      }
+    }
+    s = row_sum(s, red[turn]);
+    const float n = static_cast<float>(p.hidden);
+    const float rstd = rsqrtf(s.rr / n + p.eps);
+    const float c = rstd * rstd * (s.gr / n);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      if (w < words) {
+        float f[8], g[8], wt[8], d[8];
+        unpack<T>(r[i], f);
+        unpack<T>(dy[i], g);
+        unpack<T>(row.load_cols(p.weight, w), wt);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = rstd * (g[j] * wt[j] - f[j] * c);
+        if (p.residual != nullptr) {
+          float e[8];
+          unpack<T>(row.load(p.residual, w), e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] += e[j];
+        }
+        row.store(p.out, w, pack<T>(d));
+        if (sums) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v = g[j] * f[j] * rstd;
+            if constexpr (kSmemAcc) {
+              const int col = 8 * w + j - row.o;
+              if (ALIGNED || (col >= 0 && col < p.hidden)) cols[col] += v;
+            } else {
+              acc[i][j] += v;
+            }
+          }
+        }
+      }
+    }
+  }
+  if (!sums) return;
+  if constexpr (!kSmemAcc) {
+    // the thread rows one after the other: a fixed order
+    for (int y = 0; y < blockDim.y; ++y) {
+      __syncthreads();
+      if (threadIdx.y == y) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int col = 8 * (w0 + i * step) + j - o0;
+            if (col >= 0 && col < p.hidden) cols[col] += acc[i][j];
+          }
+      }
+    }
+  }
+  __syncthreads();
+  float* out = p.partials + static_cast<int64_t>(blockIdx.x) * p.hidden;
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < p.hidden; c += blockDim.x * blockDim.y)
+    out[c] = cols[c];
+}
+
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* partials, int rows, int n,
+                                                          float* out) {
+  __shared__ float red[8][33];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (col < n) {
+#pragma unroll 8
+    for (int r = slice; r < rows; r += 8) s += partials[static_cast<int64_t>(r) * n + col];
+  }
+  red[slice][lane] = s;
+  __syncthreads();
+  if (slice == 0 && col < n) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += red[k][lane];
+    out[col] = s;
+  }
+}
+
+// Words of a row (with one to spare where it may begin anywhere), words a thread,
+// threads a row and rows a CTA.
+struct Shape {
+  int v, threads, rows;
+};
+
+Shape norm_shape(int64_t hidden) {
+  const int words = static_cast<int>((hidden + 7) / 8) + (hidden % 8 != 0 ? 1 : 0);
+  Shape s;
+  s.v = words <= 256 ? 1 : words <= 1024 ? 2 : words <= 2048 ? 4 : 8;
+  s.threads = (words + s.v * 32 - 1) / (s.v * 32) * 32;
+  s.rows = s.threads >= 128 ? 1 : 128 / s.threads;
+  return s;
+}
+
+template <typename T, bool ALIGNED, bool FP8>
+cudaError_t forward(const NormParams& p, cudaStream_t stream, int pdl) {
+  const Shape s = norm_shape(p.hidden);
+  const dim3 grid((p.rows + s.rows - 1) / s.rows), block(s.threads, s.rows);
+  switch (s.v) {
+    case 1: return launch_pdl(norm_kernel<T, 1, ALIGNED, FP8>, grid, block, 0, stream, pdl, p);
+    case 2: return launch_pdl(norm_kernel<T, 2, ALIGNED, FP8>, grid, block, 0, stream, pdl, p);
+    case 4: return launch_pdl(norm_kernel<T, 4, ALIGNED, FP8>, grid, block, 0, stream, pdl, p);
+    case 8: return launch_pdl(norm_kernel<T, 8, ALIGNED, FP8>, grid, block, 0, stream, pdl, p);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t forward_type(const NormParams& p, cudaStream_t stream, int pdl) {
+  if (p.out8 != nullptr) return forward<T, true, true>(p, stream, pdl);
+  return p.hidden % 8 == 0 ? forward<T, true, false>(p, stream, pdl)
+                           : forward<T, false, false>(p, stream, pdl);
+}
+
+// calls f(kernel) with the backward kernel of these rows
+template <typename T, typename F>
+cudaError_t with_grad_kernel(int64_t hidden, const F& f) {
+  const bool aligned = hidden % 8 == 0;
+  switch (norm_shape(hidden).v) {
+    case 1: return f(aligned ? norm_grad_kernel<T, 1, true> : norm_grad_kernel<T, 1, false>);
+    case 2: return f(aligned ? norm_grad_kernel<T, 2, true> : norm_grad_kernel<T, 2, false>);
+    case 4: return f(aligned ? norm_grad_kernel<T, 4, true> : norm_grad_kernel<T, 4, false>);
+    case 8: return f(aligned ? norm_grad_kernel<T, 8, true> : norm_grad_kernel<T, 8, false>);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t grad_ctas(int64_t rows, int64_t hidden, int sms, int* ctas) {
+  const Shape s = norm_shape(hidden);
+  return with_grad_kernel<T>(hidden, [&](auto kernel) {
+    const size_t smem = static_cast<size_t>(hidden) * 4;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kNormMaxHidden * 4);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, s.threads * s.rows, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    int64_t n = (rows + s.rows - 1) / s.rows;
+    if (n > static_cast<int64_t>(per_sm) * sms) n = static_cast<int64_t>(per_sm) * sms;
+    if (hidden % 8 != 0) n = (n + 7) / 8 * 8;  // thread rows in whole periods
+    *ctas = static_cast<int>(n < 1 ? 1 : n);
+    return cudaSuccess;
+  });
+}
+
+template <typename T>
+cudaError_t backward(const NormParams& p, int ctas, cudaStream_t stream, int pdl) {
+  const Shape s = norm_shape(p.hidden);
+  NormParams q = p;
+  q.lanes = ctas * s.rows;
+  return with_grad_kernel<T>(p.hidden, [&](auto kernel) {
+    return launch_pdl(kernel, dim3(ctas), dim3(s.threads, s.rows),
+                      static_cast<size_t>(p.hidden) * 4, stream, pdl, q);
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams& p, int bf16, cudaStream_t stream, int pdl) {
+  return bf16 ? forward_type<__nv_bfloat16>(p, stream, pdl) : forward_type<__half>(p, stream, pdl);
+}
+
+int norm_grad_ctas(int64_t rows, int64_t hidden, int bf16, int sms, cudaError_t* err) {
+  int n = 0;
+  *err = bf16 ? grad_ctas<__nv_bfloat16>(rows, hidden, sms, &n)
+              : grad_ctas<__half>(rows, hidden, sms, &n);
+  return n;
+}
+
+cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream_t stream, int pdl) {
+  return bf16 ? backward<__nv_bfloat16>(p, ctas, stream, pdl) : backward<__half>(p, ctas, stream, pdl);
+}
+
+cudaError_t launch_column_sums(const float* partials, int rows, int cols, float* out,
+                               cudaStream_t stream, int pdl) {
+  return launch_pdl(column_sums_kernel, dim3((cols + 31) / 32), dim3(256), 0, stream, pdl,
+                    partials, rows, cols, out);
+}
+
+}  // namespace gf

@@ -24,7 +24,7 @@ struct LaunchArgs {
   int tile_n;   // 128 or 256 (single-CTA kernel)
   int pair;     // 1: the CTA-pair kernel (256 x 256 tiles)
   int wide;     // with pair: 256 x 512 tiles (one accumulator in two halves)
-  int split;    // with pair: split-k work units (256 x 256 tiles, EPILOG_NONE)
+  int split;    // with pair: split-k work units (EPILOG_NONE, RESIDUAL)
   int pdl;      // 1: programmatic dependent launch (set-up overlaps the previous kernel)
   cudaStream_t stream;
 };
@@ -33,6 +33,7 @@ cudaError_t launch_none_bias(int epi, const LaunchArgs& a);   // EPI_NONE, EPI_B
 cudaError_t launch_relu(int epi, const LaunchArgs& a);        // EPI_RELU_BIAS, EPI_RELU_AUX_BIAS
 cudaError_t launch_drelu(const LaunchArgs& a);                // EPI_DRELU_BGRAD
 cudaError_t launch_gelu(int epi, const LaunchArgs& a);        // EPI_GELU_BIAS, _AUX_BIAS, EPI_DGELU_BGRAD
+cudaError_t launch_residual(const LaunchArgs& a);             // EPI_RESIDUAL
 cudaError_t launch_swiglu(int epi, const LaunchArgs& a);      // EPI_SWIGLU, _SAVE, EPI_DSWIGLU
 cudaError_t launch_bgrad_finalize(const float* partial, int num_m_blocks, int n, float* bgrad,
                                   cudaStream_t stream, int pdl);

@@ -27,7 +27,17 @@ enum Epi : int {
   EPI_FP8 = 11,               // block-scaled e4m3 product, 16-bit out
   EPI_FP8_SWIGLU_QUANT = 12,  // ... gate+up SwiGLU, e4m3 out
   EPI_MOE = 13,               // expert routing
+  EPI_RESIDUAL = 14,          // a 16-bit GEMM plan: out = act(acc + bias) + residual
+  EPI_ROUTE = 15,             // a router's choice
+  EPI_NORM = 16,              // root-mean-square norm
+  EPI_DACT = 17,              // gradient of an activation and its bias
 };
+
+// the plans of the 16-bit GEMM kernels
+GF_HD constexpr bool epi_gemm(int epi) { return epi < EPI_FP8 || epi == EPI_RESIDUAL; }
+
+// gf_activation
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 
 // a plan of gf_fp8_matmul_plan
 GF_HD constexpr bool epi_fp8(int epi) { return epi == EPI_FP8 || epi == EPI_FP8_SWIGLU_QUANT; }
@@ -76,6 +86,8 @@ struct GemmParams {
   const uint32_t* aux_in;
   void* aux_out2;        // SWIGLU_SAVE: u
   const void* aux_in2;   // DSWIGLU: saved u
+  const void* residual;  // RESIDUAL: [M, N] of the dtype
+  int32_t act;           // RESIDUAL: a gf_activation
   float* bgrad;  // atomic: bgrad[N] (zeroed first); two-pass: partials [num_m_blocks][N]
   int32_t* status;
   uint64_t wait_limit_ns;

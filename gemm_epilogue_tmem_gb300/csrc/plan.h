@@ -12,6 +12,7 @@ struct gf_plan {
   int64_t m, n, k;
   gf_dtype dtype;
   int epi;               // gf::Epi code (the public gf_epilog values, plus SwiGLU forms)
+  int act;               // gf_activation of gf_matmul_residual_plan, gf_dact_bgrad_plan
   gf_bias_axis bias_axis;
   gf_b_layout b_layout;
   int device;
@@ -64,11 +65,16 @@ struct gf_plan {
   int64_t groups;
   int kernel;            // 1, 2 narrow, 3 single CTA, 4 CTA pair
   int tile_rows;         // rows of a tile
+  // gf_route_plan: m = tokens, n = experts, groups of experts above
+  int64_t topk_groups, ld;
+  int group_best, score, renorm;
+  float scale;           // of the weights; gf_rmsnorm_plan: eps
   // gf_moe_plan: m = tokens, k = hidden
   int64_t topk, experts;
   int chunk_tokens;      // tokens per CTA of the sort
   int num_chunks;
   int fused;             // little to copy: the sort kernel does that too
-  void* d_work;          // e4m3 products: counters and partial sums of split tiles
+  void* d_work;          // e4m3 products: counters and partial sums of split tiles;
+                         // gradients of a norm's weight, a bias: the CTAs' column sums
   size_t work_bytes;
 };

@@ -92,6 +92,8 @@ bool needs_aux_out(int e) {
   return e == gf::EPI_RELU_AUX_BIAS || e == gf::EPI_GELU_AUX_BIAS || e == gf::EPI_SWIGLU_SAVE ||
          e == gf::EPI_DSWIGLU;
 }
+// epilogs whose CTA-pair kernel has a split-k form
+bool splits_pair(int e) { return e == gf::EPI_NONE || e == gf::EPI_RESIDUAL; }
 bool needs_aux_in(int e) { return has_bgrad(e) || e == gf::EPI_DSWIGLU; }
 
 // 3-D tensor map over a row-major [k, n] matrix of 16-bit elements seen as
@@ -175,7 +177,7 @@ void plan_tiles(gf_plan* p) {
   const int64_t tiles256 = m2 * ((p->n + pair_n_narrow - 1) / pair_n_narrow);
   const int64_t tiles512 = m2 * ((p->n + pair_n_wide - 1) / pair_n_wide);
   const int64_t cl = p->max_pair_clusters > 0 ? p->max_pair_clusters : 1;
-  // The plan's split k of the CTA-pair tiles (EPILOG_NONE): when `tiles`
+  // The plan's split k of the CTA-pair tiles (EPILOG_NONE, RESIDUAL): when `tiles`
   // leave the last wave of the resident pairs at most half full, that
   // wave's tiles are shared by several pairs each (k-blocks in consecutive
   // runs), so that it ends after a fraction of a tile; the tiles before run
@@ -184,7 +186,7 @@ void plan_tiles(gf_plan* p) {
   // measured on the SwiGLU down GEMM; at k = 4096 over 13 waves it gave
   // nothing). Returns the splits, or 0.
   auto last_wave_split = [&](int64_t tiles) -> int {
-    if (dual || p->epi != gf::EPI_NONE || p->forced_split != 0 || p->max_pair_clusters <= 0)
+    if (dual || !splits_pair(p->epi) || p->forced_split != 0 || p->max_pair_clusters <= 0)
       return 0;
     const int64_t rem = tiles % cl;
     if (rem == 0 || 2 * rem > cl || p->num_k_blocks < (tiles <= 3 * cl ? 32 : 128)) return 0;
@@ -230,12 +232,12 @@ void plan_tiles(gf_plan* p) {
     p->stages = gf::stages_for(pair_n, 1, p->epi);
     p->num_n_blocks = static_cast<int>((p->n + pair_n - 1) / pair_n);
     p->num_tiles = static_cast<int>(pair_tiles);
-    // Split k (EPILOG_NONE, 256 x 256 or wide tiles): the plan's split of
+    // Split k (EPILOG_NONE and RESIDUAL, 256 x 256 or wide tiles): the plan's split of
     // a last wave (above); GF_OPT_SPLIT_K >= 2 splits every tile that many
     // ways.
     int want = 0;
     int64_t from = 0;
-    if (!dual && p->epi == gf::EPI_NONE && p->num_k_blocks >= 2) {
+    if (!dual && splits_pair(p->epi) && p->num_k_blocks >= 2) {
       if (p->forced_split >= 2) {
         want = p->forced_split;
       } else {
@@ -483,6 +485,7 @@ struct ExecArgs {
   void* aux_out;
   void* aux_out2;
   float* bgrad;
+  const void* residual = nullptr;
 };
 
 // Checks the pointers the plan's epilog needs, encodes the tensor maps and
@@ -508,6 +511,10 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
   }
   if (has_bgrad(e) && p->n > 0 && (!x.bgrad || !aligned16(x.bgrad)))
     return fail(GF_ERR_INVALID_VALUE);
+  // RESIDUAL: the bias and the saved pre-activation are as the call wants them
+  if (!empty && e == gf::EPI_RESIDUAL &&
+      (!x.residual || !aligned16(x.residual) || !aligned16(x.bias) || !aligned16(x.aux_out)))
+    return fail(GF_ERR_INVALID_VALUE);
 
   if (cudaSetDevice(p->device) != cudaSuccess) return fail(GF_ERR_CUDA);
 
@@ -528,7 +535,8 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
   memset(&tmAux, 0, sizeof tmAux);
   // the 256 x 512 tiles store their 16-bit outputs by TMA
   const bool store_maps = p->pair && p->wide;
-  const bool aux16 = e == gf::EPI_GELU_AUX_BIAS || e == gf::EPI_DSWIGLU;
+  const bool aux16 = e == gf::EPI_GELU_AUX_BIAS || e == gf::EPI_DSWIGLU ||
+                     (e == gf::EPI_RESIDUAL && x.aux_out != nullptr);
   gf_plan* pm = const_cast<gf_plan*>(p);  // the map cache only
   std::unique_lock<std::mutex> cache_lock(pm->cache_mu);
   const bool cached = p->cache_valid && p->cache_gen == p->gen && p->cache_A == x.A &&
@@ -601,6 +609,8 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
   prm.aux_in = static_cast<const uint32_t*>(x.aux_in);
   prm.aux_out2 = x.aux_out2;
   prm.aux_in2 = x.aux_in2;
+  prm.residual = x.residual;
+  prm.act = p->act;
   prm.status = p->d_status;
   prm.wait_limit_ns = p->wait_limit_ns;
   prm.drop_load = p->drop_load;
@@ -660,6 +670,7 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
     case gf::EPI_SWIGLU:
     case gf::EPI_SWIGLU_SAVE:
     case gf::EPI_DSWIGLU: err = gf::launch_swiglu(e, la); break;
+    case gf::EPI_RESIDUAL: err = gf::launch_residual(la); break;
     default: return fail(GF_ERR_INVALID_VALUE);
   }
   if (err != cudaSuccess) return fail(GF_ERR_CUDA);
@@ -836,7 +847,7 @@ static gf_status epi_option_check(const gf_plan* p, gf_option option) {
 
 GF_API gf_status gf_plan_set_option(gf_plan* p, gf_option option, int64_t value) {
   if (!p) return fail(GF_ERR_INVALID_VALUE);
-  if (p->epi >= gf::EPI_FP8) {
+  if (!gf::epi_gemm(p->epi)) {
     const gf_status st = epi_option_check(p, option);
     if (st != GF_OK) return fail(st);
     if (option == GF_OPT_KERNEL) {
@@ -976,7 +987,7 @@ GF_API gf_status gf_matmul_autotune(gf_plan* p, const void* A, const void* B, co
 GF_API gf_status gf_plan_describe(const gf_plan* p, int32_t* tile_m, int32_t* tile_n,
                                   int32_t* stages, int32_t* grid, int64_t* workspace_bytes) {
   if (!p) return fail(GF_ERR_INVALID_VALUE);
-  if (p->epi >= gf::EPI_FP8) {
+  if (!gf::epi_gemm(p->epi)) {
     if (tile_m) *tile_m = p->epi == gf::EPI_MOE ? p->chunk_tokens : p->tile_rows;
     if (tile_n) *tile_n = p->tile_n;
     if (stages) *stages = p->stages;
@@ -997,6 +1008,11 @@ GF_API gf_status gf_plan_launches(const gf_plan* p, int32_t* launches) {
   if (!p || !launches) return fail(GF_ERR_INVALID_VALUE);
   if (p->epi == gf::EPI_MOE) {
     *launches = p->fused ? 1 : 2;  // sort, copies
+    return GF_OK;
+  }
+  if (p->epi == gf::EPI_ROUTE || p->epi == gf::EPI_NORM || p->epi == gf::EPI_DACT) {
+    // the gradient of a bias has its sums added by a second kernel
+    *launches = p->m == 0 || p->n == 0 ? 0 : p->epi == gf::EPI_DACT ? 2 : 1;
     return GF_OK;
   }
   const bool finalize = has_bgrad(p->epi) && p->bgrad_mode != GF_BGRAD_ATOMIC;
@@ -1031,6 +1047,25 @@ GF_API gf_status gf_dswiglu_execute(const gf_plan* p, const void* dout, const vo
                                     struct CUstream_st* stream) {
   if (!p || p->epi != gf::EPI_DSWIGLU) return fail(GF_ERR_INVALID_VALUE);
   ExecArgs x = {dout, Wd, nullptr, nullptr, d_gate, g, u, d_up, nullptr, nullptr};
+  return execute_impl(p, x, reinterpret_cast<cudaStream_t>(stream));
+}
+
+GF_API gf_plan* gf_matmul_residual_plan(int64_t m, int64_t n, int64_t k, gf_dtype dtype,
+                                        gf_activation act, gf_b_layout b_layout) {
+  if (act < GF_ACT_NONE || act > GF_ACT_SILU) {
+    fail(GF_ERR_INVALID_VALUE);
+    return nullptr;
+  }
+  gf_plan* p = plan_create(m, n, k, dtype, gf::EPI_RESIDUAL, GF_BIAS_COL, b_layout);
+  if (p) p->act = act;
+  return p;
+}
+
+GF_API gf_status gf_matmul_residual_execute(const gf_plan* p, const void* A, const void* B,
+                                            const void* bias, const void* residual, void* out,
+                                            void* z_out, struct CUstream_st* stream) {
+  if (!p || p->epi != gf::EPI_RESIDUAL) return fail(GF_ERR_INVALID_VALUE);
+  ExecArgs x = {A, B, nullptr, bias, out, nullptr, nullptr, z_out, nullptr, nullptr, residual};
   return execute_impl(p, x, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -67,8 +67,9 @@ typedef enum gf_status {
 } gf_status;
 
 typedef enum gf_dtype {
-  GF_F16 = 0, /* IEEE binary16 in and out */
-  GF_BF16 = 1 /* bfloat16 in and out      */
+  GF_F16 = 0,  /* IEEE binary16 in and out */
+  GF_BF16 = 1, /* bfloat16 in and out      */
+  GF_F32 = 2  /* IEEE binary32: a router's logits only */
 } gf_dtype;
 
 typedef enum gf_epilog {
@@ -211,6 +212,149 @@ GF_API gf_plan* gf_dswiglu_plan(int64_t m, int64_t n, int64_t k, gf_dtype dtype)
 GF_API gf_status gf_dswiglu_execute(const gf_plan* plan, const void* dout, const void* Wd,
                                     const void* g, const void* u, void* d_gate, void* d_up,
                                     struct CUstream_st* stream);
+
+/*
+ * A product with its bias, an activation and a residual in one kernel, the last
+ * step of a block that adds to a residual stream:
+ *   z   = A . B + bias,   out = act(z) + residual
+ * in fp32, rounded once. The activation and the residual's addition run on the
+ * accumulator while it is on chip; neither z nor act(z) goes through memory (z only
+ * if z_out asks for it).
+ *
+ * m, n, k, dtype, b_layout: as gf_matmul_plan_ex. Options: as its plans, and
+ * GF_OPT_KERNEL 4, the kernel for few rows; gf_matmul_autotune does not take it.
+ */
+typedef enum gf_activation {
+  GF_ACT_NONE = 0, /* act(z) = z                                             */
+  GF_ACT_RELU = 1, /* max(z, 0)                                              */
+  GF_ACT_GELU = 2, /* GELU in its tanh form                                  */
+  GF_ACT_SILU = 3  /* z / (1 + e^-z)                                         */
+} gf_activation;
+
+GF_API gf_plan* gf_matmul_residual_plan(int64_t m, int64_t n, int64_t k, gf_dtype dtype,
+                                        gf_activation act, gf_b_layout b_layout);
+
+/*
+ * A, B: as gf_matmul_execute. bias: device, n elements of dtype, or NULL: none.
+ * residual, out: device [m, n] of dtype; they may be the same array, which then holds
+ * the sum. z_out: device [m, n] of dtype, or NULL: z is not kept (gf_dact_bgrad
+ * takes it). Otherwise outputs overlap neither each other nor an input. One kernel launch,
+ * asynchronous on stream; errors as gf_matmul_execute. The plan's workspace is
+ * shared by its calls: one stream at a time.
+ */
+GF_API gf_status gf_matmul_residual_execute(const gf_plan* plan, const void* A, const void* B,
+                                            const void* bias, const void* residual, void* out,
+                                            void* z_out, struct CUstream_st* stream);
+
+/*
+ * The gradients of that call up to its product: with d_out the gradient of out,
+ * which is the residual's as well,
+ *   d_z = d_out * act'(z),   bgrad[j] = sum_i d_z[i][j]  (fp32, before rounding)
+ * d_z goes on into the products of the gradients of A and B. act'(z) of ReLU is 1 for
+ * z > 0, else 0. Sums run in an order that the plan fixes: the same bits every time.
+ *
+ * m, n: 0 <= m, n < 2^31, n % 8 == 0 (else GF_ERR_UNSUPPORTED). d_out, z, d_z: device
+ * [m, n] of dtype; d_z may be d_out or z. bgrad: device fp32 [n], or NULL: not
+ * wanted. GF_ACT_NONE: z and d_z are NULL (d_z is d_out) and bgrad is not. One launch,
+ * two with bgrad; asynchronous on stream. Options: GF_OPT_PDL. The plan's workspace
+ * is shared by its calls: one stream at a time.
+ */
+GF_API gf_plan* gf_dact_bgrad_plan(int64_t m, int64_t n, gf_dtype dtype, gf_activation act);
+GF_API gf_status gf_dact_bgrad_execute(const gf_plan* plan, const void* d_out, const void* z,
+                                       void* d_z, float* bgrad, struct CUstream_st* stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it, in 16
+ * bits or as the e4m3 operand of gf_fp8_matmul:
+ *   r = x + residual rounded to dtype (x, without a residual)
+ *   y = r * weight / sqrt(mean(r^2) + eps)
+ * y is of r as it is stored. Sums and y are fp32 (the mean of r^2 has to be within
+ * its range), rounded once.
+ *
+ * rows >= 0, 1 <= hidden <= 32768 (more: GF_ERR_UNSUPPORTED), eps >= 0 and finite.
+ * Options: GF_OPT_PDL.
+ */
+GF_API gf_plan* gf_rmsnorm_plan(int64_t rows, int64_t hidden, gf_dtype dtype, float eps);
+
+/*
+ * x: device [rows, hidden] of dtype; residual: the same, or NULL: none; weight:
+ * device, hidden elements of dtype. residual_out: device [rows, hidden], or NULL: r
+ * is not kept (NULL without a residual, when r is x). out: y in dtype. out8 and
+ * out_scale: y as gf_fp8_quantize with block_rows 1 would hold it, from the fp32 y:
+ * e4m3 bytes [rows, hidden], fp32 [rows, ceil(hidden / 128)]; hidden % 16 == 0, else
+ * GF_ERR_UNSUPPORTED. Either out or out8 or both; out8 and out_scale go together. The scales are those
+ * of 64-bit arithmetic, also where a block's largest y lies next to the border of
+ * two. residual_out and out may each be x or residual; outputs do not overlap
+ * otherwise. 16-byte aligned (out_scale: 4). One launch, asynchronous on stream.
+ */
+GF_API gf_status gf_rmsnorm_execute(const gf_plan* plan, const void* x, const void* residual,
+                                    const void* weight, void* residual_out, void* out, void* out8,
+                                    float* out_scale, struct CUstream_st* stream);
+
+/*
+ * Its gradients, from the gradient d_out of y and, along the residual stream,
+ * d_residual of r (NULL: none). With h = r / sqrt(mean(r^2) + eps) and g = d_out * weight:
+ *   d_x = (g - h mean(g h)) / sqrt(mean(r^2) + eps) + d_residual
+ *   d_weight = sum over the rows of d_out * h
+ * d_x is the gradient of x and of the residual alike. r: residual_out of the
+ * forward (x, without a residual); nothing else of the forward is needed. d_x: device [rows,
+ * hidden] of dtype, may be d_out or d_residual. d_weight: device fp32 [hidden], or NULL: not
+ * wanted; its sums run in an order that the plan fixes. One launch, two with d_weight;
+ * asynchronous on stream. The plan's workspace is shared by its calls: one stream
+ * at a time.
+ */
+GF_API gf_status gf_rmsnorm_grad_execute(const gf_plan* plan, const void* d_out, const void* r,
+                                         const void* weight, const void* d_residual, void* d_x,
+                                         float* d_weight, struct CUstream_st* stream);
+
+/*
+ * A router's choice: each token's experts and their weights, from its logits l.
+ *   s = softmax(l), or 1 / (1 + e^-l) for each expert (gf_score), over the experts
+ *   c = s + bias; without a bias experts are compared by l, which has their order
+ * An expert is left out where l or c is -inf. With groups > 1 the experts are in `groups`
+ * groups of as many consecutive ones, and only those of the topk_groups best groups
+ * are chosen from: a group's score is its best c (group_best 1) or the sum of its two
+ * best (2; of s without a bias; of one where it has no second). Then
+ *   expert[t][0 .. topk - 1] = the experts of the largest c, the largest first
+ *   weight[t][j] = scale * s[expert[t][j]], renorm: over the sum of the token's chosen s
+ * Of equal ones the lowest index goes first, experts and groups. Slots that find no
+ * expert left get -1 and weight 0 (gf_moe_dispatch drops them). NaN ranks above every
+ * number, and is in the weights what the formulas make of it. Scores that fp32 does not tell
+ * apart are compared in 64 bits. Chosen scores that sum to 0 have the weights 0 and
+ * pass no gradient.
+ * Logits and scores are fp32 whatever dtype is.
+ *
+ * tokens >= 0, 1 <= experts <= 1024, 1 <= topk <= 64, tokens * topk < 2^31, topk at most the
+ * experts of topk_groups groups, groups a divisor of experts, else GF_ERR_INVALID_VALUE; at most 32
+ * groups, else GF_ERR_UNSUPPORTED. dtype: of the logits, GF_F32 too. ld: elements
+ * between the rows of logits and of d_logits, experts <= ld <= 2^24 (a router's product
+ * may have more columns than there are experts). Options: GF_OPT_PDL; no workspace.
+ */
+typedef enum gf_score { GF_SCORE_SOFTMAX = 0, GF_SCORE_SIGMOID = 1 } gf_score;
+
+GF_API gf_plan* gf_route_plan(int64_t tokens, int64_t experts, int64_t topk, gf_dtype dtype,
+                              gf_score score, int32_t renorm, float scale, int64_t groups,
+                              int64_t topk_groups, int32_t group_best, int64_t ld);
+
+/*
+ * logits: device [tokens, ld] of dtype, of which the first `experts` columns are
+ * read; bias: device fp32 [experts], or NULL: none. expert: device int32 [tokens,
+ * topk] and weight: device fp32 [tokens, topk], what gf_moe_dispatch and gf_moe_combine
+ * take. 16-byte aligned (bias: 4). One launch, asynchronous on stream.
+ */
+GF_API gf_status gf_route_execute(const gf_plan* plan, const void* logits, const float* bias,
+                                  int32_t* expert, float* weight, struct CUstream_st* stream);
+
+/*
+ * The gradient of the logits from that of the weights, the choice held (the bias
+ * takes part in the choice alone). expert: of the forward; entries outside [0,
+ * experts) have no part, and the d_weight beside them is not used. d_weight: device fp32
+ * [tokens, topk] (of gf_moe_combine_grad); d_logits: device [tokens, ld] of dtype, columns from
+ * `experts` on set to 0. One launch, asynchronous on stream.
+ */
+GF_API gf_status gf_route_grad_execute(const gf_plan* plan, const void* logits,
+                                       const int32_t* expert, const float* d_weight,
+                                       void* d_logits, struct CUstream_st* stream);
 
 /*
  * Mixture-of-experts routing: the rows of a token batch, sorted by expert and
