@@ -6,17 +6,21 @@
 //   weight = scale s (/ the sum of the token's chosen s)
 //
 // One warp a token: a lane holds consecutive experts of one group, so that lanes
-// and experts are in the same order and the lowest lane that has the maximum has the
-// lowest expert. Of each pick every lane takes part in one warp-wide integer
-// maximum over order-preserving keys; only the lane that loses its best looks again.
+// and experts are in the same order. Scores become order-preserving integers whose
+// last bits are the place within the lane, so that a lane sorts its experts by
+// minimum and maximum alone, a pick is one warp-wide integer maximum and the lowest
+// lane that has it, and the lane that loses its best moves up the others. What bounds
+// it is instructions (some 400 a token of 256 experts) and, for a token, latency.
 //
-// Experts are whole numbers, and scores may lie closer together than fp32 tells
-// them apart. The fp32 comparisons that decide something are therefore looked at
-// again: where two differ by no more than their error bounds, and not for equal
-// inputs, the token is chosen anew in 64 bits. Without a bias, experts are compared
-// by their logits, exactly.
+// Experts are whole numbers, and scores may lie closer together than fp32, less the
+// bits of the place, tells them apart. The comparisons that decide something are
+// therefore looked at again: where two differ by no more than their error bounds, and
+// not for equal inputs, those in question are compared in 64 bits (a few in a thousand
+// tokens of 256 experts with a bias). Without a bias experts are compared by their
+// logits; those of 16 bits leave the place's bits free and are exact at once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 
 #include <type_traits>
@@ -36,29 +40,65 @@ __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float as_float(float v) { return v; }
 
-// Order-preserving keys: NaN above everything (as it would spread), -inf 0.
-__device__ __forceinline__ uint32_t key_of(float v) {
-  if (v != v) return 0xFFFFFFFFu;
-  if (v == -INFINITY) return 0u;
-  const uint32_t b = __float_as_uint(v + 0.f);  // -0 is 0
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+// Order-preserving integers of scores: NaN above everything (as it would spread:
+// arithmetic leaves the positive one), -inf and what is not there below kNone. The
+// last bits are taken by the place i in the lane, the first place the largest.
+constexpr int kNone = static_cast<int>(0x80800000u);  // of the lowest finite value
+
+__device__ __forceinline__ int ordered(int bits) { return bits ^ ((bits >> 31) & 0x7FFFFFFF); }
+
+template <int MASK>
+__device__ __forceinline__ int key_of(float v, int i) {
+  return (ordered(__float_as_int(v + 0.f)) & ~MASK) | (MASK - i);  // (-0 becomes 0)
 }
-// (of a key that is not 0 or NaN's)
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+// the value, less the place's bits
+template <int MASK>
+__device__ __forceinline__ float value_of(int key) {
+  if (key < kNone) return -INFINITY;
+  return __int_as_float(ordered(key & ~MASK));
 }
-__device__ __forceinline__ float value_or(uint32_t key) {
-  return key == 0u ? -INFINITY : key == 0xFFFFFFFFu ? NAN : value_of(key);
+
+// largest first: Batcher's odd-even merge sort (1968)
+template <int N>
+__device__ __forceinline__ void sort_keys(int (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int a = k[i + j], b = k[i + j + q];
+            k[i + j] = max(a, b);
+            k[i + j + q] = min(a, b);
+          }
 }
 
 // 1 / (1 + e^-l) without overflow, in the accuracy that the weights take
 __device__ __forceinline__ float logistic(float l) {
   const float e = expf(-fabsf(l));
-  return (l >= 0.f ? 1.f : e) / (1.f + e);
+  return __fdividef(l >= 0.f ? 1.f : e, 1.f + e);
 }
 __device__ __forceinline__ double logistic(double l) {
   const double e = exp(-fabs(l));
   return (l >= 0. ? 1. : e) / (1. + e);
+}
+
+// a score as it is compared in fp32: e^x by the hardware exponential and the
+// hardware reciprocal, small results flushed
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float fast_score(const RouteParams& p, float x, float top, float inv) {
+  if (!p.sigmoid) return exp_fast(x - top) * inv;
+  const float e = exp_fast(-fabsf(x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return (x >= 0.f ? 1.f : e) * r;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -98,6 +138,105 @@ __device__ __forceinline__ void warp_best(double& v, int& i) {
   }
 }
 
+// The largest logit and the sum of softmax's exponentials in 64 bits, by a whole warp.
+template <typename L>
+__device__ __forceinline__ void exact_softmax(const RouteParams& p, const L* row, double& top,
+                                              double& total) {
+  const int lane = threadIdx.x & 31;
+  top = -INFINITY;
+  for (int e = lane; e < p.experts; e += 32) top = fmax(top, static_cast<double>(as_float(row[e])));
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, d));
+  if (top == -INFINITY) top = 0.;
+  double sum = 0.;
+#pragma unroll 4
+  for (int e = lane; e < p.experts; e += 32) sum += exp(static_cast<double>(as_float(row[e])) - top);
+  total = warp_sum(sum);
+}
+
+// Whether this lane's group is one of the best, in 64 bits. Groups whose fp32 score
+// lies between `low` and `high` are in question, the others keep theirs; of them only
+// experts whose fp32 score is at least `least` may be among the two best.
+template <typename L>
+__device__ __noinline__ bool groups_exactly(const RouteParams& p, const L* row, int base, int count,
+                                            float score32, float low, float high, float least,
+                                            float top32, float inv) {
+  const int lane = threadIdx.x & 31;
+  double top = 0., total = 1.;
+  const bool by_logit = p.bias == nullptr && p.group_best == 1;
+  if (!p.sigmoid && !by_logit) exact_softmax(p, row, top, total);
+  const bool asked = !(score32 < low) && !(score32 > high);
+  uint64_t left = 0ull;  // places of experts to look at
+  for (int i = 0; i < count && asked; ++i) {
+    const float l = as_float(row[base + i]);
+    const float add = p.bias != nullptr ? p.bias[base + i] : 0.f;
+    const float c32 = by_logit ? l : fast_score(p, l, top32, inv) + add;
+    if (!(c32 < least) && c32 != -INFINITY && l != -INFINITY) left |= 1ull << i;
+  }
+  double a = -INFINITY, b = -INFINITY;
+  while (__any_sync(kAll, left != 0ull)) {
+    if (left == 0ull) continue;
+    const int i = __ffsll(static_cast<long long>(left)) - 1;
+    left &= left - 1ull;
+    double c = as_float(row[base + i]);
+    if (!by_logit) {
+      c = p.sigmoid ? logistic(c) : exp(c - top) / total;
+      if (p.bias != nullptr) c += static_cast<double>(p.bias[base + i]);
+    }
+    if (before(c, 0, a, a == -INFINITY ? -1 : 1)) {
+      b = a;
+      a = c;
+    } else if (before(c, 0, b, b == -INFINITY ? -1 : 1)) {
+      b = c;
+    }
+  }
+  for (int d = 1; d < 1 << p.lane_shift; d <<= 1) {
+    const double oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
+    const bool mine = before(a, 0, oa, oa == -INFINITY ? -1 : 1);
+    const double less = mine ? oa : a, second = mine ? b : ob;
+    a = mine ? a : oa;
+    b = before(less, 0, second, second == -INFINITY ? -1 : 1) ? less : second;
+  }
+  double score = asked ? a : static_cast<double>(score32);
+  if (asked && p.group_best == 2 && b != -INFINITY) score += b;
+  const int g = lane >> p.lane_shift;
+  int rank = 0;
+  for (int h = 0; h < p.groups; ++h) {
+    const double other = __shfl_sync(kAll, score, h << p.lane_shift);
+    rank += h != g && before(other, h, score, g) ? 1 : 0;
+  }
+  return g < p.groups && rank < p.topk_groups;
+}
+
+// The order of up to 32 experts, one a lane (`expert` -1: none), in 64 bits: returns
+// the one of rank `lane`.
+template <typename L>
+__device__ __noinline__ int order_exactly(const RouteParams& p, const L* row, int expert, int n) {
+  const int lane = threadIdx.x & 31;
+  double top = 0., total = 1.;
+  if (!p.sigmoid && p.bias != nullptr) exact_softmax(p, row, top, total);
+  double c = 0.;
+  if (expert >= 0) {
+    c = as_float(row[expert]);
+    if (p.bias != nullptr)
+      c = (p.sigmoid ? logistic(c) : exp(c - top) / total) + static_cast<double>(p.bias[expert]);
+  }
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const double v = __shfl_sync(kAll, c, j);
+    const int e = __shfl_sync(kAll, expert, j);
+    rank += before(v, e, c, expert) ? 1 : 0;
+  }
+  int out = -1;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const int where = __shfl_sync(kAll, rank, j), e = __shfl_sync(kAll, expert, j);
+    if (where == lane && e >= 0) out = e;
+  }
+  return out;
+}
+
 // The choice of one token in 64 bits, by a whole warp: expert number j of it goes
 // to slot j (lane j, or lane j - 32's second). Lane i looks after the experts i,
 // i + 32, ..., and after group i.
@@ -105,16 +244,8 @@ template <typename L>
 __device__ __noinline__ void choose_exactly(const RouteParams& p, const L* row, int& first,
                                             int& second) {
   const int lane = threadIdx.x & 31;
-  double total = 1., top = -INFINITY;
-  if (!p.sigmoid) {
-    for (int e = lane; e < p.experts; e += 32) top = fmax(top, static_cast<double>(as_float(row[e])));
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, d));
-    if (top == -INFINITY) top = 0.;
-    double sum = 0.;
-    for (int e = lane; e < p.experts; e += 32) sum += exp(static_cast<double>(as_float(row[e])) - top);
-    total = warp_sum(sum);
-  }
+  double total = 1., top = 0.;
+  if (!p.sigmoid) exact_softmax(p, row, top, total);
   auto score = [&](double l) { return p.sigmoid ? logistic(l) : exp(l - top) / total; };
   double c[32];  // of this lane's experts
   for (int i = 0; i < 32; ++i) {
@@ -213,223 +344,244 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, const L* row, 
   for (int i = 0; i < VPL; ++i) l[i] = i < count ? as_float(row[first + i]) : -INFINITY;
 }
 
-template <typename L, int VPL>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteParams p) {
+// CTAs of an SM (the grid is as large: warps loop over the tokens)
+constexpr int resident(int vpl) { return vpl <= 8 ? 6 : vpl <= 16 ? 5 : 2; }
+
+// BIAS: scores are compared, else logits.
+template <typename L, int VPL, bool BIAS>
+__global__ void __launch_bounds__(32 * kWarps, resident(VPL))
+    route_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int MASK = VPL - 1;
+  constexpr int S = VPL >= 32 ? 2 : 1;  // slots a lane: the instances for more than 32 have two
+  // keys tell everything apart but what is equal
+  constexpr bool kExact = !BIAS && sizeof(L) == 2;
+  // what the place's bits take from a value, relative to it
+  constexpr float kCut = 1.2e-7f * VPL;
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  __shared__ int2 slot_of[kWarps][kMaxSlots + 2];
+  int2* slots = slot_of[threadIdx.x >> 5];
+  const uint32_t below = (1u << lane) - 1u;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t token = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (token >= p.tokens) return;
-  const L* row = static_cast<const L*>(p.logits) + token * p.ld;
   // this lane's experts
-  const int g = lane / p.lanes, in_group = (lane - g * p.lanes) * p.per_lane;
+  const int g = lane >> p.lane_shift, lane_mask = (1 << p.lane_shift) - 1;
+  const int in_group = (lane & lane_mask) * p.per_lane;
   const int base = g * p.group_size + in_group;
   int count = g < p.groups ? min(p.per_lane, p.group_size - in_group) : 0;
   if (count < 0) count = 0;
-  float l[VPL];
-  load_logits<L, VPL>(p, row, base, count, l);
-
-  const bool bias = p.bias != nullptr;
+  float bias[BIAS ? VPL : 1];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) bias[i] = i < count ? p.bias[base + i] : 0.f;
+  }
   const bool grouped = p.groups > 1;
   const bool sums = grouped && p.group_best == 2;
-  // the largest logit, and the sum that all scores are divided by
-  float top = 0.f, inv = 1.f;
-  if (!p.sigmoid) {
-    float m = l[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-    top = value_or(__reduce_max_sync(kAll, m != m ? 0u : key_of(m)));  // (of those that are numbers)
-    if (top == -INFINITY) top = 0.f;
-    if (bias || sums || !p.renorm) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += __expf(l[i] - top);
-      inv = 1.f / warp_sum(sum);
-    }
-  }
-  // scores as they are compared, and their error: of the exponential (2^-22 of it
-  // and 2^-23 |x|), the sum and the division. |x| e^x <= 0.4 bounds the error by
-  // a part of the largest score, which is `inv` for softmax and 1 for sigmoid.
-  auto fast = [&](float x) {
-    if (!p.sigmoid) return __expf(x - top) * inv;
-    const float e = __expf(-fabsf(x));
-    return __fdividef(x >= 0.f ? 1.f : e, 1.f + e);
-  };
-  const float error = p.sigmoid ? 6e-7f : inv * (1.1e-6f + VPL * 6e-8f);
-  uint32_t key[VPL];
-  bool doubt = false;
-  if (bias || sums) {
-    float c[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      c[i] = l[i] == -INFINITY ? l[i] : fast(l[i]);
-      if (bias && i < count && l[i] != -INFINITY) c[i] += p.bias[base + i];
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = key_of(c[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = key_of(l[i]);
-  }
-  if (grouped) {
-    // the group's two best, over this lane's experts and then its lanes
-    uint32_t a = 0u, b = 0u;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      b = max(b, min(a, key[i]));
-      a = max(a, key[i]);
-    }
-    for (int d = 1; d < p.lanes; d <<= 1) {
-      const uint32_t oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
-      b = max(max(b, ob), min(a, oa));
-      a = max(a, oa);
-    }
-    float score = value_or(a);
-    if (sums && b != 0u) score += value_or(b);
-    const uint32_t mine = g < p.groups ? key_of(score) : 0u;
-    int rank = 0;
-    for (int h = 0; h < p.groups; ++h) {
-      const uint32_t other = __shfl_sync(kAll, mine, h * p.lanes);
-      rank += other > mine || (other == mine && h < g) ? 1 : 0;
-    }
-    const bool in = g < p.groups && rank < p.topk_groups;
-    if (bias || sums) {
-      // the worst group that stays and the best that goes
-      const uint32_t lo = ~__reduce_max_sync(kAll, in ? ~mine : 0u);
-      const uint32_t hi = __reduce_max_sync(kAll, in ? 0u : mine);
-      if (hi != 0u) {
-        // rounding errors of sums, by the largest terms of any group
-        const float terms = a == 0u ? 0.f : fabsf(value_or(a)) + (b == 0u ? 0.f : fabsf(value_or(b)));
-        const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(terms)));
-        doubt = !(value_or(lo) - value_or(hi) > 4.f * error + 3e-7f * most);
-      }
-    }
-    if (sums && !bias) {  // the experts themselves by their logits
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = key_of(l[i]);
-    }
-    if (!in) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = 0u;
-    }
-  }
+  const int picks = p.topk + (kExact ? 0 : 1);  // the next one, to compare the last with
 
-  // the picks; slot j is in lane j % 32
-  int expert[2] = {-1, -1};
-  uint32_t picked[2] = {0u, 0u};
-  uint32_t best = 0u;
-  int at = 0;
-  auto look = [&]() {
-    best = key[0];
-    at = 0;
+  float l[VPL];
+  load_logits<L, VPL>(p, static_cast<const L*>(p.logits) + token * p.ld, base, count, l);
+  for (;;) {
+    const L* row = static_cast<const L*>(p.logits) + token * p.ld;
+    // the largest logit, and the sum that all scores are divided by
+    float top = 0.f, inv = 1.f;
+    if (!p.sigmoid) {
+      float m = l[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);  // (of those that are numbers)
+      if (m != m) m = -INFINITY;
+      m = __int_as_float(ordered(__reduce_max_sync(kAll, ordered(__float_as_int(m + 0.f)))));
+      top = m == -INFINITY ? 0.f : m;
+      if (BIAS || sums || !p.renorm) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sum += exp_fast(l[i] - top);
+        inv = 1.f / warp_sum(sum);
       }
     }
-  };
-  look();
-  const int picks = p.topk + (bias ? 1 : 0);  // the next one, to compare the last with
-  uint32_t after = 0u;
-  int after_expert = -1;
-  for (int j = 0; j < picks; ++j) {
-    const uint32_t m = __reduce_max_sync(kAll, best);
-    if (m == 0u) break;
-    const int who = __ffs(__ballot_sync(kAll, best == m)) - 1;
-    const int e = __shfl_sync(kAll, base + at, who);
-    if (j < p.topk) {
-      if (lane == (j & 31)) {
-        if (j < 32) {
-          expert[0] = e;
-          picked[0] = m;
-        } else {
-          expert[1] = e;
-          picked[1] = m;
+    // the error of fast_score: of the exponential (2^-22 of it and 2^-23 |x|), the sum
+    // and the division. |x| e^x <= 0.4 bounds it by a part of the largest score, which
+    // is `inv` for softmax and 1 for sigmoid.
+    const float error = p.sigmoid ? 6e-7f : inv * (1.1e-6f + VPL * 6e-8f);
+    int key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if constexpr (BIAS)
+        key[i] = key_of<MASK>(
+            fast_score(p, l[i], top, inv) + (l[i] == -INFINITY ? -INFINITY : bias[i]), i);
+      else
+        key[i] = key_of<MASK>(l[i], i);
+    }
+    sort_keys<VPL>(key);
+    bool out = false;  // this lane's group goes
+    if (grouped) {
+      // the group's two best, over this lane's experts and then its lanes
+      float a, b;
+      if (!BIAS && sums) {  // sums are of scores, in which the experts are in the same order
+        a = fast_score(p, value_of<MASK>(key[0]), top, inv);
+        b = VPL > 1 ? fast_score(p, value_of<MASK>(key[VPL > 1 ? 1 : 0]), top, inv) : 0.f;
+        if (key[0] < kNone) a = -INFINITY;
+        if (VPL == 1 || key[VPL > 1 ? 1 : 0] < kNone) b = -INFINITY;
+      } else {
+        a = value_of<MASK>(key[0]);
+        b = VPL > 1 ? value_of<MASK>(key[VPL > 1 ? 1 : 0]) : -INFINITY;
+      }
+      int ka = ordered(__float_as_int(a)), kb = ordered(__float_as_int(b));
+      for (int d = 0; d < p.lane_shift; ++d) {
+        const int oa = __shfl_xor_sync(kAll, ka, 1 << d), ob = __shfl_xor_sync(kAll, kb, 1 << d);
+        kb = max(max(kb, ob), min(ka, oa));
+        ka = max(ka, oa);
+      }
+      a = __int_as_float(ordered(ka));
+      b = __int_as_float(ordered(kb));
+      float score = a;
+      if (sums && kb >= kNone) score += b;
+      const int mine = g < p.groups ? ordered(__float_as_int(score + 0.f)) : INT_MIN;
+      // the groups before this one, shared by the group's lanes
+      int rank = 0;
+      for (int h0 = 0; h0 < p.groups; h0 += lane_mask + 1) {
+        const int h = h0 + (lane & lane_mask);
+        const int other = __shfl_sync(kAll, mine, (h << p.lane_shift) & 31);
+        rank += h < p.groups && (other > mine || (other == mine && h < g)) ? 1 : 0;
+      }
+      for (int d = 0; d < p.lane_shift; ++d) rank += __shfl_xor_sync(kAll, rank, 1 << d);
+      bool in = g < p.groups && rank < p.topk_groups;
+      if (!kExact || sums) {
+        // the worst group that stays and the best that goes
+        const int lo = __reduce_min_sync(kAll, in ? mine : INT_MAX);
+        const int hi = __reduce_max_sync(kAll, in ? INT_MIN : mine);
+        if (hi >= kNone) {
+          // rounding errors, by the largest terms of any group
+          const float terms = ka < kNone ? 0.f : fabsf(a) + (kb < kNone ? 0.f : fabsf(b));
+          const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(terms)));
+          const float tol = (BIAS || sums ? 4.f * error + 3e-7f * most : 0.f) + kCut * most;
+          const float worst = __int_as_float(ordered(lo)), first = __int_as_float(ordered(hi));
+          if (!(worst - first > tol))
+            in = groups_exactly<L>(p, row, base, count, score, first - tol, worst + tol,
+                                   (sums ? b : a) - tol, top, inv);
         }
       }
-    } else {
-      after = m;
-      after_expert = e;
+      out = !in;
     }
-    if (lane == who) {
+    if (out) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == at) key[i] = 0u;
-      look();
+      for (int i = 0; i < VPL; ++i) key[i] = INT_MIN;
     }
-  }
-  if (bias) {
-    // each pick against the one after it
+
+    // the picks, each put down by the lane that has it: key and expert
+    __syncwarp();
+    int found = 0;
+    for (; found < picks; ++found) {
+      const int mine = key[0] & ~MASK;
+      const int best = __reduce_max_sync(kAll, mine);
+      if (best < kNone) break;
+      const uint32_t have = __ballot_sync(kAll, mine == best);
+      if (mine == best && (have & below) == 0u) {
+        slots[found] = make_int2(mine, base + (MASK - (key[0] & MASK)));
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+        for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+        key[VPL - 1] = INT_MIN;
+      }
+    }
+    __syncwarp();
+    // the next token's logits come meanwhile
+    const int64_t next = token + step;
+    const bool more = next < p.tokens;
+    if (more) load_logits<L, VPL>(p, row + step * p.ld, base, count, l);
+    int expert[S];
+    float value[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
       const int j = lane + 32 * s;
-      uint32_t next = __shfl_down_sync(kAll, picked[s], 1);
-      int next_e = __shfl_down_sync(kAll, expert[s], 1);
-      if (s == 0) {
-        const uint32_t k32 = __shfl_sync(kAll, picked[1], 0);
-        const int e32 = __shfl_sync(kAll, expert[1], 0);
-        if (lane == 31) {
-          next = k32;
-          next_e = e32;
+      const int2 slot = j < found ? slots[j] : make_int2(INT_MIN, -1);
+      expert[s] = slot.y;
+      value[s] = __int_as_float(ordered(slot.x));
+    }
+    if constexpr (!kExact) {
+      // each pick against the one after it
+      bool doubt = false, edge = false;
+      auto near = [&](float v, float n) {
+        const float most = fmaxf(fabsf(v), fabsf(n));
+        return !(v - n > (BIAS ? 2.f * error + 4e-7f * most : 0.f) + kCut * most);
+      };
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const int j = lane + 32 * s;
+        if (j < p.topk && j + 1 < found) {
+          const int2 follow = slots[j + 1];
+          if (near(value[s], __int_as_float(ordered(follow.x)))) {
+            bool same = __float_as_uint(as_float(row[expert[s]])) ==
+                        __float_as_uint(as_float(row[follow.y]));
+            if (BIAS) same = same && p.bias[expert[s]] == p.bias[follow.y];
+            doubt |= !same;
+            // equal inputs, but the one after them may belong before both
+            edge |= j == p.topk - 1;
+          }
         }
       }
-      if (j == p.topk - 1) {
-        next = after;
-        next_e = after_expert;
-      }
-      if (j < p.topk && picked[s] != 0u && next != 0u) {
-        const float v = value_or(picked[s]), n = value_or(next);
-        if (!(v - n > 2.f * error + 2e-7f * (fabsf(v) + fabsf(n)))) {
-          const bool same = __float_as_uint(as_float(row[expert[s]])) ==
-                                __float_as_uint(as_float(row[next_e])) &&
-                            p.bias[expert[s]] == p.bias[next_e];
-          doubt |= !same;
+      if (__any_sync(kAll, doubt || edge)) {
+        // the picks and the one after them, if the next is further away; else all over
+        bool few = p.topk < 32;
+        if (few && found > p.topk) {
+          const int m = __reduce_max_sync(kAll, key[0] & ~MASK);
+          const float last = __shfl_sync(kAll, value[0], p.topk);
+          few = m < kNone || !near(last, __int_as_float(ordered(m)));
+        }
+        if (few && !__any_sync(kAll, doubt)) {
+          // nothing else comes near
+        } else if (few) {
+          expert[0] = order_exactly<L>(p, row, expert[0], p.topk + 1);
+        } else {
+          int second;
+          choose_exactly<L>(p, row, expert[0], second);
+          if (S == 2) expert[S - 1] = second;
         }
       }
     }
-  }
-  if (__any_sync(kAll, doubt)) choose_exactly<L>(p, row, expert[0], expert[1]);
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (lane + 32 * s >= p.topk) expert[s] = -1;
 
-  // the weights; softmax over the chosen alone where they are renormalised, unless
-  // their scores are 0 in 64 bits too
-  bool none = false;
-  if (!p.sigmoid && p.renorm) {
-    const float of_all = top;
-    float m = -INFINITY;
+    // the weights; softmax over the chosen alone where they are renormalised, unless
+    // their scores are 0 in 64 bits too
+    float x[S], w[S];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (expert[s] >= 0) m = fmaxf(m, as_float(row[expert[s]]));
-    top = value_or(__reduce_max_sync(kAll, key_of(m)));
-    none = top - of_all < kNoScore;
-    if (top == -INFINITY) top = 0.f;
-  }
-  float w[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    w[s] = 0.f;
-    if (expert[s] >= 0) {
-      const float x = as_float(row[expert[s]]);
-      w[s] = p.sigmoid ? logistic(x) : expf(x - top);
-      if (!p.sigmoid && !p.renorm) w[s] *= inv;
+    for (int s = 0; s < S; ++s) x[s] = expert[s] >= 0 ? as_float(row[expert[s]]) : -INFINITY;
+    bool none = false;
+    if (!p.sigmoid && p.renorm) {
+      const float of_all = top;
+      top = warp_max(fmaxf(x[0], x[S - 1]));
+      none = top - of_all < kNoScore;
+      if (top == -INFINITY) top = 0.f;
     }
-  }
-  float factor = p.scale;
-  if (p.renorm) {
-    const float sum = warp_sum(w[0] + w[1]);
-    // (chosen scores that are all 0 stay 0)
-    factor = sum == 0.f || none ? 0.f : p.scale / sum;
-    // a logit without a number (or infinite) makes every score NaN, chosen or not
-    if (inv != inv) factor = inv;
-  }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int j = lane + 32 * s;
-    if (j < p.topk) {
-      p.expert[token * p.topk + j] = expert[s];
-      p.weight[token * p.topk + j] = w[s] * factor;
+    for (int s = 0; s < S; ++s) {
+      w[s] = 0.f;
+      if (expert[s] >= 0) {
+        w[s] = p.sigmoid ? logistic(x[s]) : expf(x[s] - top);
+        if (!p.sigmoid && !p.renorm) w[s] *= inv;
+      }
     }
+    float factor = p.scale;
+    if (p.renorm) {
+      const float sum = warp_sum(S == 2 ? w[0] + w[S - 1] : w[0]);
+      // (chosen scores that are all 0 stay 0)
+      factor = sum == 0.f || none ? 0.f : p.scale / sum;
+      // a logit without a number (or infinite) makes every score NaN, chosen or not
+      if (inv != inv) factor = inv;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int j = lane + 32 * s;
+      if (j < p.topk) {
+        p.expert[token * p.topk + j] = expert[s];
+        p.weight[token * p.topk + j] = w[s] * factor;
+      }
+    }
+    if (!more) return;
+    token = next;
   }
 }
 
@@ -449,7 +601,7 @@ template <>
 __device__ __forceinline__ float to_logit<float>(float v) { return v; }
 
 template <typename L>
-__global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ float rows[];  // [kWarps][experts]
   grid_dep_wait();
   grid_dep_launch();
@@ -548,17 +700,26 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const RoutePara
   for (int64_t e = lane; e < p.ld; e += 32) out[e] = to_logit<L>(e < p.experts ? d[e] : 0.f);
 }
 
+template <typename L, int VPL>
+cudaError_t route_of(const RouteParams& p, cudaStream_t stream, int pdl) {
+  // as many CTAs as are resident at once; more tokens follow in their loop
+  const int64_t all = (static_cast<int64_t>(p.tokens) + kWarps - 1) / kWarps;
+  const int64_t most = static_cast<int64_t>(p.sms) * resident(VPL);
+  const dim3 grid(static_cast<unsigned>(all < most ? all : most)), block(32 * kWarps);
+  return p.bias != nullptr ? launch_pdl(route_kernel<L, VPL, true>, grid, block, 0, stream, pdl, p)
+                           : launch_pdl(route_kernel<L, VPL, false>, grid, block, 0, stream, pdl, p);
+}
+
 template <typename L>
 cudaError_t route(const RouteParams& p, cudaStream_t stream, int pdl) {
-  const dim3 grid((p.tokens + kWarps - 1) / kWarps), block(32 * kWarps);
-  const int n = p.per_lane;
-  if (n <= 1) return launch_pdl(route_kernel<L, 1>, grid, block, 0, stream, pdl, p);
-  if (n <= 2) return launch_pdl(route_kernel<L, 2>, grid, block, 0, stream, pdl, p);
-  if (n <= 4) return launch_pdl(route_kernel<L, 4>, grid, block, 0, stream, pdl, p);
-  if (n <= 8) return launch_pdl(route_kernel<L, 8>, grid, block, 0, stream, pdl, p);
-  if (n <= 16) return launch_pdl(route_kernel<L, 16>, grid, block, 0, stream, pdl, p);
-  if (n <= 32) return launch_pdl(route_kernel<L, 32>, grid, block, 0, stream, pdl, p);
-  return launch_pdl(route_kernel<L, 64>, grid, block, 0, stream, pdl, p);
+  const int n = p.topk > 32 && p.per_lane < 32 ? 32 : p.per_lane;  // two slots a lane
+  if (n <= 1) return route_of<L, 1>(p, stream, pdl);
+  if (n <= 2) return route_of<L, 2>(p, stream, pdl);
+  if (n <= 4) return route_of<L, 4>(p, stream, pdl);
+  if (n <= 8) return route_of<L, 8>(p, stream, pdl);
+  if (n <= 16) return route_of<L, 16>(p, stream, pdl);
+  if (n <= 32) return route_of<L, 32>(p, stream, pdl);
+  return route_of<L, 64>(p, stream, pdl);
 }
 
 template <typename L>
