@@ -45,6 +45,7 @@ struct gf_plan {
   void* d_splitk;        // split-k partial sums, then the per-tile counters
   size_t splitk_bytes;   // capacity of d_splitk
   size_t splitk_cnt_offset;
+  int narrow;            // RESIDUAL: the kernel for few rows, with tile_rows rows a tile
   int pdl;               // 1: launches overlap their set-up with the previous kernel
   // Tensor maps of the last execute, reused while the operand pointers and
   // the plan's tiling are unchanged (encoding them is host work on every

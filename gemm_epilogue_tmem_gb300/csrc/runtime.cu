@@ -22,6 +22,7 @@
 #include "launch.h"
 #include "params.h"
 #include "plan.h"
+#include "residual_narrow.h"
 #include "runtime_internal.h"
 
 namespace {
@@ -147,6 +148,49 @@ bool encode_2d(CUtensorMap* map, const void* ptr, gf_dtype dt, uint64_t inner, u
   return r == CUDA_SUCCESS;
 }
 
+// The CTAs that share a tile of the kernel for few rows, a cluster: as many as can be
+// resident for all tiles at once, with two k-blocks each at least. Above four, tiles of
+// 64 rows want longer parts for what it costs to join them (us, four and eight CTAs: 64
+// rows, 4096 columns, k = 4096 10.3 and 12.8; 512 columns, k = 8192 13.7 and 10.8).
+int narrow_splits(const gf_plan* p, int rows, int64_t tiles) {
+  int splits = p->forced_split > 0 ? p->forced_split : gf::kNarrowMaxSplits;
+  if (splits > gf::kNarrowMaxSplits) splits = gf::kNarrowMaxSplits;
+  for (; splits > 1; --splits) {
+    const int least = p->forced_split > 0 ? 1 : rows == 64 && splits > 4 ? 16 : 2;
+    if (splits * least <= p->num_k_blocks && gf::narrow_clusters(rows, splits) >= tiles) break;
+  }
+  return splits;
+}
+
+// RESIDUAL: whether the kernel for few rows, tiles of up to 64 rows and 128 columns, takes
+// the product, and its tiling. Without the caller's choice it takes up to 64 rows, and up to
+// 128 where its tiles, then two for each 128 columns, are so few that clusters share them. us,
+// this kernel and the single-CTA one, k = 17408, 5120 columns, 1 row 29 and 47, 32 rows 32 and 40,
+// 64 rows 36 and 41, 128 rows 40 and 42; 12288 columns, k = 4096, 128 rows (tiles not shared) 27 and 25.
+bool plan_narrow(gf_plan* p) {
+  if (p->epi != gf::EPI_RESIDUAL) return false;
+  const bool asked = p->forced_kernel == 4;
+  if (!asked && (p->forced_kernel != 0 || p->forced_tile_n != 0 || p->forced_split != 0 || p->m > 128))
+    return false;
+  const int rows = gf::narrow_rows(p->m);
+  const int64_t row_tiles = (p->m + rows - 1) / rows, tiles = row_tiles * ((p->n + 127) / 128);
+  const int splits = narrow_splits(p, rows, tiles);
+  if (!asked && row_tiles > 1 && splits == 1) return false;
+  if (tiles * splits > kMaxDim) return false;
+  p->narrow = 1;
+  p->pair = p->wide = 0;
+  p->tile_rows = rows;
+  p->tile_n = 128;
+  p->stages = gf::narrow_stages(p->tile_rows);
+  p->num_m_blocks = static_cast<int>(row_tiles);
+  p->num_n_blocks = static_cast<int>((p->n + 127) / 128);
+  p->num_tiles = static_cast<int>(tiles);
+  p->k_splits = splits;
+  p->kb_per_split = (p->num_k_blocks + splits - 1) / splits;
+  p->grid = static_cast<int>(tiles * splits);
+  return true;
+}
+
 void plan_tiles(gf_plan* p) {
   const bool dual = gf::epi_dual(p->epi);
   const int64_t mblocks = (p->m + kBM - 1) / kBM;
@@ -227,6 +271,8 @@ void plan_tiles(gf_plan* p) {
     if (p->forced_group_m == 0) p->group_m = 4;
   }
   p->split_from = 0;
+  p->narrow = 0;
+  if (plan_narrow(p)) return;
   if (pair) {
     p->tile_n = pair_n;
     p->stages = gf::stages_for(pair_n, 1, p->epi);
@@ -310,7 +356,7 @@ void plan_tiles(gf_plan* p) {
 // [tiles][splits][tile_n / 4][128] float4, then one zeroed counter per tile. Grown when
 // too small; on failure the plan falls back to no split.
 gf_status ensure_splitk(gf_plan* p) {
-  if (p->k_splits < 2) return GF_OK;
+  if (p->k_splits < 2 || p->narrow) return GF_OK;  // (few rows: joined in shared memory)
   // partial sums per split tile, or per (split tile, CTA rank) for the pair kernel
   const size_t parts = p->pair ? 2 * static_cast<size_t>(p->num_tiles - p->split_from)
                                : static_cast<size_t>(p->num_tiles);
@@ -552,7 +598,8 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
     b_mn_3d = p->cache_b_mn_3d;
   } else {
     if (p->k > 0) {
-      if (!encode_2d(&tmA, x.A, p->dtype, p->k, p->m, 64, kBM)) return fail(GF_ERR_INVALID_VALUE);
+      if (!encode_2d(&tmA, x.A, p->dtype, p->k, p->m, 64, p->narrow ? p->tile_rows : kBM))
+        return fail(GF_ERR_INVALID_VALUE);
       // K-major B boxes: a pair CTA loads half of the tile's columns, or with
       // two B operands all of the tile's columns of one operand; the wide
       // tiles load 128-row parts
@@ -617,7 +664,9 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
   prm.l2_hint_a = p->l2_hint_a;
   prm.l2_hint_b = p->l2_hint_b;
   prm.b_mn_3d = b_mn_3d ? 1 : 0;
-  if (p->k_splits > 1) {
+  if (p->narrow) {
+    prm.k_splits = p->k_splits;
+  } else if (p->k_splits > 1) {
     prm.split_from = p->split_from;
     prm.k_splits = p->k_splits;
     prm.kb_per_split = p->kb_per_split;
@@ -650,7 +699,7 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
   la.grid = p->grid;
   la.bf16 = p->dtype == GF_BF16 ? 1 : 0;
   la.b_mn = p->b_layout == GF_B_KN ? 1 : 0;
-  la.tile_n = p->tile_n;
+  la.tile_n = p->narrow ? p->tile_rows : p->tile_n;
   la.pair = p->pair;
   la.wide = p->wide;
   la.split = p->pair && p->k_splits > 1 ? 1 : 0;
@@ -670,7 +719,7 @@ gf_status execute_impl(const gf_plan* p, const ExecArgs& x, cudaStream_t st) {
     case gf::EPI_SWIGLU:
     case gf::EPI_SWIGLU_SAVE:
     case gf::EPI_DSWIGLU: err = gf::launch_swiglu(e, la); break;
-    case gf::EPI_RESIDUAL: err = gf::launch_residual(la); break;
+    case gf::EPI_RESIDUAL: err = p->narrow ? gf::launch_residual_narrow(la) : gf::launch_residual(la); break;
     default: return fail(GF_ERR_INVALID_VALUE);
   }
   if (err != cudaSuccess) return fail(GF_ERR_CUDA);
@@ -869,8 +918,8 @@ GF_API gf_status gf_plan_set_option(gf_plan* p, gf_option option, int64_t value)
       p->forced_tile_n = static_cast<int>(value);
       return replan(p) == GF_OK ? GF_OK : fail(GF_ERR_OUT_OF_MEMORY);
     case GF_OPT_KERNEL:
-      if (value < 0 || value > 3) return fail(GF_ERR_INVALID_VALUE);
-      if (value >= 2 && p->max_pair_clusters == 0) return fail(GF_ERR_UNSUPPORTED);
+      if (value < 0 || value > (p->epi == gf::EPI_RESIDUAL ? 4 : 3)) return fail(GF_ERR_INVALID_VALUE);
+      if ((value == 2 || value == 3) && p->max_pair_clusters == 0) return fail(GF_ERR_UNSUPPORTED);
       p->forced_kernel = static_cast<int>(value);
       return replan(p) == GF_OK ? GF_OK : fail(GF_ERR_OUT_OF_MEMORY);
     case GF_OPT_L2_HINTS:
@@ -995,7 +1044,7 @@ GF_API gf_status gf_plan_describe(const gf_plan* p, int32_t* tile_m, int32_t* ti
     if (workspace_bytes) *workspace_bytes = static_cast<int64_t>(p->work_bytes) + 256;
     return GF_OK;
   }
-  if (tile_m) *tile_m = p->pair ? 2 * kBM : kBM;
+  if (tile_m) *tile_m = p->narrow ? p->tile_rows : p->pair ? 2 * kBM : kBM;
   if (tile_n) *tile_n = p->tile_n;
   if (stages) *stages = p->stages;
   if (grid) *grid = p->grid;
@@ -1092,7 +1141,7 @@ GF_API gf_status gf_plan_status(const gf_plan* p, struct CUstream_st* stream) {
     // a launch that gave up may leave split-k counters part-way
     const size_t counters = p->pair ? 2 * static_cast<size_t>(p->num_tiles - p->split_from)
                                     : static_cast<size_t>(p->num_tiles);
-    if (p->k_splits > 1 &&
+    if (p->k_splits > 1 && !p->narrow &&
         gf::runtime_zero(static_cast<char*>(p->d_splitk) + p->splitk_cnt_offset, counters * 4) !=
             GF_OK)
       return fail(GF_ERR_CUDA);

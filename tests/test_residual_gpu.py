@@ -121,6 +121,40 @@ def test_every_kernel(kernel, split, dtype, layout, kind, m, n, k):
     plan.free()
 
 
+# rows of each tile height, and of several tiles; one k-block and many; tiles whole and dealt out; column tails with and
+# without whole 64-column chunks
+@pytest.mark.parametrize("m,n,k", [(1, 8, 8), (1, 5120, 1088), (7, 264, 4096), (16, 128, 64), (17, 200, 2056), (32, 1024, 520), (33, 72, 3000),
+                                   (48, 4096, 1024), (64, 136, 8192), (65, 328, 1000), (128, 640, 2048), (129, 264, 520), (300, 72, 4104), (20, 64, 0),
+                                   (5, 40000, 200), (1, 16, 65536)])
+@pytest.mark.parametrize("dtype,layout,kind,bias", [(gf.GF_F16, gf.GF_B_NK, gf.GF_ACT_GELU, True), (gf.GF_BF16, gf.GF_B_KN, gf.GF_ACT_SILU, True),
+                                                    (gf.GF_BF16, gf.GF_B_NK, gf.GF_ACT_NONE, False), (gf.GF_F16, gf.GF_B_KN, gf.GF_ACT_RELU, False)])
+def test_few_rows(m, n, k, dtype, layout, kind, bias):
+    c = Case(m, n, k, dtype, layout, bias, seed=50)
+    plan = gf.gf_matmul_residual_plan(m, n, k, dtype, kind, layout)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_KERNEL, 4)
+    z = filled(m, n, dtype=TDT[dtype])
+    out = c.run(plan, z_out=z)
+    c.check(kind, out, z)
+    for _ in range(3):  # the same bits whichever CTA ends last, and into the residual
+        inplace = c.res.clone()
+        assert torch.equal(c.run(plan, out=inplace, res=inplace), out)
+    plan.free()
+
+
+def test_few_rows_times_out_and_recovers():
+    """A load that never comes: the waits run out, the status says so, and the plan works again."""
+    c = Case(3, 256, 4096, gf.GF_BF16, gf.GF_B_NK, seed=55)
+    plan = gf.gf_matmul_residual_plan(3, 256, 4096, gf.GF_BF16, gf.GF_ACT_NONE, gf.GF_B_NK)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_WAIT_LIMIT_US, 20000)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_FAULT_DROP_LOAD, 2)
+    out = torch.empty_like(c.res)
+    gf.gf_matmul_residual_execute(plan, c.a, c.b, c.res, out, bias=c.bias)
+    assert gf.gf_plan_status(plan) == gf.GF_ERR_DEVICE_TIMEOUT
+    gf.gf_plan_set_option(plan, gf.GF_OPT_FAULT_DROP_LOAD, 0)
+    c.check(gf.GF_ACT_NONE, c.run(plan))
+    plan.free()
+
+
 def test_without_an_activation_it_is_the_product_and_the_sum():
     """The same kernel without a bias and with a residual of zeros gives the bits of the plain product."""
     c = Case(300, 328, 520, gf.GF_BF16, gf.GF_B_NK, bias=False, seed=60)
