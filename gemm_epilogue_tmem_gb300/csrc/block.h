@@ -43,6 +43,10 @@ struct NormParams {
   int32_t rows, hidden;
   float eps;
   int32_t lanes;        // backward: rows in work at a time, a column sum each
+  int32_t sms;
+  int32_t stages;       // of a streaming kernel's ring
+  int32_t* status;
+  uint64_t wait_limit_ns;
   const void* x;        // backward: the rows that were normed
   const void* residual; // backward: the gradient that comes along the residual
   const void* weight;
@@ -51,13 +55,17 @@ struct NormParams {
   uint8_t* out8;
   float* scale;
   const void* d_out;
-  float* partials;      // backward: [CTAs][hidden]; NULL: no gradient of the weight
+  float* partials;      // backward: [partial rows][hidden]; NULL: no gradient of the weight
 };
 
 cudaError_t launch_norm(const NormParams& p, int bf16, cudaStream_t stream, int pdl);
-// The CTAs of the backward kernel for so many rows (0 with an error in *err).
+// The CTAs of the backward kernel that loads its rows itself, for so many (0 with an
+// error in *err), and the most rows of partial sums of either backward kernel.
 int norm_grad_ctas(int64_t rows, int64_t hidden, int bf16, int sms, cudaError_t* err);
-cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream_t stream, int pdl);
+int norm_grad_partials(int64_t rows, int64_t hidden, int sms, int ctas);
+// *partial_rows: rows of partial sums that it leaves
+cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream_t stream, int pdl,
+                             int* partial_rows);
 
 // --------------------------------------------- gradient of an activation, bias
 struct DactParams {

@@ -1,90 +1,16 @@
-// Root-mean-square norm with the residual's addition before it.
+// Root-mean-square norm with the residual's addition before it: few rows, and rows
+// that are not whole 16-byte words.
 //
-//   r = round(x + residual),  y = r w rstd,  rstd = 1 / sqrt(mean(r^2) + eps)
-//   g = d_y w,  d = rstd (g - r rstd^2 mean(g r)) + d_r,  d_w = sum of d_y r rstd
-//
-// A row is read once: it stays in registers, in 16 bits, between its sum and its
-// output. 16-byte accesses for rows of any length: where rows do not start on
-// 16 bytes, the row's words are those it would have in an aligned array, the ones
-// at its two ends are read and written one element at a time. HBM bounds both
-// directions; nothing is kept from the forward but r itself, whose sum of squares
-// the backward forms along with the other one that it needs.
-//
-// e4m3 output: the scale of 128 elements is a power of two that the block's
-// largest magnitude decides, so that a last bit of rstd could turn the whole block's
-// scale. That magnitude is max|r w| rstd; the products r w of 16-bit values are exact
-// in fp32, and rstd is held as the sum of two fp32, from a sum of squares held the
-// same way (error-free addition: Knuth, The Art of Computer Programming 2, 4.2.2,
-// and one Newton step), so that the scale is the one of 64-bit arithmetic.
-#include <math.h>
-
-#include "block.h"
-#include "fp8.cuh"
-#include "ptx.cuh"
+// A CTA loads its rows itself and keeps them in registers, in 16 bits, between their sum
+// and the output. 16-byte accesses for rows of any length: where rows do not start on
+// 16 bytes, the row's words are those it would have in an aligned array, the ones at its
+// two ends are read and written one element at a time. HBM bounds both directions (one
+// row: latency); nothing is kept from the forward but r itself, whose sum of squares the
+// backward forms along with the other one that it needs.
+#include "norm_common.cuh"
 
 namespace gf {
 namespace {
-
-// a + b = s + e exactly
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-  s = __fadd_rn(a, b);
-  const float z = __fsub_rn(s, a);
-  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
-}
-
-// a sum of squares: fp32, or (EXACT) two fp32
-template <bool EXACT>
-struct Sum {
-  float hi, lo;
-  __device__ __forceinline__ void add(float v) {
-    if constexpr (EXACT) {
-      float e;
-      two_sum(hi, v, hi, e);
-      lo += e;
-    } else {
-      hi += v;
-    }
-  }
-  __device__ __forceinline__ void add(const Sum& o) {
-    add(o.hi);
-    if constexpr (EXACT) lo += o.lo;
-  }
-  __device__ __forceinline__ Sum other(int lane_mask) const {
-    Sum o = {0.f, 0.f};
-    o.hi = __shfl_xor_sync(0xFFFFFFFFu, hi, lane_mask);
-    if constexpr (EXACT) o.lo = __shfl_xor_sync(0xFFFFFFFFu, lo, lane_mask);
-    return o;
-  }
-};
-
-// 1 / sqrt(sum / n + eps), as hi + lo (EXACT)
-template <bool EXACT>
-__device__ __forceinline__ float inv_rms(const Sum<EXACT>& sum, int n, float eps, float& lo) {
-  lo = 0.f;
-  const float nf = static_cast<float>(n);
-  if constexpr (!EXACT) {
-    return rsqrtf(sum.hi / nf + eps);
-  } else {
-    float sh, sl;
-    two_sum(sum.hi, sum.lo, sh, sl);
-    if (!isfinite(sum.hi)) return rsqrtf(sum.hi);
-    const float q = __fdiv_rn(sh, nf);
-    const float ql = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, nf, sh), sl), nf);
-    float v, vl;
-    two_sum(q, eps, v, vl);
-    vl = __fadd_rn(vl, ql);
-    const float r = rsqrtf(v);
-    if (!isfinite(r)) return r;
-    // r^2 and v r^2 with their rounding errors; 1 - v r^2 is small
-    const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
-    const float t = __fmul_rn(v, p), te = __fmaf_rn(v, p, -t);
-    float e = __fsub_rn(__fsub_rn(1.f, t), te);
-    e = __fsub_rn(e, __fmul_rn(v, pe));
-    e = __fsub_rn(e, __fmul_rn(vl, p));
-    lo = __fmul_rn(__fmul_rn(0.5f, r), e);
-    return r;
-  }
-}
 
 // A row of a dense [rows, n] matrix of 16-bit elements as 16-byte words. ALIGNED:
 // n is a multiple of 8; else the row begins at element `o` of its first word.
@@ -141,23 +67,6 @@ struct Row {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = Pair16<T>::unpack(w[i]);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-  return make_uint4(Pair16<T>::pack(f[0], f[1]), Pair16<T>::pack(f[2], f[3]),
-                    Pair16<T>::pack(f[4], f[5]), Pair16<T>::pack(f[6], f[7]));
-}
-
 // the sum over the blockDim.x threads of a row, in the same order in each of them
 template <typename S>
 __device__ __forceinline__ S row_sum(S s, S* red) {
@@ -197,14 +106,8 @@ __global__ void __launch_bounds__(544) norm_kernel(const NormParams p) {
       add[i] = w < words ? row.load(p.residual, w) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float a[8], b[8];
-      unpack<T>(r[i], a);
-      unpack<T>(add[i], b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] += b[j];
-      r[i] = pack<T>(a);  // the residual stream is kept in 16 bits, and normed as it is kept
-    }
+    for (int i = 0; i < V; ++i)
+      r[i] = add8<T>(r[i], add[i]);  // the stream is kept in 16 bits, and normed as it is kept
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -247,14 +150,8 @@ __global__ void __launch_bounds__(544) norm_kernel(const NormParams p) {
       // 16 lanes hold a block of 128
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d));
-      const float m = __uint_as_float(mag);
-      const float top = __fmul_rn(m, rstd);
-      const float err = __fmaf_rn(m, lo, __fmaf_rn(m, rstd, -top));
-      uint32_t bits = finite_mag_bits(top);
-      // the rounded product lies on the border of two scales, the product above it
-      if ((bits & 0x7FFFFFu) == 0x600000u && err > 0.f) ++bits;
       float inv;
-      const float scale = e4m3_scale(bits, inv);
+      const float scale = e4m3_scale(exact_mag(__uint_as_float(mag), rstd, lo), inv);
       if (w < words) {
         reinterpret_cast<uint2*>(p.out8)[row.word0 + w] =
             make_uint2(e4m3x4(f[0], f[1], f[2], f[3], inv), e4m3x4(f[4], f[5], f[6], f[7], inv));
@@ -265,20 +162,6 @@ __global__ void __launch_bounds__(544) norm_kernel(const NormParams p) {
 }
 
 // ----------------------------------------------------------------- backward
-struct Sum2 {
-  float rr, gr;
-  __device__ __forceinline__ void add(const Sum2& o) {
-    rr += o.rr;
-    gr += o.gr;
-  }
-  __device__ __forceinline__ Sum2 other(int lane_mask) const {
-    Sum2 o;
-    o.rr = __shfl_xor_sync(0xFFFFFFFFu, rr, lane_mask);
-    o.gr = __shfl_xor_sync(0xFFFFFFFFu, gr, lane_mask);
-    return o;
-  }
-};
-
 // CTAs walk over the rows, a thread keeping the same columns from row to row for
 // the weight's gradient (in registers; from V = 8 on in shared memory). Rows whose
 // words do not begin on the row begin elsewhere in their first word each time,
@@ -496,6 +379,9 @@ cudaError_t backward(const NormParams& p, int ctas, cudaStream_t stream, int pdl
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, int bf16, cudaStream_t stream, int pdl) {
+  NormStream s;
+  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 2 : 1, p.sms, &s))
+    return launch_norm_stream(p, s, bf16, stream, pdl);
   return bf16 ? forward_type<__nv_bfloat16>(p, stream, pdl) : forward_type<__half>(p, stream, pdl);
 }
 
@@ -506,7 +392,22 @@ int norm_grad_ctas(int64_t rows, int64_t hidden, int bf16, int sms, cudaError_t*
   return n;
 }
 
-cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream_t stream, int pdl) {
+int norm_grad_partials(int64_t rows, int64_t hidden, int sms, int ctas) {
+  int most = ctas;
+  NormStream s;
+  for (int arrays = 2; arrays <= 3; ++arrays)
+    if (norm_stream_shape(rows, hidden, arrays, sms, &s) && s.ctas > most) most = s.ctas;
+  return most;
+}
+
+cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream_t stream, int pdl,
+                             int* partial_rows) {
+  NormStream s;
+  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 3 : 2, p.sms, &s)) {
+    *partial_rows = s.ctas;
+    return launch_norm_grad_stream(p, s, bf16, stream, pdl);
+  }
+  *partial_rows = ctas;
   return bf16 ? backward<__nv_bfloat16>(p, ctas, stream, pdl) : backward<__half>(p, ctas, stream, pdl);
 }
 

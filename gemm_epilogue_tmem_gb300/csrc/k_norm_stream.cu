@@ -1,0 +1,397 @@
+// The root-mean-square norm of many rows of whole 16-byte words.
+//
+// CTAs that stay walk over the rows, which bulk copies bring to a ring in shared memory
+// several rows ahead, so that HBM, which bounds both directions, is asked for the next
+// rows while the sum of one is formed. Groups of blockDim.y consecutive rows (short ones
+// share a CTA) are the turns of CTA blockIdx.x, blockIdx.x + gridDim.x, ...; a stage of
+// the ring holds a group of two or three arrays, each brought by one copy. A turn has one
+// barrier, that of the row's sum: after it every thread has done with the stage of
+// the turn before, which is filled again.
+//
+// A thread has the same columns in every turn: the weight stays in its registers, and
+// so do the column sums of the weight's gradient.
+#include "norm_common.cuh"
+
+namespace gf {
+namespace {
+
+constexpr int kMaxStages = 8;
+constexpr size_t kStreamSmem = 216 * 1024;  // of an SM, for rings
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+struct Ring {
+  uint32_t data, full;   // shared-memory addresses: the stages, their barriers
+  volatile int* stop;
+  uint32_t array_bytes;  // of one array of a stage
+  int arrays, stages;
+  int64_t groups;
+
+  __device__ __forceinline__ void start(const NormParams& p, int arrays_, uint8_t* smem, uint64_t* bars,
+                                        int* flag) {
+    data = smem_u32(smem);
+    full = smem_u32(bars);
+    stop = flag;
+    arrays = arrays_;
+    stages = p.stages;
+    array_bytes = blockDim.y * static_cast<uint32_t>(p.hidden) * 2u;
+    groups = (static_cast<int64_t>(p.rows) + blockDim.y - 1) / blockDim.y;
+    if (leader()) {
+      for (int s = 0; s < stages; ++s) mbar_init(full + 8u * s, 1);
+      *flag = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+    if (leader())
+      for (int s = 0; s < stages; ++s)
+        issue(p, s, blockIdx.x + static_cast<int64_t>(s) * gridDim.x);
+  }
+  __device__ __forceinline__ bool leader() const { return threadIdx.x == 0 && threadIdx.y == 0; }
+  __device__ __forceinline__ uint32_t array(int stage, int a) const {
+    return data + static_cast<uint32_t>(stage * arrays + a) * array_bytes;
+  }
+  // a group's rows of each array into the stage; nothing past the last group
+  __device__ __forceinline__ void issue(const NormParams& p, int stage, int64_t group) const {
+    if (group >= groups) return;
+    const int64_t row = group * blockDim.y, left = p.rows - row;
+    const int rows = left < blockDim.y ? static_cast<int>(left) : static_cast<int>(blockDim.y);
+    const uint32_t bytes = static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.hidden) * 2u;
+    const uint32_t bar = full + 8u * static_cast<uint32_t>(stage);
+    const int64_t at = row * p.hidden * 2;
+    mbar_arrive_expect_tx(bar, bytes * static_cast<uint32_t>(arrays));
+    bulk_load(array(stage, 0), static_cast<const char*>(p.x) + at, bytes, bar);
+    if (p.d_out != nullptr)
+      bulk_load(array(stage, 1), static_cast<const char*>(p.d_out) + at, bytes, bar);
+    if (p.residual != nullptr)
+      bulk_load(array(stage, arrays - 1), static_cast<const char*>(p.residual) + at, bytes, bar);
+  }
+  __device__ __forceinline__ void wait(const NormParams& p, int stage, uint32_t phase) const {
+    if (!mbar_wait_bounded(full + 8u * static_cast<uint32_t>(stage), phase, stop, p.wait_limit_ns)) {
+      *stop = 1;  // the waits that follow end at once; outputs are incomplete
+      atomicOr(p.status, 1);
+    }
+  }
+  // a CTA that gave up may still have copies in flight towards its shared memory
+  __device__ __forceinline__ void finish() const {
+    if (__syncthreads_or(*stop)) sleep_ns(200000);
+  }
+};
+
+// the sum over a row's threads, with the turn's one barrier
+template <typename S>
+__device__ __forceinline__ S turn_sum(S s, S* red) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s.add(s.other(d));
+  const int warps = blockDim.x >> 5;
+  S* mine = red + threadIdx.y * warps;
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = mine[0];
+  for (int i = 1; i < warps; ++i) s.add(mine[i]);
+  return s;
+}
+
+// exact_mag with the row's sum formed anew, in two fp32, by one warp from the ring
+template <typename T>
+__device__ __noinline__ uint32_t sure_mag(const NormParams& p, uint32_t x, uint32_t residual, float mag) {
+  Sum<true> s = {0.f, 0.f};
+  for (int w = threadIdx.x & 31; w < p.hidden / 8; w += 32) {
+    uint4 v = ld_shared_v4(x + 16u * static_cast<uint32_t>(w));
+    if (residual != 0u) v = add8<T>(v, ld_shared_v4(residual + 16u * static_cast<uint32_t>(w)));
+    float f[8];
+    unpack<T>(v, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.add(__fmul_rn(f[j], f[j]));
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s.add(s.other(d));
+  float lo;
+  const float hi = inv_rms<true>(s, p.hidden, p.eps, lo);
+  return exact_mag(mag, hi, lo);
+}
+
+template <typename T, int V, bool FP8>
+__global__ void __launch_bounds__(512) norm_stream_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Sum<false> red[2][32];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int stop;
+  const int words = p.hidden >> 3, step = blockDim.x, w0 = threadIdx.x;
+  Ring ring;
+  ring.start(p, p.residual != nullptr ? 2 : 1, smem, full, &stop);
+  uint4 wt[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int w = w0 + i * step;
+    wt[i] = w < words ? static_cast<const uint4*>(p.weight)[w] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  for (int64_t group = blockIdx.x; group < ring.groups; group += gridDim.x, turn ^= 1) {
+    ring.wait(p, stage, phase);
+    const int64_t at = group * blockDim.y + threadIdx.y;
+    const bool row_ok = at < p.rows;
+    const uint32_t row_off = threadIdx.y * static_cast<uint32_t>(p.hidden) * 2u;
+    const uint32_t x = ring.array(stage, 0) + row_off;
+    const uint32_t residual = p.residual != nullptr ? ring.array(stage, 1) + row_off : 0u;
+    const int64_t word0 = at * words;
+    uint4 r[V];
+    Sum<false> s = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      r[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row_ok && w < words) {
+        r[i] = ld_shared_v4(x + 16u * static_cast<uint32_t>(w));
+        if (residual != 0u) {
+          r[i] = add8<T>(r[i], ld_shared_v4(residual + 16u * static_cast<uint32_t>(w)));
+          if (p.residual_out != nullptr) static_cast<uint4*>(p.residual_out)[word0 + w] = r[i];
+        }
+      }
+      float f[8];
+      unpack<T>(r[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s.hi = fmaf(f[j], f[j], s.hi);
+    }
+    s = turn_sum(s, red[turn]);
+    if (ring.leader() && group != blockIdx.x)
+      ring.issue(p, stage == 0 ? ring.stages - 1 : stage - 1,
+                 group + static_cast<int64_t>(ring.stages - 1) * gridDim.x);
+    float lo;
+    const float rstd = inv_rms<false>(s, p.hidden, p.eps, lo);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      const bool here = row_ok && w < words;
+      float f[8], g[8];
+      unpack<T>(r[i], f);
+      unpack<T>(wt[i], g);
+      float mag = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] *= g[j];
+        if (FP8) mag = fmaxf(mag, fabsf(f[j]));  // (NaN left out)
+      }
+      if (here && (!FP8 || p.out != nullptr)) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = f[j] * rstd;
+        static_cast<uint4*>(p.out)[word0 + w] = pack<T>(y);
+      }
+      if constexpr (FP8) {
+        // 16 lanes hold a block of 128
+        uint32_t m = __float_as_uint(mag);
+        const bool finite = __all_sync(0xFFFFFFFFu, m < 0x7F800000u && isfinite(s.hi));
+        if (!finite) {  // the finite ones' alone
+          m = 0u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, finite_mag_bits(f[j]));
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        uint32_t bits = finite_mag_bits(__uint_as_float(m) * rstd);
+        // Next to the border of two scales: rstd is of fp32 sums of 8 V + 22 additions, half
+        // of whose error it has, a division and a root, 2^-18 at most; 64 is 2^-17.8.
+        const bool doubt =
+            row_ok && abs(static_cast<int>(bits & 0x7FFFFFu) - 0x600000) <= 64;
+        if (__any_sync(0xFFFFFFFFu, doubt)) {
+          const uint32_t sure = sure_mag<T>(p, x, residual, __uint_as_float(m));
+          if (doubt) bits = sure;
+        }
+        float inv;
+        const float scale = e4m3_scale(bits, inv);
+        uint2 q;
+        if (finite) {
+          const float by = rstd * inv;  // (times a power of two: rounded as f * rstd is)
+          q.x = e4m3x4<true>(f[0], f[1], f[2], f[3], by);
+          q.y = e4m3x4<true>(f[4], f[5], f[6], f[7], by);
+        } else {
+          q.x = e4m3x4(f[0] * rstd, f[1] * rstd, f[2] * rstd, f[3] * rstd, inv);
+          q.y = e4m3x4(f[4] * rstd, f[5] * rstd, f[6] * rstd, f[7] * rstd, inv);
+        }
+        if (here) {
+          reinterpret_cast<uint2*>(p.out8)[word0 + w] = q;
+          if ((threadIdx.x & 15) == 0) p.scale[at * ((p.hidden + 127) >> 7) + (w >> 4)] = scale;
+        }
+      }
+    }
+    if (++stage == ring.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  ring.finish();
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(512) norm_grad_stream_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Sum2 red[2][32];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int stop;
+  const int words = p.hidden >> 3, step = blockDim.x, w0 = threadIdx.x;
+  Ring ring;
+  ring.start(p, p.residual != nullptr ? 3 : 2, smem, full, &stop);
+  uint4 wt[V];
+  float acc[V][8];  // the weight's gradient, of this thread's columns
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int w = w0 + i * step;
+    wt[i] = w < words ? static_cast<const uint4*>(p.weight)[w] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  }
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  for (int64_t group = blockIdx.x; group < ring.groups; group += gridDim.x, turn ^= 1) {
+    ring.wait(p, stage, phase);
+    const int64_t at = group * blockDim.y + threadIdx.y;
+    const bool row_ok = at < p.rows;
+    const uint32_t row_off = threadIdx.y * static_cast<uint32_t>(p.hidden) * 2u;
+    const uint32_t x = ring.array(stage, 0) + row_off, dy = ring.array(stage, 1) + row_off;
+    const uint32_t along = ring.array(stage, 2) + row_off;
+    Sum2 s = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      if (row_ok && w < words) {
+        float f[8], g[8], wf[8];
+        unpack<T>(ld_shared_v4(x + 16u * static_cast<uint32_t>(w)), f);
+        unpack<T>(ld_shared_v4(dy + 16u * static_cast<uint32_t>(w)), g);
+        unpack<T>(wt[i], wf);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s.rr = fmaf(f[j], f[j], s.rr);
+          s.gr = fmaf(g[j] * wf[j], f[j], s.gr);
+        }
+      }
+    }
+    s = turn_sum(s, red[turn]);
+    if (ring.leader() && group != blockIdx.x)
+      ring.issue(p, stage == 0 ? ring.stages - 1 : stage - 1,
+                 group + static_cast<int64_t>(ring.stages - 1) * gridDim.x);
+    const float n = static_cast<float>(p.hidden);
+    const float rstd = rsqrtf(s.rr / n + p.eps);
+    const float c = rstd * rstd * (s.gr / n);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int w = w0 + i * step;
+      if (row_ok && w < words) {
+        float f[8], g[8], wf[8], d[8];
+        unpack<T>(ld_shared_v4(x + 16u * static_cast<uint32_t>(w)), f);
+        unpack<T>(ld_shared_v4(dy + 16u * static_cast<uint32_t>(w)), g);
+        unpack<T>(wt[i], wf);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          d[j] = rstd * (g[j] * wf[j] - f[j] * c);
+          acc[i][j] = fmaf(g[j] * f[j], rstd, acc[i][j]);
+        }
+        if (p.residual != nullptr) {
+          float e[8];
+          unpack<T>(ld_shared_v4(along + 16u * static_cast<uint32_t>(w)), e);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] += e[j];
+        }
+        static_cast<uint4*>(p.out)[at * words + w] = pack<T>(d);
+      }
+    }
+    if (++stage == ring.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  ring.finish();
+  if (p.partials == nullptr) return;
+  // the thread rows one after the other, a fixed order, in the ring's memory
+  float* cols = reinterpret_cast<float*>(smem);
+  for (int y = 0; y < blockDim.y; ++y) {
+    if (threadIdx.y == y) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int w = w0 + i * step;
+        if (w < words) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            cols[8 * w + j] = acc[i][j] + (y > 0 ? cols[8 * w + j] : 0.f);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  float* out = p.partials + static_cast<int64_t>(blockIdx.x) * p.hidden;
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < p.hidden; c += blockDim.x * blockDim.y)
+    out[c] = cols[c];
+}
+
+template <typename K>
+cudaError_t launch_ring(K kernel, const NormParams& p, const NormStream& s, cudaStream_t stream, int pdl) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(s.smem));
+  if (e != cudaSuccess) return e;
+  NormParams q = p;
+  q.stages = s.stages;
+  return launch_pdl(kernel, dim3(s.ctas), dim3(s.threads, s.rows), s.smem, stream, pdl, q);
+}
+
+template <typename T, bool FP8>
+cudaError_t forward(const NormParams& p, const NormStream& s, cudaStream_t stream, int pdl) {
+  switch (s.v) {
+    case 1: return launch_ring(norm_stream_kernel<T, 1, FP8>, p, s, stream, pdl);
+    case 2: return launch_ring(norm_stream_kernel<T, 2, FP8>, p, s, stream, pdl);
+    case 4: return launch_ring(norm_stream_kernel<T, 4, FP8>, p, s, stream, pdl);
+    case 8: return launch_ring(norm_stream_kernel<T, 8, FP8>, p, s, stream, pdl);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t backward(const NormParams& p, const NormStream& s, cudaStream_t stream, int pdl) {
+  switch (s.v) {
+    case 1: return launch_ring(norm_grad_stream_kernel<T, 1>, p, s, stream, pdl);
+    case 2: return launch_ring(norm_grad_stream_kernel<T, 2>, p, s, stream, pdl);
+    case 4: return launch_ring(norm_grad_stream_kernel<T, 4>, p, s, stream, pdl);
+    case 8: return launch_ring(norm_grad_stream_kernel<T, 8>, p, s, stream, pdl);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+// About 256 threads a CTA and two CTAs an SM, the ring all of its shared memory. Not for
+// rows that give a CTA no second turn, nor for those of which it does not hold two.
+bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, int sms, NormStream* s) {
+  if (hidden % 8 != 0) return false;
+  const int words = static_cast<int>(hidden / 8);
+  s->v = words <= 256 ? 1 : words <= 1024 ? 2 : words <= 2048 ? 4 : 8;
+  s->threads = (words + s->v * 32 - 1) / (s->v * 32) * 32;
+  s->rows = s->threads >= 192 ? 1 : 256 / s->threads;
+  const size_t stage = static_cast<size_t>(s->rows) * words * 16 * arrays;
+  const int per_sm = 2 * 2 * stage <= kStreamSmem ? 2 : 1;
+  s->stages = static_cast<int>(kStreamSmem / per_sm / stage);
+  if (s->stages > kMaxStages) s->stages = kMaxStages;
+  if (s->stages < 2) return false;
+  s->smem = s->stages * stage;
+  s->ctas = per_sm * sms;
+  return (rows + s->rows - 1) / s->rows > s->ctas;
+}
+
+cudaError_t launch_norm_stream(const NormParams& p, const NormStream& s, int bf16, cudaStream_t stream,
+                               int pdl) {
+  if (p.out8 != nullptr)
+    return bf16 ? forward<__nv_bfloat16, true>(p, s, stream, pdl) : forward<__half, true>(p, s, stream, pdl);
+  return bf16 ? forward<__nv_bfloat16, false>(p, s, stream, pdl) : forward<__half, false>(p, s, stream, pdl);
+}
+
+cudaError_t launch_norm_grad_stream(const NormParams& p, const NormStream& s, int bf16,
+                                    cudaStream_t stream, int pdl) {
+  return bf16 ? backward<__nv_bfloat16>(p, s, stream, pdl) : backward<__half>(p, s, stream, pdl);
+}
+
+}  // namespace gf

@@ -147,6 +147,17 @@ GF_API gf_status gf_route_grad_execute(const gf_plan* p, const void* logits, con
 }
 
 // --------------------------------------------------------------------- norm
+static gf::NormParams norm_params(const gf_plan* p) {
+  gf::NormParams n = {};
+  n.rows = static_cast<int32_t>(p->m);
+  n.hidden = static_cast<int32_t>(p->n);
+  n.eps = p->scale;
+  n.sms = p->num_sms;
+  n.status = p->d_status;
+  n.wait_limit_ns = p->wait_limit_ns;
+  return n;
+}
+
 GF_API gf_plan* gf_rmsnorm_plan(int64_t rows, int64_t hidden, gf_dtype dtype, float eps) {
   if (rows < 0 || rows > kMaxDim || hidden < 1 || hidden > kMaxDim ||
       (dtype != GF_F16 && dtype != GF_BF16) || !(eps >= 0.f) || !isfinite(eps))
@@ -162,7 +173,9 @@ GF_API gf_plan* gf_rmsnorm_plan(int64_t rows, int64_t hidden, gf_dtype dtype, fl
   cudaError_t e = cudaSuccess;
   p->grid = rows == 0 ? 0
                       : gf::norm_grad_ctas(rows, hidden, dtype == GF_BF16, p->num_sms, &e);
-  gf_status st = e == cudaSuccess ? add_partials(p, p->grid, hidden) : GF_ERR_CUDA;
+  gf_status st = e != cudaSuccess ? GF_ERR_CUDA
+                 : rows == 0      ? GF_OK
+                                  : add_partials(p, gf::norm_grad_partials(rows, hidden, p->num_sms, p->grid), hidden);
   if (st != GF_OK) {
     cudaGetLastError();
     gf_plan_free(p);
@@ -184,10 +197,7 @@ GF_API gf_status gf_rmsnorm_execute(const gf_plan* p, const void* x, const void*
     return runtime_fail(GF_ERR_INVALID_VALUE);
   if (out8 != nullptr && p->n % 16 != 0) return runtime_fail(GF_ERR_UNSUPPORTED);
   if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
-  gf::NormParams n = {};
-  n.rows = static_cast<int32_t>(p->m);
-  n.hidden = static_cast<int32_t>(p->n);
-  n.eps = p->scale;
+  gf::NormParams n = norm_params(p);
   n.x = x;
   n.residual = residual;
   n.weight = weight;
@@ -213,19 +223,17 @@ GF_API gf_status gf_rmsnorm_grad_execute(const gf_plan* p, const void* d_out, co
   if (!given(d_out) || !given(r) || !given(weight) || !aligned(d_residual) || !given(d_x))
     return runtime_fail(GF_ERR_INVALID_VALUE);
   if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
-  gf::NormParams n = {};
-  n.rows = static_cast<int32_t>(p->m);
-  n.hidden = static_cast<int32_t>(p->n);
-  n.eps = p->scale;
+  gf::NormParams n = norm_params(p);
   n.x = r;
   n.residual = d_residual;
   n.weight = weight;
   n.out = d_x;
   n.d_out = d_out;
   n.partials = d_weight != nullptr ? static_cast<float*>(p->d_work) : nullptr;
-  cudaError_t e = gf::launch_norm_grad(n, p->dtype == GF_BF16, p->grid, st, p->pdl);
+  int partial_rows = 0;
+  cudaError_t e = gf::launch_norm_grad(n, p->dtype == GF_BF16, p->grid, st, p->pdl, &partial_rows);
   if (e == cudaSuccess && d_weight != nullptr)
-    e = gf::launch_column_sums(n.partials, p->grid, n.hidden, d_weight, st, p->pdl);
+    e = gf::launch_column_sums(n.partials, partial_rows, n.hidden, d_weight, st, p->pdl);
   return launched(e);
 }
 

@@ -18,6 +18,10 @@ EPS = 1e-5
 SHAPES = [(1, 1), (3, 5), (9, 8), (70, 16), (33, 17), (257, 130), (40, 1000), (5, 1027), (700, 2047), (3, 2048), (17, 4095),
           (2, 5120), (19, 8190), (3, 8192), (2, 16385), (3, 20000), (2, 32767), (2, 32768)]
 
+# many rows of whole words, which stream through shared memory: short ones that share a turn, a last turn that is not
+# full, one and more words a thread, rows of which a ring holds two
+MANY = [(40001, 8), (9005, 64), (7003, 1024), (4099, 136), (1000, 2048), (1500, 5120), (701, 8192), (400, 16384), (320, 20000), (310, 32768)]
+
 
 def randn(*shape, seed, dtype):
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -49,7 +53,7 @@ def filled(*shape, dtype):
     return torch.full(shape, float("nan"), device="cuda").to(dtype)
 
 
-@pytest.mark.parametrize("rows,hidden", SHAPES)
+@pytest.mark.parametrize("rows,hidden", SHAPES + MANY)
 @pytest.mark.parametrize("dtype", [gf.GF_F16, gf.GF_BF16])
 def test_forward(rows, hidden, dtype):
     t = TDT[dtype]
@@ -72,7 +76,8 @@ def test_forward(rows, hidden, dtype):
     plan.free()
 
 
-@pytest.mark.parametrize("rows,hidden", [(1, 16), (5, 128), (3, 144), (66, 1040), (1, 5120), (31, 8192), (2, 16400), (3, 32768)])
+@pytest.mark.parametrize("rows,hidden", [(1, 16), (5, 128), (3, 144), (66, 1040), (1, 5120), (31, 8192), (2, 16400), (3, 32768)] +
+                         [(rows, hidden) for rows, hidden in MANY if hidden % 16 == 0])
 @pytest.mark.parametrize("dtype", [gf.GF_F16, gf.GF_BF16])
 def test_e4m3(rows, hidden, dtype):
     t, blocks = TDT[dtype], -(-hidden // 128)
@@ -106,9 +111,10 @@ def test_e4m3(rows, hidden, dtype):
     plan.free()
 
 
-def test_scales_at_the_border():
+@pytest.mark.parametrize("rows", [250, 8192])  # loaded by their CTA, and streamed
+def test_scales_at_the_border(rows):
     """Blocks whose largest value is 448 times a power of two, and as near to it as inputs allow: the scale of 64 bits."""
-    rows, hidden = 4096, 256
+    hidden = 256
     g = torch.Generator(device="cuda").manual_seed(3)
     x = torch.randn(rows, hidden, generator=g, device="cuda").half()
     w = torch.ones(hidden, device="cuda").half()
@@ -128,14 +134,15 @@ def test_scales_at_the_border():
     gf.gf_rmsnorm_execute(plan, x, w, out8=q, out_scale=scale)
     y = x.double() * w.double() / x.double().square().mean(1, keepdim=True).sqrt()
     top = y[:, :128].abs().amax(1)
-    assert int(((top / 1.75 - 1).abs() < 1e-4).sum()) > 1000  # the case is what it says
+    assert int(((top / 1.75 - 1).abs() < 1e-4).sum()) > rows // 4  # the case is what it says
     want = torch.where(top > 1.75, 2.0 ** -7, 2.0 ** -8)
     assert torch.equal(scale[:, 0].double(), want)
     plan.free()
 
 
-def test_values_without_a_number():
-    rows, hidden = 6, 256
+@pytest.mark.parametrize("rows", [6, 6000])
+def test_values_without_a_number(rows):
+    hidden = 256
     x, _, w = inputs(rows, hidden, gf.GF_BF16)
     x[1, 3] = float("nan")
     x[2, 200] = float("inf")
@@ -152,7 +159,7 @@ def test_values_without_a_number():
     plan.free()
 
 
-@pytest.mark.parametrize("rows,hidden", SHAPES + [(5003, 136), (4099, 250), (999, 1027)])
+@pytest.mark.parametrize("rows,hidden", SHAPES + MANY + [(5003, 136), (4099, 250), (999, 1027)])
 @pytest.mark.parametrize("dtype,along", [(gf.GF_F16, True), (gf.GF_BF16, True), (gf.GF_BF16, False)])
 def test_backward(rows, hidden, dtype, along):
     t = TDT[dtype]
