@@ -137,13 +137,11 @@ __device__ __forceinline__ float sigmoid_f(float g) { return fmaf(0.5f, tanh_fas
 
 __device__ __forceinline__ float silu_f(float g) { return g * sigmoid_f(g); }
 
-// The activations of the RESIDUAL epilogue and of their gradient, z / (1 + e^-u)
+// The activations of the RESIDUAL epilogue, z / (1 + e^-u)
 // with u = z (SiLU) or 2 c (z + k z^3) (GELU's tanh form: (1 + tanh v) / 2 =
 // 1 / (1 + e^-2v)), by the hardware exponential and reciprocal: errors of a few
 // 2^-24 relative to the value. Their sum with the residual is what is rounded, and
 // fp16 keeps 2^-11 of it, which the error of tanh.approx would reach.
-__device__ __forceinline__ float logistic_f(float u) { return __fdividef(1.f, 1.f + __expf(-u)); }
-
 __device__ __forceinline__ float act_value(int act, float z) {
   if (act == kActRelu) return z > 0.f ? z : 0.f;
   if (act == kActNone) return z;

@@ -3,7 +3,7 @@
 // residual's gradient is d_out itself).
 //
 // One pass over d_out and z, bound by HBM. A warp has 256 columns, 16 bytes a lane,
-// and every eighth row of its CTA's chunk, four in flight; a thread's columns stay
+// and every eighth row of its CTA's chunk; a thread's columns stay
 // the same, so their sums are in registers until the CTA's eight warps meet. The
 // chunks' sums are added by a second kernel, in a fixed order.
 #include "block.h"
@@ -13,24 +13,32 @@
 namespace gf {
 namespace {
 
-constexpr int kRowsInFlight = 4;
+constexpr int kPerSm = 4;  // CTAs of an SM
 
-// act'(z), with s = 1 / (1 + e^-u) and act = z s: s + z s (1 - s) u'
-__device__ __forceinline__ float act_slope(int act, float z) {
-  if (act == kActRelu) return z > 0.f ? 1.f : 0.f;
-  float u = z, du = 1.f;
-  if (act == kActGelu) {
-    u = z * fmaf(2.f * kGeluCK, z * z, 2.f * kGeluC);
-    du = fmaf(2.f * kGelu3CK, z * z, 2.f * kGeluC);
-  }
-  const float s = logistic_f(u);
-  // where the logistic has reached its end the second term is 0, also for an infinite z
-  const float t = s * (1.f - s);
-  return t == 0.f ? s : fmaf(z * du, t, s);
+// act'(z): with s = 1 / (1 + e^-u) and act = z s, s + z u' s (1 - s); u = z (SiLU) or
+// 2 c (z + k z^3) (GELU's tanh form). e^-u by the hardware's exponential of base 2, the
+// base in the constants, and its reciprocal, small results flushed. Where s has reached
+// its end the second term is 0, also for an infinite z.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float z2 = z * z;
+  const float t = ACT == kActGelu ? z * fmaf(-2.f * kGeluCK * kLog2e, z2, -2.f * kGeluC * kLog2e)
+                                  : z * -kLog2e;
+  const float zdu = ACT == kActGelu ? z * fmaf(2.f * kGelu3CK, z2, 2.f * kGeluC) : z;
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  const float w = fmaf(-s, s, s);
+  return w == 0.f ? s : fmaf(zdu, w, s);
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(256) dact_kernel(const DactParams p) {
+__global__ void __launch_bounds__(256, kPerSm) dact_kernel(const DactParams p) {
+  // rows of a thread whose loads are in flight (GELU of 8192 x 16384 with two 123 us, with
+  // four 128; sums alone 57 and 44)
+  constexpr int kRowsInFlight = ACT == kActNone ? 4 : 2;
   __shared__ float red[8][256];
   grid_dep_wait();
   grid_dep_launch();
@@ -61,7 +69,7 @@ __global__ void __launch_bounds__(256) dact_kernel(const DactParams p) {
           if constexpr (ACT != kActNone) {
             unpack8<T>(z[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] *= act_slope(ACT, f[j]);
+            for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(f[j]);
             static_cast<uint4*>(p.d_z)[((row0 + 8 * i) * p.cols + col) >> 3] =
                 make_uint4(pack2<T>(d[0], d[1]), pack2<T>(d[2], d[3]), pack2<T>(d[4], d[5]),
                            pack2<T>(d[6], d[7]));
@@ -101,8 +109,8 @@ cudaError_t dact(const DactParams& p, int chunks, cudaStream_t stream, int pdl) 
 
 int dact_chunks(int64_t rows, int64_t cols, int sms) {
   const int64_t blocks = (cols + 255) / 256;
-  int64_t chunks = static_cast<int64_t>(sms) * 4 / blocks;  // one wave of CTAs
-  const int64_t most = (rows + 8 * kRowsInFlight - 1) / (8 * kRowsInFlight);
+  int64_t chunks = static_cast<int64_t>(sms) * kPerSm / blocks;  // one wave of CTAs
+  const int64_t most = (rows + 31) / 32;
   if (chunks > most) chunks = most;
   return static_cast<int>(chunks < 1 ? 1 : chunks);
 }

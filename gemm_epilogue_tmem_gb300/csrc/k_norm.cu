@@ -276,9 +276,11 @@ __global__ void __launch_bounds__(544) norm_grad_kernel(const NormParams p) {
     out[c] = cols[c];
 }
 
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* partials, int rows, int n,
+// 32 columns a CTA, its warps the rows in turn
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(32 * kSlices) column_sums_kernel(const float* partials, int rows, int n,
                                                           float* out) {
-  __shared__ float red[8][33];
+  __shared__ float red[kSlices][33];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
@@ -286,13 +288,13 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* partials,
   float s = 0.f;
   if (col < n) {
 #pragma unroll 8
-    for (int r = slice; r < rows; r += 8) s += partials[static_cast<int64_t>(r) * n + col];
+    for (int r = slice; r < rows; r += kSlices) s += partials[static_cast<int64_t>(r) * n + col];
   }
   red[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && col < n) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += red[k][lane];
+    for (int k = 1; k < kSlices; ++k) s += red[k][lane];
     out[col] = s;
   }
 }
@@ -380,7 +382,7 @@ cudaError_t backward(const NormParams& p, int ctas, cudaStream_t stream, int pdl
 
 cudaError_t launch_norm(const NormParams& p, int bf16, cudaStream_t stream, int pdl) {
   NormStream s;
-  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 2 : 1, p.sms, &s))
+  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 2 : 1, p.out8 != nullptr, p.sms, &s))
     return launch_norm_stream(p, s, bf16, stream, pdl);
   return bf16 ? forward_type<__nv_bfloat16>(p, stream, pdl) : forward_type<__half>(p, stream, pdl);
 }
@@ -396,14 +398,14 @@ int norm_grad_partials(int64_t rows, int64_t hidden, int sms, int ctas) {
   int most = ctas;
   NormStream s;
   for (int arrays = 2; arrays <= 3; ++arrays)
-    if (norm_stream_shape(rows, hidden, arrays, sms, &s) && s.ctas > most) most = s.ctas;
+    if (norm_stream_shape(rows, hidden, arrays, false, sms, &s) && s.ctas > most) most = s.ctas;
   return most;
 }
 
 cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream_t stream, int pdl,
                              int* partial_rows) {
   NormStream s;
-  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 3 : 2, p.sms, &s)) {
+  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 3 : 2, false, p.sms, &s)) {
     *partial_rows = s.ctas;
     return launch_norm_grad_stream(p, s, bf16, stream, pdl);
   }
@@ -413,7 +415,7 @@ cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream
 
 cudaError_t launch_column_sums(const float* partials, int rows, int cols, float* out,
                                cudaStream_t stream, int pdl) {
-  return launch_pdl(column_sums_kernel, dim3((cols + 31) / 32), dim3(256), 0, stream, pdl,
+  return launch_pdl(column_sums_kernel, dim3((cols + 31) / 32), dim3(32 * kSlices), 0, stream, pdl,
                     partials, rows, cols, out);
 }
 

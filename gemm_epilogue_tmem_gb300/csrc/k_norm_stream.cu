@@ -16,7 +16,11 @@ namespace gf {
 namespace {
 
 constexpr int kMaxStages = 8;
+constexpr int kLeastTurns = 2;
 constexpr size_t kStreamSmem = 216 * 1024;  // of an SM, for rings
+// by the words of a thread: most threads of a CTA, CTAs of an SM
+constexpr int stream_threads(int v) { return v == 1 ? 256 : 512; }
+constexpr int stream_per_sm(int v) { return v == 1 ? 5 : v == 2 ? 2 : 1; }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -94,6 +98,7 @@ __device__ __forceinline__ S turn_sum(S s, S* red) {
   if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = s;
   __syncthreads();
   s = mine[0];
+#pragma unroll 4
   for (int i = 1; i < warps; ++i) s.add(mine[i]);
   return s;
 }
@@ -117,21 +122,27 @@ __device__ __noinline__ uint32_t sure_mag(const NormParams& p, uint32_t x, uint3
   return exact_mag(mag, hi, lo);
 }
 
+// e4m3: a thread has pairs of words, 16 columns, so that 8 lanes hold a block of 128.
 template <typename T, int V, bool FP8>
-__global__ void __launch_bounds__(512) norm_stream_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(stream_threads(V), stream_per_sm(V))
+    norm_stream_kernel(const __grid_constant__ NormParams p) {
+  static_assert(!FP8 || V % 2 == 0, "pairs of words");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Sum<false> red[2][32];
   __shared__ uint64_t full[kMaxStages];
   __shared__ int stop;
-  const int words = p.hidden >> 3, step = blockDim.x, w0 = threadIdx.x;
+  const int words = p.hidden >> 3, step = blockDim.x;
+  auto word = [&](int i) {
+    return FP8 ? 2 * (static_cast<int>(threadIdx.x) + (i >> 1) * step) + (i & 1)
+               : static_cast<int>(threadIdx.x) + i * step;
+  };
   Ring ring;
   ring.start(p, p.residual != nullptr ? 2 : 1, smem, full, &stop);
   uint4 wt[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int w = w0 + i * step;
-    wt[i] = w < words ? static_cast<const uint4*>(p.weight)[w] : make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int i = 0; i < V; ++i)
+    wt[i] = word(i) < words ? static_cast<const uint4*>(p.weight)[word(i)] : make_uint4(0u, 0u, 0u, 0u);
+  const float inv_n = 1.f / static_cast<float>(p.hidden);
   int stage = 0, turn = 0;
   uint32_t phase = 0;
   for (int64_t group = blockIdx.x; group < ring.groups; group += gridDim.x, turn ^= 1) {
@@ -143,18 +154,22 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(const __grid_constant_
     const uint32_t residual = p.residual != nullptr ? ring.array(stage, 1) + row_off : 0u;
     const int64_t word0 = at * words;
     uint4 r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      r[i] = row_ok && word(i) < words ? ld_shared_v4(x + 16u * static_cast<uint32_t>(word(i)))
+                                       : make_uint4(0u, 0u, 0u, 0u);
+    if (residual != 0u) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (row_ok && word(i) < words) {
+          r[i] = add8<T>(r[i], ld_shared_v4(residual + 16u * static_cast<uint32_t>(word(i))));
+          if (p.residual_out != nullptr) static_cast<uint4*>(p.residual_out)[word0 + word(i)] = r[i];
+        }
+      }
+    }
     Sum<false> s = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int w = w0 + i * step;
-      r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row_ok && w < words) {
-        r[i] = ld_shared_v4(x + 16u * static_cast<uint32_t>(w));
-        if (residual != 0u) {
-          r[i] = add8<T>(r[i], ld_shared_v4(residual + 16u * static_cast<uint32_t>(w)));
-          if (p.residual_out != nullptr) static_cast<uint4*>(p.residual_out)[word0 + w] = r[i];
-        }
-      }
       float f[8];
       unpack<T>(r[i], f);
 #pragma unroll
@@ -164,61 +179,73 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(const __grid_constant_
     if (ring.leader() && group != blockIdx.x)
       ring.issue(p, stage == 0 ? ring.stages - 1 : stage - 1,
                  group + static_cast<int64_t>(ring.stages - 1) * gridDim.x);
-    float lo;
-    const float rstd = inv_rms<false>(s, p.hidden, p.eps, lo);
+    const float rstd = rsqrtf(fmaf(s.hi, inv_n, p.eps));
+    if constexpr (!FP8) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int w = w0 + i * step;
-      const bool here = row_ok && w < words;
-      float f[8], g[8];
-      unpack<T>(r[i], f);
-      unpack<T>(wt[i], g);
-      float mag = 0.f;
+      for (int i = 0; i < V; ++i) {
+        float f[8], g[8];
+        unpack<T>(r[i], f);
+        unpack<T>(wt[i], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] *= g[j];
-        if (FP8) mag = fmaxf(mag, fabsf(f[j]));  // (NaN left out)
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * g[j] * rstd;
+        if (row_ok && word(i) < words) static_cast<uint4*>(p.out)[word0 + word(i)] = pack<T>(f);
       }
-      if (here && (!FP8 || p.out != nullptr)) {
-        float y[8];
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = f[j] * rstd;
-        static_cast<uint4*>(p.out)[word0 + w] = pack<T>(y);
-      }
-      if constexpr (FP8) {
-        // 16 lanes hold a block of 128
+      for (int u = 0; u < V / 2; ++u) {
+        const bool here = row_ok && word(2 * u) < words;
+        float f[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float a[8], g[8];
+          unpack<T>(r[2 * u + h], a);
+          unpack<T>(wt[2 * u + h], g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[8 * h + j] = a[j] * g[j];
+        }
+        if (p.out != nullptr && here) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = f[8 * h + j] * rstd;
+            static_cast<uint4*>(p.out)[word0 + word(2 * u + h)] = pack<T>(y);
+          }
+        }
+        float mag = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) mag = fmaxf(mag, fabsf(f[j]));  // (NaN left out)
         uint32_t m = __float_as_uint(mag);
-        const bool finite = __all_sync(0xFFFFFFFFu, m < 0x7F800000u && isfinite(s.hi));
+        const bool finite = __all_sync(0xFFFFFFFFu, m < 0x7F800000u && s.hi < INFINITY);
         if (!finite) {  // the finite ones' alone
           m = 0u;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = max(m, finite_mag_bits(f[j]));
+          for (int j = 0; j < 16; ++j) m = max(m, finite_mag_bits(f[j]));
         }
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
         uint32_t bits = finite_mag_bits(__uint_as_float(m) * rstd);
         // Next to the border of two scales: rstd is of fp32 sums of 8 V + 22 additions, half
-        // of whose error it has, a division and a root, 2^-18 at most; 64 is 2^-17.8.
-        const bool doubt =
-            row_ok && abs(static_cast<int>(bits & 0x7FFFFFu) - 0x600000) <= 64;
+        // of whose error it has, a product and a root, 2^-18 at most; 64 is 2^-17.8.
+        const bool doubt = row_ok && abs(static_cast<int>(bits & 0x7FFFFFu) - 0x600000) <= 64;
         if (__any_sync(0xFFFFFFFFu, doubt)) {
           const uint32_t sure = sure_mag<T>(p, x, residual, __uint_as_float(m));
           if (doubt) bits = sure;
         }
         float inv;
         const float scale = e4m3_scale(bits, inv);
-        uint2 q;
+        uint4 q;
         if (finite) {
-          const float by = rstd * inv;  // (times a power of two: rounded as f * rstd is)
-          q.x = e4m3x4<true>(f[0], f[1], f[2], f[3], by);
-          q.y = e4m3x4<true>(f[4], f[5], f[6], f[7], by);
+          q = quant16<true>(f, rstd * inv);  // (inv a power of two: rounded as f * rstd is)
         } else {
-          q.x = e4m3x4(f[0] * rstd, f[1] * rstd, f[2] * rstd, f[3] * rstd, inv);
-          q.y = e4m3x4(f[4] * rstd, f[5] * rstd, f[6] * rstd, f[7] * rstd, inv);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] *= rstd;
+          q = quant16<false>(f, inv);
         }
         if (here) {
-          reinterpret_cast<uint2*>(p.out8)[word0 + w] = q;
-          if ((threadIdx.x & 15) == 0) p.scale[at * ((p.hidden + 127) >> 7) + (w >> 4)] = scale;
+          reinterpret_cast<uint4*>(p.out8)[(word0 + word(2 * u)) >> 1] = q;
+          if ((threadIdx.x & 7) == 0)
+            p.scale[at * ((p.hidden + 127) >> 7) + (word(2 * u) >> 4)] = scale;
         }
       }
     }
@@ -231,7 +258,8 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(const __grid_constant_
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(512) norm_grad_stream_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(stream_threads(V), stream_per_sm(V))
+    norm_grad_stream_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Sum2 red[2][32];
   __shared__ uint64_t full[kMaxStages];
@@ -240,6 +268,7 @@ __global__ void __launch_bounds__(512) norm_grad_stream_kernel(const __grid_cons
   Ring ring;
   ring.start(p, p.residual != nullptr ? 3 : 2, smem, full, &stop);
   uint4 wt[V];
+  const float inv_n = 1.f / static_cast<float>(p.hidden);
   float acc[V][8];  // the weight's gradient, of this thread's columns
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -277,9 +306,8 @@ __global__ void __launch_bounds__(512) norm_grad_stream_kernel(const __grid_cons
     if (ring.leader() && group != blockIdx.x)
       ring.issue(p, stage == 0 ? ring.stages - 1 : stage - 1,
                  group + static_cast<int64_t>(ring.stages - 1) * gridDim.x);
-    const float n = static_cast<float>(p.hidden);
-    const float rstd = rsqrtf(s.rr / n + p.eps);
-    const float c = rstd * rstd * (s.gr / n);
+    const float rstd = rsqrtf(fmaf(s.rr, inv_n, p.eps));
+    const float c = rstd * rstd * (s.gr * inv_n);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int w = w0 + i * step;
@@ -343,7 +371,9 @@ cudaError_t launch_ring(K kernel, const NormParams& p, const NormStream& s, cuda
 template <typename T, bool FP8>
 cudaError_t forward(const NormParams& p, const NormStream& s, cudaStream_t stream, int pdl) {
   switch (s.v) {
-    case 1: return launch_ring(norm_stream_kernel<T, 1, FP8>, p, s, stream, pdl);
+    case 1:
+      if constexpr (!FP8) return launch_ring(norm_stream_kernel<T, 1, FP8>, p, s, stream, pdl);
+      break;
     case 2: return launch_ring(norm_stream_kernel<T, 2, FP8>, p, s, stream, pdl);
     case 4: return launch_ring(norm_stream_kernel<T, 4, FP8>, p, s, stream, pdl);
     case 8: return launch_ring(norm_stream_kernel<T, 8, FP8>, p, s, stream, pdl);
@@ -364,22 +394,28 @@ cudaError_t backward(const NormParams& p, const NormStream& s, cudaStream_t stre
 
 }  // namespace
 
-// About 256 threads a CTA and two CTAs an SM, the ring all of its shared memory. Not for
-// rows that give a CTA no second turn, nor for those of which it does not hold two.
-bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, int sms, NormStream* s) {
+// About 256 threads a CTA, and as many CTAs an SM as there are registers for and rings of
+// two stages fit: a turn is a chain of latencies that others fill. Not for rows that give a CTA no second
+// turn, nor for those of which a ring does not hold two.
+bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, bool pairs, int sms, NormStream* s) {
   if (hidden % 8 != 0) return false;
   const int words = static_cast<int>(hidden / 8);
-  s->v = words <= 256 ? 1 : words <= 1024 ? 2 : words <= 2048 ? 4 : 8;
+  s->v = words <= 256 && !pairs ? 1 : words <= 1024 ? 2 : words <= 2048 ? 4 : 8;
   s->threads = (words + s->v * 32 - 1) / (s->v * 32) * 32;
   s->rows = s->threads >= 192 ? 1 : 256 / s->threads;
   const size_t stage = static_cast<size_t>(s->rows) * words * 16 * arrays;
-  const int per_sm = 2 * 2 * stage <= kStreamSmem ? 2 : 1;
+  // (16384 x 5120 to e4m3, two CTAs an SM 94 us, three 104; 16384 x 4096 backward 90 and 85)
+  int per_sm = s->v == 2 && s->threads <= 320 && !pairs ? 3 : stream_per_sm(s->v);
+  while (per_sm > 1 && per_sm * 2 * stage > kStreamSmem) --per_sm;
   s->stages = static_cast<int>(kStreamSmem / per_sm / stage);
   if (s->stages > kMaxStages) s->stages = kMaxStages;
   if (s->stages < 2) return false;
   s->smem = s->stages * stage;
-  s->ctas = per_sm * sms;
-  return (rows + s->rows - 1) / s->rows > s->ctas;
+  const int64_t groups = (rows + s->rows - 1) / s->rows, most = static_cast<int64_t>(per_sm) * sms;
+  // as many turns for every CTA, but for one
+  const int64_t turns = (groups + most - 1) / most;
+  s->ctas = static_cast<int>(turns > 0 ? (groups + turns - 1) / turns : 0);
+  return turns >= kLeastTurns;
 }
 
 cudaError_t launch_norm_stream(const NormParams& p, const NormStream& s, int bf16, cudaStream_t stream,

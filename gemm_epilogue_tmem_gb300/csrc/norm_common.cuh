@@ -148,7 +148,8 @@ struct NormStream {
   int stages, ctas;
   size_t smem;
 };
-bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, int sms, NormStream* s);
+// (pairs: the threads have pairs of words)
+bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, bool pairs, int sms, NormStream* s);
 cudaError_t launch_norm_stream(const NormParams& p, const NormStream& s, int bf16,
                                cudaStream_t stream, int pdl);
 cudaError_t launch_norm_grad_stream(const NormParams& p, const NormStream& s, int bf16,
