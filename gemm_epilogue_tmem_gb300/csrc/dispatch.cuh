@@ -10,7 +10,8 @@ namespace gf {
 template <int EPI, typename T, bool B_MN, int BN>
 cudaError_t launch_instance(const LaunchArgs& a) {
   auto kernel = gemm_epilog_kernel<EPI, T, B_MN, BN>;
-  constexpr int smem = TileCfg<BN, epi_dual(EPI) ? 2 : 1, epi_has_bgrad(EPI)>::kSmemBytes;
+  constexpr int smem =
+      TileCfg<BN, epi_dual(EPI) ? 2 : 1, epi_has_bgrad(EPI), single_stg(EPI)>::kSmemBytes;
   static bool attr_set = false;  // once per instance and process
   if (!attr_set) {
     cudaError_t e =

@@ -47,8 +47,9 @@ constexpr int kBK = 64;  // 64 x 16-bit = 128 bytes = one swizzle row
 constexpr int kThreads = 192;
 
 // NB = number of B operands (2 for the gate+up SwiGLU: two accumulators);
-// RED = the epilog reduces a bias gradient and needs the [4][BN] scratch.
-template <int BN, int NB = 1, bool RED = false>
+// RED = the epilog reduces a bias gradient and needs the [4][BN] scratch; STG = a 2 KB
+// staging buffer per epilogue warp (single_stg).
+template <int BN, int NB = 1, bool RED = false, bool STG = false>
 struct TileCfg {
   static_assert(BN == 128 || BN == 256, "tile N");
   static_assert(NB == 1 || (NB == 2 && BN == 128), "two B operands need 128-wide tiles");
@@ -59,11 +60,16 @@ struct TileCfg {
   static constexpr int kTmemCols = 2 * kAccCols;          // two accumulator buffers
   static constexpr int kCtrlBytes = kSmemCtrlBytes;
   static constexpr int kRedBytes = RED ? 4 * BN * 4 : 0;
-  static constexpr int kStages = ring_stages(kABytes + kStageBBytes, kRedBytes);
+  static constexpr int kStgBytes = STG ? 4 * 2048 : 0;
+  static constexpr int kStages = ring_stages(kABytes + kStageBBytes, kRedBytes + kStgBytes);
   static constexpr int kSmemBytes =
-      kSmemAlignSlack + kStages * (kABytes + kStageBBytes) + kCtrlBytes + kRedBytes;
+      kSmemAlignSlack + kStages * (kABytes + kStageBBytes) + kCtrlBytes + kRedBytes + kStgBytes;
   static_assert(kStages >= 3 && kSmemBytes <= kSmemPerCta, "shared memory budget");
 };
+
+// The single-CTA kernel's epilogs whose rows go through the staging buffer: RESIDUAL,
+// with up to three 16-bit streams (1003 x 2056 x 1000 with GELU and z saved 19.2 us without).
+GF_HD constexpr bool single_stg(int epi) { return epi == EPI_RESIDUAL; }
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);
@@ -137,16 +143,36 @@ __device__ __forceinline__ float sigmoid_f(float g) { return fmaf(0.5f, tanh_fas
 
 __device__ __forceinline__ float silu_f(float g) { return g * sigmoid_f(g); }
 
-// The activations of the RESIDUAL epilogue, z / (1 + e^-u)
-// with u = z (SiLU) or 2 c (z + k z^3) (GELU's tanh form: (1 + tanh v) / 2 =
-// 1 / (1 + e^-2v)), by the hardware exponential and reciprocal: errors of a few
-// 2^-24 relative to the value. Their sum with the residual is what is rounded, and
+// The activations of the RESIDUAL epilogue, z / (1 + e^-u) with u = z (SiLU) or
+// 2 c (z + k z^3) (GELU's tanh form: (1 + tanh v) / 2 = 1 / (1 + e^-2v)): e^-u by the
+// hardware's exponential of base 2, the base in the constants, and its reciprocal; errors of
+// a few 2^-24 relative to the value. The sum with the residual is what is rounded, and
 // fp16 keeps 2^-11 of it, which the error of tanh.approx would reach.
-__device__ __forceinline__ float act_value(int act, float z) {
-  if (act == kActRelu) return z > 0.f ? z : 0.f;
-  if (act == kActNone) return z;
-  const float u = act == kActGelu ? z * fmaf(2.f * kGeluCK, z * z, 2.f * kGeluC) : z;
-  return __fdividef(z, 1.f + __expf(-u));
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? z : 0.f;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float t = ACT == kActGelu ? z * fmaf(-2.f * kGeluCK * kLog2e, z * z, -2.f * kGeluC * kLog2e)
+                                  : z * -kLog2e;
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return z * s;
+}
+
+// (one branch for all of them: 1003 x 2056 x 1000 with one for each 18.8 us)
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
+  if (act == kActGelu) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_value<kActGelu>(v[j]);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_value<kActSilu>(v[j]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_value<kActRelu>(v[j]);
+  }
 }
 
 // 32 consecutive values of one row -> 4 x 16-byte stores of T (columns at or
@@ -626,10 +652,7 @@ __device__ __forceinline__ bool epilogue_drain(const GemmParams& p, uint32_t t_r
         }
       }
       if (p.aux_out != nullptr) emit(true, col0, v);  // what the activation takes, rounded to T
-      if (p.act != kActNone) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = act_value(p.act, v[j]);
-      }
+      apply_act(p.act, v);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float r8[8];
@@ -1045,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmB2, const GemmParams p) {
   constexpr int NB = epi_dual(EPI) ? 2 : 1;
-  using C = TileCfg<BN, NB, epi_has_bgrad(EPI)>;
+  using C = TileCfg<BN, NB, epi_has_bgrad(EPI), single_stg(EPI)>;
   constexpr int S = C::kStages;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ uint8_t smem_raw[];
@@ -1267,7 +1290,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(tempty0 + 8u * buf);
         continue;
       }
-      epilogue_drain<EPI, T, BN>(p, t_row, m0, n0, q, lane, red);
+      if constexpr (single_stg(EPI))
+        epilogue_drain<EPI, T, BN, BN, true>(
+            p, t_row, m0, n0, q, lane, red,
+            ctrl + C::kCtrlBytes + C::kRedBytes + 2048u * static_cast<uint32_t>(q));
+      else
+        epilogue_drain<EPI, T, BN>(p, t_row, m0, n0, q, lane, red);
       // accumulator buffer drained: the MMA warp may reuse it
       tc_fence_before();
       __syncwarp();

@@ -24,6 +24,8 @@ int stages_for(int tile_n, int pair, int epi) {
   if (pair && tile_n == 512)
     return red ? PairCfg<1, true, true>::kStages : PairCfg<1, false, true>::kStages;
   if (pair) return red ? PairCfg<1, true>::kStages : PairCfg<1, false>::kStages;
+  if (single_stg(epi))
+    return tile_n == 256 ? TileCfg<256, 1, false, true>::kStages : TileCfg<128, 1, false, true>::kStages;
   if (tile_n == 256) return red ? TileCfg<256, 1, true>::kStages : TileCfg<256, 1, false>::kStages;
   return red ? TileCfg<128, 1, true>::kStages : TileCfg<128, 1, false>::kStages;
 }

@@ -289,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.aux_out) + at(i)) =
                 make_uint4(pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]), pack2<T>(z[4], z[5]),
                            pack2<T>(z[6], z[7]));
+          apply_act(p.act, z);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = act_value(p.act, z[j]) + r8[j];
+          for (int j = 0; j < 8; ++j) z[j] += r8[j];
           *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at(i)) =
               make_uint4(pack2<T>(z[0], z[1]), pack2<T>(z[2], z[3]), pack2<T>(z[4], z[5]),
                          pack2<T>(z[6], z[7]));
