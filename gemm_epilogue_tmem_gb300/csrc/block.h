@@ -18,7 +18,8 @@ struct RouteParams {
   int32_t renorm;
   float scale;
   int64_t ld;           // elements between rows of logits and of d_logits
-  // a power of two of lanes, 1 << lane_shift, share a group, and the experts of each
+  // set by the launcher: a power of two of lanes, 1 << lane_shift, share a group; the
+  // experts of each
   int32_t lane_shift, per_lane;
   int32_t sms;
   int32_t vector;       // 1: a lane's experts are loaded in words (aligned, none missing)

@@ -32,7 +32,7 @@ namespace gf {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kMaxSlots = 64;  // two a lane
+constexpr int kManyTokens = 2048;  // from which on a token may have eight lanes
 constexpr int kWarps = 4;      // tokens of a CTA
 constexpr float kNoScore = -745.f;  // e to this is 0 in 64 bits
 
@@ -93,12 +93,14 @@ __device__ __forceinline__ float exp_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
   return y;
 }
-__device__ __forceinline__ float fast_score(const RouteParams& p, float x, float top, float inv) {
-  if (!p.sigmoid) return exp_fast(x - top) * inv;
+__device__ __forceinline__ float fast_logistic(float x) {
   const float e = exp_fast(-fabsf(x));
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return (x >= 0.f ? 1.f : e) * r;
+}
+__device__ __forceinline__ float fast_score(const RouteParams& p, float x, float top, float inv) {
+  return p.sigmoid ? fast_logistic(x) : exp_fast(x - top) * inv;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -347,31 +349,68 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, const L* row, 
 // CTAs of an SM (the grid is as large: warps loop over the tokens)
 constexpr int resident(int vpl) { return vpl <= 8 ? 6 : vpl <= 16 ? 5 : 2; }
 
-// BIAS: scores are compared, else logits.
-template <typename L, int VPL, bool BIAS>
+// over the W lanes of a token
+template <int W>
+__device__ __forceinline__ int lanes_max(int v) {
+  if constexpr (W == 32) {
+    return __reduce_max_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int d = W / 2; d >= 1; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  }
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int d = W / 2; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = W / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// W lanes a token, VPL experts a lane. BIAS: scores are compared, else logits. Eight lanes
+// a token: 16-bit logits that are compared as they are, of which nothing is ever in doubt.
+template <typename L, int W, int VPL, bool BIAS>
 __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
     route_kernel(const __grid_constant__ RouteParams p) {
   constexpr int MASK = VPL - 1;
-  constexpr int S = VPL >= 32 ? 2 : 1;  // slots a lane: the instances for more than 32 have two
+  constexpr int T = 32 / W;  // tokens of a warp
+  // slots a lane: with a warp a token, the instances for more than 32 have two
+  constexpr int S = W < 32 || VPL >= 32 ? 2 : 1;
   // keys tell everything apart but what is equal
   constexpr bool kExact = !BIAS && sizeof(L) == 2;
   // what the place's bits take from a value, relative to it
   constexpr float kCut = 1.2e-7f * VPL;
+  static_assert(W == 32 || kExact, "no doubt with fewer lanes");
+  // a token's lanes each have a sorted list: short ones in registers, others in shared memory
+  constexpr bool kListed = W < 32 && VPL > 8;
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  __shared__ int2 slot_of[kWarps][kMaxSlots + 2];
-  int2* slots = slot_of[threadIdx.x >> 5];
+  // the lane among its token's, and the token among its warp's
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & (W - 1), part = (threadIdx.x & 31) / W;
+  __shared__ int2 slot_of[kWarps * T][W * S + 2];
+  __shared__ int list_of[kListed ? 32 * kWarps : 1][VPL + 1];
+  int2* slots = slot_of[warp * T + part];
+  int* list = list_of[kListed ? threadIdx.x : 0];
   const uint32_t below = (1u << lane) - 1u;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t token = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (token >= p.tokens) return;
+  auto votes = [&](bool v) {
+    const uint32_t b = __ballot_sync(kAll, v);
+    return W == 32 ? b : b >> (W * part) & ((1u << (W & 31)) - 1u);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * T;
+  int64_t token = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * T + part;
+  if (token - part >= p.tokens) return;
   // this lane's experts
   const int g = lane >> p.lane_shift, lane_mask = (1 << p.lane_shift) - 1;
   const int in_group = (lane & lane_mask) * p.per_lane;
   const int base = g * p.group_size + in_group;
-  int count = g < p.groups ? min(p.per_lane, p.group_size - in_group) : 0;
-  if (count < 0) count = 0;
+  const int experts_here = g < p.groups ? max(0, min(p.per_lane, p.group_size - in_group)) : 0;
+  int count = token < p.tokens ? experts_here : 0;
   float bias[BIAS ? VPL : 1];
   if constexpr (BIAS) {
 #pragma unroll
@@ -392,13 +431,13 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
 #pragma unroll
       for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);  // (of those that are numbers)
       if (m != m) m = -INFINITY;
-      m = __int_as_float(ordered(__reduce_max_sync(kAll, ordered(__float_as_int(m + 0.f)))));
+      m = __int_as_float(ordered(lanes_max<W>(ordered(__float_as_int(m + 0.f)))));
       top = m == -INFINITY ? 0.f : m;
       if (BIAS || sums || !p.renorm) {
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) sum += exp_fast(l[i] - top);
-        inv = 1.f / warp_sum(sum);
+        inv = 1.f / lanes_sum<W>(sum);
       }
     }
     // the error of fast_score: of the exponential (2^-22 of it and 2^-23 |x|), the sum
@@ -406,13 +445,21 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
     // is `inv` for softmax and 1 for sigmoid.
     const float error = p.sigmoid ? 6e-7f : inv * (1.1e-6f + VPL * 6e-8f);
     int key[VPL];
+    if constexpr (BIAS) {
+      float c[VPL];
+      if (p.sigmoid) {  // (one branch for all experts)
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if constexpr (BIAS)
-        key[i] = key_of<MASK>(
-            fast_score(p, l[i], top, inv) + (l[i] == -INFINITY ? -INFINITY : bias[i]), i);
-      else
-        key[i] = key_of<MASK>(l[i], i);
+        for (int i = 0; i < VPL; ++i) c[i] = fast_logistic(l[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = exp_fast(l[i] - top) * inv;
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        key[i] = key_of<MASK>(c[i] + (l[i] == -INFINITY ? -INFINITY : bias[i]), i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = key_of<MASK>(l[i], i);
     }
     sort_keys<VPL>(key);
     bool out = false;  // this lane's group goes
@@ -443,12 +490,12 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
       int rank = 0;
       for (int h0 = 0; h0 < p.groups; h0 += lane_mask + 1) {
         const int h = h0 + (lane & lane_mask);
-        const int other = __shfl_sync(kAll, mine, (h << p.lane_shift) & 31);
+        const int other = __shfl_sync(kAll, mine, (h << p.lane_shift) & (W - 1), W);
         rank += h < p.groups && (other > mine || (other == mine && h < g)) ? 1 : 0;
       }
       for (int d = 0; d < p.lane_shift; ++d) rank += __shfl_xor_sync(kAll, rank, 1 << d);
       bool in = g < p.groups && rank < p.topk_groups;
-      if (!kExact || sums) {
+      if (W == 32 && (!kExact || sums)) {
         // the worst group that stays and the best that goes
         const int lo = __reduce_min_sync(kAll, in ? mine : INT_MAX);
         const int hi = __reduce_max_sync(kAll, in ? INT_MIN : mine);
@@ -470,31 +517,48 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
       for (int i = 0; i < VPL; ++i) key[i] = INT_MIN;
     }
 
+    int head = key[0], place = 0;
+    if constexpr (kListed) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) list[i] = key[i];
+      list[VPL] = INT_MIN;
+    }
+
     // the picks, each put down by the lane that has it: key and expert
     __syncwarp();
     int found = 0;
-    for (; found < picks; ++found) {
-      const int mine = key[0] & ~MASK;
-      const int best = __reduce_max_sync(kAll, mine);
-      if (best < kNone) break;
-      const uint32_t have = __ballot_sync(kAll, mine == best);
-      if (mine == best && (have & below) == 0u) {
-        slots[found] = make_int2(mine, base + (MASK - (key[0] & MASK)));
+    for (int j = 0; j < picks; ++j) {
+      const int mine = head & ~MASK;
+      const int best = lanes_max<W>(mine);
+      const bool some = best >= kNone;
+      if (W == 32 ? !some : !__any_sync(kAll, some)) break;
+      const uint32_t have = votes(mine == best);
+      if (some) ++found;
+      if (some && mine == best && (have & below) == 0u) {
+        slots[j] = make_int2(mine, base + (MASK - (head & MASK)));
+        if constexpr (kListed) {
+          head = list[++place];
+        } else {
 #pragma unroll
-        for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
-        key[VPL - 1] = INT_MIN;
+          for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+          key[VPL - 1] = INT_MIN;
+          head = key[0];
+        }
       }
     }
     __syncwarp();
     // the next token's logits come meanwhile
     const int64_t next = token + step;
-    const bool more = next < p.tokens;
-    if (more) load_logits<L, VPL>(p, row + step * p.ld, base, count, l);
+    const bool valid = token < p.tokens, more = next - part < p.tokens;
+    if (more) {
+      count = next < p.tokens ? experts_here : 0;
+      load_logits<L, VPL>(p, row + step * p.ld, base, count, l);
+    }
     int expert[S];
     float value[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int j = lane + 32 * s;
+      const int j = lane + W * s;
       const int2 slot = j < found ? slots[j] : make_int2(INT_MIN, -1);
       expert[s] = slot.y;
       value[s] = __int_as_float(ordered(slot.x));
@@ -508,7 +572,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
       };
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const int j = lane + 32 * s;
+        const int j = lane + W * s;
         if (j < p.topk && j + 1 < found) {
           const int2 follow = slots[j + 1];
           if (near(value[s], __int_as_float(ordered(follow.x)))) {
@@ -525,7 +589,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
         // the picks and the one after them, if the next is further away; else all over
         bool few = p.topk < 32;
         if (few && found > p.topk) {
-          const int m = __reduce_max_sync(kAll, key[0] & ~MASK);
+          const int m = __reduce_max_sync(kAll, head & ~MASK);
           const float last = __shfl_sync(kAll, value[0], p.topk);
           few = m < kNone || !near(last, __int_as_float(ordered(m)));
         }
@@ -542,7 +606,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
     }
 #pragma unroll
     for (int s = 0; s < S; ++s)
-      if (lane + 32 * s >= p.topk) expert[s] = -1;
+      if (lane + W * s >= p.topk) expert[s] = -1;
 
     // the weights; softmax over the chosen alone where they are renormalised, unless
     // their scores are 0 in 64 bits too
@@ -552,7 +616,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
     bool none = false;
     if (!p.sigmoid && p.renorm) {
       const float of_all = top;
-      top = warp_max(fmaxf(x[0], x[S - 1]));
+      top = lanes_max<W>(fmaxf(x[0], x[S - 1]));
       none = top - of_all < kNoScore;
       if (top == -INFINITY) top = 0.f;
     }
@@ -566,16 +630,16 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
     }
     float factor = p.scale;
     if (p.renorm) {
-      const float sum = warp_sum(S == 2 ? w[0] + w[S - 1] : w[0]);
+      const float sum = lanes_sum<W>(S == 2 ? w[0] + w[S - 1] : w[0]);
       // (chosen scores that are all 0 stay 0)
-      factor = sum == 0.f || none ? 0.f : p.scale / sum;
+      factor = sum == 0.f || none ? 0.f : __fdividef(p.scale, sum);
       // a logit without a number (or infinite) makes every score NaN, chosen or not
       if (inv != inv) factor = inv;
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int j = lane + 32 * s;
-      if (j < p.topk) {
+      const int j = lane + W * s;
+      if (valid && j < p.topk) {
         p.expert[token * p.topk + j] = expert[s];
         p.weight[token * p.topk + j] = w[s] * factor;
       }
@@ -700,26 +764,55 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
   for (int64_t e = lane; e < p.ld; e += 32) out[e] = to_logit<L>(e < p.experts ? d[e] : 0.f);
 }
 
-template <typename L, int VPL>
+template <typename L, int W, int VPL>
 cudaError_t route_of(const RouteParams& p, cudaStream_t stream, int pdl) {
   // as many CTAs as are resident at once; more tokens follow in their loop
-  const int64_t all = (static_cast<int64_t>(p.tokens) + kWarps - 1) / kWarps;
+  constexpr int kTokens = kWarps * (32 / W);
+  const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
   const int64_t most = static_cast<int64_t>(p.sms) * resident(VPL);
   const dim3 grid(static_cast<unsigned>(all < most ? all : most)), block(32 * kWarps);
-  return p.bias != nullptr ? launch_pdl(route_kernel<L, VPL, true>, grid, block, 0, stream, pdl, p)
-                           : launch_pdl(route_kernel<L, VPL, false>, grid, block, 0, stream, pdl, p);
+  if constexpr (W == 32) {
+    if (p.bias != nullptr)
+      return launch_pdl(route_kernel<L, W, VPL, true>, grid, block, 0, stream, pdl, p);
+  }
+  return launch_pdl(route_kernel<L, W, VPL, false>, grid, block, 0, stream, pdl, p);
+}
+
+// The lanes of w that share a group, a power of two, and the experts of each.
+template <typename L>
+RouteParams map_lanes(RouteParams p, int w) {
+  p.lane_shift = 0;
+  while (p.groups << (p.lane_shift + 1) <= w) ++p.lane_shift;
+  const int lanes = 1 << p.lane_shift, size = static_cast<int>(sizeof(L));
+  p.per_lane = (p.group_size + lanes - 1) / lanes;
+  const int bytes = p.per_lane * size, word = bytes < 16 ? bytes : 16;
+  p.vector = (p.per_lane & (p.per_lane - 1)) == 0 && p.group_size == lanes * p.per_lane &&
+                     (p.ld * size) % word == 0
+                 ? 1
+                 : 0;
+  return p;
 }
 
 template <typename L>
-cudaError_t route(const RouteParams& p, cudaStream_t stream, int pdl) {
+cudaError_t route(const RouteParams& args, cudaStream_t stream, int pdl) {
+  if constexpr (sizeof(L) == 2) {
+    if (args.tokens >= kManyTokens && args.bias == nullptr && args.groups <= 8 && args.topk <= 16 &&
+        (args.groups == 1 || args.group_best == 1)) {
+      const RouteParams p = map_lanes<L>(args, 8);
+      if (p.per_lane <= 4) return route_of<L, 8, 4>(p, stream, pdl);
+      if (p.per_lane <= 8) return route_of<L, 8, 8>(p, stream, pdl);
+      if (p.per_lane <= 16) return route_of<L, 8, 16>(p, stream, pdl);
+    }
+  }
+  const RouteParams p = map_lanes<L>(args, 32);
   const int n = p.topk > 32 && p.per_lane < 32 ? 32 : p.per_lane;  // two slots a lane
-  if (n <= 1) return route_of<L, 1>(p, stream, pdl);
-  if (n <= 2) return route_of<L, 2>(p, stream, pdl);
-  if (n <= 4) return route_of<L, 4>(p, stream, pdl);
-  if (n <= 8) return route_of<L, 8>(p, stream, pdl);
-  if (n <= 16) return route_of<L, 16>(p, stream, pdl);
-  if (n <= 32) return route_of<L, 32>(p, stream, pdl);
-  return route_of<L, 64>(p, stream, pdl);
+  if (n <= 1) return route_of<L, 32, 1>(p, stream, pdl);
+  if (n <= 2) return route_of<L, 32, 2>(p, stream, pdl);
+  if (n <= 4) return route_of<L, 32, 4>(p, stream, pdl);
+  if (n <= 8) return route_of<L, 32, 8>(p, stream, pdl);
+  if (n <= 16) return route_of<L, 32, 16>(p, stream, pdl);
+  if (n <= 32) return route_of<L, 32, 32>(p, stream, pdl);
+  return route_of<L, 32, 64>(p, stream, pdl);
 }
 
 template <typename L>

@@ -98,18 +98,7 @@ static gf::RouteParams route_params(const gf_plan* p, const void* logits) {
   r.scale = p->scale;
   r.ld = p->ld;
   r.logits = logits;
-  // a power of two of lanes for each group
-  r.lane_shift = 5;
-  while (r.groups << r.lane_shift > 32) --r.lane_shift;
-  const int lanes = 1 << r.lane_shift;
-  r.per_lane = (r.group_size + lanes - 1) / lanes;
   r.sms = p->num_sms;
-  const int size = p->dtype == GF_F32 ? 4 : 2;
-  const int bytes = r.per_lane * size, word = bytes < 16 ? bytes : 16;
-  r.vector = (r.per_lane & (r.per_lane - 1)) == 0 && r.group_size == lanes * r.per_lane &&
-                     (r.ld * size) % word == 0
-                 ? 1
-                 : 0;
   return r;
 }
 

@@ -20,7 +20,10 @@ NAN, INF = float("nan"), float("inf")
 SHAPES = [(1, 1, 1, 1, 1, 1), (5, 3, 3, 1, 1, 1), (0, 8, 2, 1, 1, 1), (67, 8, 2, 4, 2, 1), (130, 60, 6, 1, 1, 1), (130, 60, 6, 3, 2, 2),
           (99, 64, 8, 8, 8, 2), (41, 128, 8, 1, 1, 1), (300, 160, 6, 8, 3, 2), (257, 256, 8, 8, 4, 2), (77, 256, 8, 32, 4, 1),
           (33, 33, 4, 33 // 11, 2, 2), (19, 17, 5, 17, 9, 2), (31, 512, 33, 1, 1, 1), (7, 1000, 64, 4, 3, 2), (9, 1024, 10, 1, 1, 1),
-          (5, 1023, 8, 3, 2, 2), (6, 1020, 8, 17, 5, 2), (12, 1024, 8, 32, 32, 2), (40, 2, 1, 2, 1, 2)]
+          (5, 1023, 8, 3, 2, 2), (6, 1020, 8, 17, 5, 2), (12, 1024, 8, 32, 32, 2), (40, 2, 1, 2, 1, 2),
+          # many tokens, eight lanes each: the last warp not full, every number of experts a lane, one group's lane that has all picks
+          (2049, 8, 2, 1, 1, 1), (2500, 60, 6, 1, 1, 1), (2051, 64, 8, 8, 3, 2), (2048, 128, 16, 4, 2, 1), (3003, 160, 6, 8, 3, 2), (2100, 256, 8, 8, 1, 2),
+          (2600, 256, 8, 8, 4, 2), (2050, 96, 3, 3, 2, 2)]
 
 
 def logits_of(tokens, ld, seed, dtype, size=1.5):
@@ -66,9 +69,10 @@ def test_choice(tokens, experts, topk, groups, topk_groups, best, dtype, score, 
 @pytest.mark.parametrize("dtype", [gf.GF_F32, gf.GF_BF16])
 @pytest.mark.parametrize("score,biased", [(SOFTMAX, True), (SOFTMAX, False), (SIGMOID, True), (SIGMOID, False)])
 @pytest.mark.parametrize("groups,topk_groups,best", [(1, 1, 1), (4, 2, 2), (4, 2, 1), (5, 2, 2)])
-def test_scores_next_to_each_other(dtype, score, biased, groups, topk_groups, best):
+@pytest.mark.parametrize("tokens", [200, 2061])
+def test_scores_next_to_each_other(dtype, score, biased, groups, topk_groups, best, tokens):
     """Equal logits, and logits a step of fp32 apart with biases that nearly undo them."""
-    tokens, experts = 200, 40
+    experts = 40
     rng = np.random.default_rng(3)
     l = rng.choice([0.0, -0.0, 0.5, 0.75, 1.0], (tokens, experts)).astype(np.float32)
     if dtype == gf.GF_F32:
@@ -85,8 +89,9 @@ def test_scores_next_to_each_other(dtype, score, biased, groups, topk_groups, be
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 @pytest.mark.parametrize("biased", [True, False])
 @pytest.mark.parametrize("groups,topk_groups,best", [(1, 1, 1), (4, 2, 2), (4, 2, 1)])
-def test_masked_and_without_a_number(score, biased, groups, topk_groups, best):
-    tokens, experts, topk = 12, 64, 8
+@pytest.mark.parametrize("tokens", [12, 2060])
+def test_masked_and_without_a_number(score, biased, groups, topk_groups, best, tokens):
+    experts, topk = 64, 8
     logits = logits_of(tokens, experts, 4, gf.GF_F32)
     logits[0] = -INF                       # nothing left
     logits[1, 3:] = -INF                   # fewer than topk
