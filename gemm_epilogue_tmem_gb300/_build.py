@@ -24,7 +24,7 @@ SOURCES = ["runtime.cu", "k_none_bias.cu", "k_relu.cu", "k_drelu.cu", "k_gelu.cu
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "gemm_kernel_2sm.cuh", "dispatch.cuh", "launch.h",
            "params.h", "runtime_internal.h", "plan.h", "moe.h", "fp8.cuh", "fp8_common.cuh",
            "fp8_params.h", "block.h",
-           "residual_narrow.h", "norm_common.cuh"]
+           "residual_narrow.h", "norm_common.cuh", "two_float.cuh"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",

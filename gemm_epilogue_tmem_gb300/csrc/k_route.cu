@@ -15,8 +15,8 @@
 // Experts are whole numbers, and scores may lie closer together than fp32, less the
 // bits of the place, tells them apart. The comparisons that decide something are
 // therefore looked at again: where two differ by no more than their error bounds, and
-// not for equal inputs, those in question are compared in 64 bits (a few in a thousand
-// tokens of 256 experts with a bias). Without a bias experts are compared by their
+// not for equal inputs, those in question are compared in two fp32, and where that leaves it open in 64
+// bits (a few in a thousand tokens of 256 experts with a bias, and hardly any). Without a bias experts are compared by their
 // logits; those of 16 bits leave the place's bits free and are exact at once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,6 +27,7 @@
 
 #include "block.h"
 #include "ptx.cuh"
+#include "two_float.cuh"
 
 namespace gf {
 namespace {
@@ -156,17 +157,67 @@ __device__ __forceinline__ void exact_softmax(const RouteParams& p, const L* row
   total = warp_sum(sum);
 }
 
-// Whether this lane's group is one of the best, in 64 bits. Groups whose fp32 score
-// lies between `low` and `high` are in question, the others keep theirs; of them only
-// experts whose fp32 score is at least `least` may be among the two best.
+// ------------------------------------------------------ comparisons more closely
+// Scores in two fp32, right to 2^-38 of the largest: enough for all but a few in a
+// million of the comparisons that fp32 leaves open, at a third of the time of 64 bits.
+struct Scale {
+  float top;   // softmax: the largest logit, and what every exponential is multiplied by
+  Two inv;
+  float size;  // the largest score
+};
+
 template <typename L>
-__device__ __noinline__ bool groups_exactly(const RouteParams& p, const L* row, int base, int count,
-                                            float score32, float low, float high, float least,
-                                            float top32, float inv) {
+__device__ __forceinline__ Scale scale_closely(const RouteParams& p, const L* row) {
+  Scale c = {0.f, {1.f, 0.f}, 1.f};
+  if (p.sigmoid) return c;
   const int lane = threadIdx.x & 31;
-  double top = 0., total = 1.;
+  float top = -INFINITY;
+  for (int e = lane; e < p.experts; e += 32) top = fmaxf(top, as_float(row[e]));
+  top = warp_max(top);
+  c.top = top == -INFINITY ? 0.f : top;
+  Two sum = {0.f, 0.f};
+#pragma unroll 2
+  for (int e = lane; e < p.experts; e += 32) {
+    const float l = as_float(row[e]);
+    const Two x = two_of(c.top, -l);
+    if (l != -INFINITY) sum = two_add(sum, two_exp_minus(x.h, x.l));
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1)
+    sum = two_add(sum, Two{__shfl_xor_sync(kAll, sum.h, d), __shfl_xor_sync(kAll, sum.l, d)});
+  c.inv = two_inverse(sum);
+  c.size = c.inv.h;
+  return c;
+}
+
+__device__ __forceinline__ Two score_closely(const RouteParams& p, const Scale& c, float l) {
+  if (p.sigmoid) {
+    const Two e = two_exp_minus(fabsf(l), 0.f);
+    const Two q = two_inverse(two_add(e, 1.f));
+    return l >= 0.f ? q : two_mul(e, q);
+  }
+  const Two x = two_of(c.top, -l);
+  return two_mul(two_exp_minus(x.h, x.l), c.inv);
+}
+
+__device__ __forceinline__ bool above(const Two& a, const Two& b) {
+  return a.h > b.h || (a.h == b.h && a.l > b.l);
+}
+// whether a is told from b (not where one is no number, or both are infinite)
+__device__ __forceinline__ bool apart(const Two& a, const Two& b, float size) {
+  return fabsf((a.h - b.h) + (a.l - b.l)) > size * 0x1p-37f + fabsf(a.h) * 0x1p-44f;
+}
+
+// Whether this lane's group is one of the best. Groups whose fp32 score lies between
+// `low` and `high` are in question, the others keep theirs; of them only experts whose
+// fp32 score is at least `least` may be among the two best. *sure: whether that decides.
+template <typename L>
+__device__ __noinline__ bool groups_closely(const RouteParams& p, const L* row, int base, int count,
+                                            float score32, float low, float high, float least,
+                                            float top32, float inv, bool* sure) {
+  const int lane = threadIdx.x & 31;
   const bool by_logit = p.bias == nullptr && p.group_best == 1;
-  if (!p.sigmoid && !by_logit) exact_softmax(p, row, top, total);
+  const Scale scale = by_logit ? Scale{0.f, {1.f, 0.f}, 0.f} : scale_closely(p, row);
   const bool asked = !(score32 < low) && !(score32 > high);
   uint64_t left = 0ull;  // places of experts to look at
   for (int i = 0; i < count && asked; ++i) {
@@ -175,60 +226,96 @@ __device__ __noinline__ bool groups_exactly(const RouteParams& p, const L* row, 
     const float c32 = by_logit ? l : fast_score(p, l, top32, inv) + add;
     if (!(c32 < least) && c32 != -INFINITY && l != -INFINITY) left |= 1ull << i;
   }
-  double a = -INFINITY, b = -INFINITY;
+  // the two best, and the logits and biases that they are of
+  const Two kNone2 = {-INFINITY, 0.f};
+  Two a = kNone2, b = kNone2;
+  float la = 0.f, lb = 0.f, ba = 0.f, bb = 0.f;
+  bool good = true;  // every score a number
   while (__any_sync(kAll, left != 0ull)) {
     if (left == 0ull) continue;
     const int i = __ffsll(static_cast<long long>(left)) - 1;
     left &= left - 1ull;
-    double c = as_float(row[base + i]);
-    if (!by_logit) {
-      c = p.sigmoid ? logistic(c) : exp(c - top) / total;
-      if (p.bias != nullptr) c += static_cast<double>(p.bias[base + i]);
-    }
-    if (before(c, 0, a, a == -INFINITY ? -1 : 1)) {
-      b = a;
-      a = c;
-    } else if (before(c, 0, b, b == -INFINITY ? -1 : 1)) {
-      b = c;
+    const float l = as_float(row[base + i]), add = p.bias != nullptr ? p.bias[base + i] : 0.f;
+    const Two c = by_logit ? Two{l, 0.f} : two_add(score_closely(p, scale, l), add);
+    good = good && fabsf(c.h) < INFINITY;
+    if (above(c, a)) {
+      b = a, lb = la, bb = ba;
+      a = c, la = l, ba = add;
+    } else if (above(c, b)) {
+      b = c, lb = l, bb = add;
     }
   }
   for (int d = 1; d < 1 << p.lane_shift; d <<= 1) {
-    const double oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
-    const bool mine = before(a, 0, oa, oa == -INFINITY ? -1 : 1);
-    const double less = mine ? oa : a, second = mine ? b : ob;
-    a = mine ? a : oa;
-    b = before(less, 0, second, second == -INFINITY ? -1 : 1) ? less : second;
+    auto from = [&](float v) { return __shfl_xor_sync(kAll, v, d); };
+    const Two oa = {from(a.h), from(a.l)}, ob = {from(b.h), from(b.l)};
+    const float ola = from(la), olb = from(lb), oba = from(ba), obb = from(bb);
+    // (of equal ones the lower lane's first, in both lanes)
+    const bool mine = above(a, oa) || (!above(oa, a) && (lane & d) == 0);
+    const Two less = mine ? oa : a, second = mine ? b : ob;
+    const float lless = mine ? ola : la, bless = mine ? oba : ba;
+    const float lsec = mine ? lb : olb, bsec = mine ? bb : obb;
+    a = mine ? a : oa, la = mine ? la : ola, ba = mine ? ba : oba;
+    const bool keep = above(second, less);
+    b = keep ? second : less, lb = keep ? lsec : lless, bb = keep ? bsec : bless;
   }
-  double score = asked ? a : static_cast<double>(score32);
-  if (asked && p.group_best == 2 && b != -INFINITY) score += b;
+  Two score = a;
+  if (p.group_best == 2 && b.h != -INFINITY) score = two_add(a, b);
+  if (p.group_best == 1) lb = bb = 0.f;
+  if (!asked) score = {score32, 0.f};
   const int g = lane >> p.lane_shift;
+  const int in_question = g < p.groups && asked ? 1 : 0;
   int rank = 0;
+  uint32_t close = 0u;  // groups that this one is not told from
   for (int h = 0; h < p.groups; ++h) {
-    const double other = __shfl_sync(kAll, score, h << p.lane_shift);
-    rank += h != g && before(other, h, score, g) ? 1 : 0;
+    const int src = h << p.lane_shift;
+    const Two o = {__shfl_sync(kAll, score.h, src), __shfl_sync(kAll, score.l, src)};
+    const float ola = __shfl_sync(kAll, la, src), olb = __shfl_sync(kAll, lb, src);
+    const float oba = __shfl_sync(kAll, ba, src), obb = __shfl_sync(kAll, bb, src);
+    const int other_in_question = __shfl_sync(kAll, in_question, src);
+    const bool same = ola == la && olb == lb && oba == ba && obb == bb;
+    const bool both = (other_in_question & in_question) != 0;
+    if (h == g) continue;
+    if (above(o, score) || (h < g && !above(score, o))) ++rank;
+    if (both && !same && !apart(o, score, 2.f * scale.size)) close |= 1u << h;
   }
-  return g < p.groups && rank < p.topk_groups;
+  const bool in = g < p.groups && rank < p.topk_groups;
+  // (which decides nothing where both stay, or go)
+  const uint32_t stay = __ballot_sync(kAll, in);
+  for (int h = 0; h < p.groups; ++h)
+    if ((close >> h & 1u) != 0u && ((stay >> (h << p.lane_shift) & 1u) != 0u) != in) good = false;
+  *sure = __all_sync(kAll, good);
+  return in;
 }
 
-// The order of up to 32 experts, one a lane (`expert` -1: none), in 64 bits: returns
-// the one of rank `lane`.
+// The order of up to 32 experts, one a lane (`expert` -1: none): returns the one of rank
+// `lane`. *sure: whether that decides it.
 template <typename L>
-__device__ __noinline__ int order_exactly(const RouteParams& p, const L* row, int expert, int n) {
+__device__ __noinline__ int order_closely(const RouteParams& p, const L* row, int expert, int n,
+                                          bool* sure) {
   const int lane = threadIdx.x & 31;
-  double top = 0., total = 1.;
-  if (!p.sigmoid && p.bias != nullptr) exact_softmax(p, row, top, total);
-  double c = 0.;
+  Scale scale = {0.f, {1.f, 0.f}, 0.f};
+  if (p.bias != nullptr) scale = scale_closely(p, row);
+  Two c = {-INFINITY, 0.f};
+  float l = 0.f, add = 0.f;
   if (expert >= 0) {
-    c = as_float(row[expert]);
-    if (p.bias != nullptr)
-      c = (p.sigmoid ? logistic(c) : exp(c - top) / total) + static_cast<double>(p.bias[expert]);
+    l = as_float(row[expert]);
+    c = {l, 0.f};
+    if (p.bias != nullptr) {
+      add = p.bias[expert];
+      c = two_add(score_closely(p, scale, l), add);
+    }
   }
+  bool good = expert < 0 || fabsf(c.h) < INFINITY;
   int rank = 0;
 #pragma unroll 4
   for (int j = 0; j < n; ++j) {
-    const double v = __shfl_sync(kAll, c, j);
+    const Two o = {__shfl_sync(kAll, c.h, j), __shfl_sync(kAll, c.l, j)};
     const int e = __shfl_sync(kAll, expert, j);
-    rank += before(v, e, c, expert) ? 1 : 0;
+    const float ol = __shfl_sync(kAll, l, j), oadd = __shfl_sync(kAll, add, j);
+    const bool same = ol == l && oadd == add;
+    if (e < 0 || expert < 0 || e == expert) continue;
+    if (same ? e < expert : above(o, c)) ++rank;
+    good = good && (same || apart(o, c, scale.size));
   }
   int out = -1;
 #pragma unroll 4
@@ -236,6 +323,7 @@ __device__ __noinline__ int order_exactly(const RouteParams& p, const L* row, in
     const int where = __shfl_sync(kAll, rank, j), e = __shfl_sync(kAll, expert, j);
     if (where == lane && e >= 0) out = e;
   }
+  *sure = __all_sync(kAll, good);
   return out;
 }
 
@@ -462,7 +550,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
       for (int i = 0; i < VPL; ++i) key[i] = key_of<MASK>(l[i], i);
     }
     sort_keys<VPL>(key);
-    bool out = false;  // this lane's group goes
+    bool out = false, unsure = false;  // this lane's group goes; the choice needs 64 bits
     if (grouped) {
       // the group's two best, over this lane's experts and then its lanes
       float a, b;
@@ -505,9 +593,12 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
           const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(terms)));
           const float tol = (BIAS || sums ? 4.f * error + 3e-7f * most : 0.f) + kCut * most;
           const float worst = __int_as_float(ordered(lo)), first = __int_as_float(ordered(hi));
-          if (!(worst - first > tol))
-            in = groups_exactly<L>(p, row, base, count, score, first - tol, worst + tol,
-                                   (sums ? b : a) - tol, top, inv);
+          if (!(worst - first > tol)) {
+            bool sure;
+            in = groups_closely<L>(p, row, base, count, score, first - tol, worst + tol,
+                                   (sums ? b : a) - tol, top, inv, &sure);
+            unsure = !sure;
+          }
         }
       }
       out = !in;
@@ -585,7 +676,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
           }
         }
       }
-      if (__any_sync(kAll, doubt || edge)) {
+      if (!unsure && __any_sync(kAll, doubt || edge)) {
         // the picks and the one after them, if the next is further away; else all over
         bool few = p.topk < 32;
         if (few && found > p.topk) {
@@ -596,12 +687,20 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
         if (few && !__any_sync(kAll, doubt)) {
           // nothing else comes near
         } else if (few) {
-          expert[0] = order_exactly<L>(p, row, expert[0], p.topk + 1);
+          bool sure;
+          const int e = order_closely<L>(p, row, expert[0], p.topk + 1, &sure);
+          if (sure) expert[0] = e;
+          unsure = !sure;
         } else {
-          int second;
-          choose_exactly<L>(p, row, expert[0], second);
-          if (S == 2) expert[S - 1] = second;
+          unsure = true;
         }
+      }
+    }
+    if constexpr (W == 32) {
+      if (unsure) {
+        int second;
+        choose_exactly<L>(p, row, expert[0], second);
+        if (S == 2) expert[S - 1] = second;
       }
     }
 #pragma unroll

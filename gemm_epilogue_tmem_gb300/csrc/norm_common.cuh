@@ -7,8 +7,7 @@
 // largest magnitude decides, so that a last bit of rstd could turn the whole block's
 // scale. That magnitude is max|r w| rstd; the products r w of 16-bit values are exact
 // in fp32, and where it matters rstd is held as the sum of two fp32, from a sum of
-// squares held the same way (error-free addition: Knuth, The Art of Computer
-// Programming 2, 4.2.2, and one Newton step), so that the scale is the one of 64-bit
+// squares held the same way and one Newton step, so that the scale is the one of 64-bit
 // arithmetic.
 #pragma once
 
@@ -19,15 +18,9 @@
 #include "block.h"
 #include "fp8.cuh"
 #include "ptx.cuh"
+#include "two_float.cuh"
 
 namespace gf {
-
-// a + b = s + e exactly
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-  s = __fadd_rn(a, b);
-  const float z = __fsub_rn(s, a);
-  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
-}
 
 // a sum of squares: fp32, or (EXACT) two fp32
 template <bool EXACT>

@@ -79,7 +79,7 @@ def test_no_device_here(L):
         assert not plan and L.gf_last_error() == gf.GF_ERR_NO_DEVICE
 
 
-@pytest.mark.parametrize("name", ["k_route.cu", "k_norm.cu", "norm_common.cuh", "k_norm_stream.cu", "k_dact.cu", "k_residual_narrow.cu"])
+@pytest.mark.parametrize("name", ["k_route.cu", "two_float.cuh", "k_norm.cu", "norm_common.cuh", "k_norm_stream.cu", "k_dact.cu", "k_residual_narrow.cu"])
 def test_no_read_only_loads(name):
     """Launched while the kernel that writes their inputs may still run, and some in place: no loads that take data for constant."""
     with open(os.path.join(CSRC, name)) as f:
