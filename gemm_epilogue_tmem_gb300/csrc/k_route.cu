@@ -763,6 +763,128 @@ __device__ __forceinline__ __nv_bfloat16 to_logit<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ float to_logit<float>(float v) { return v; }
 
+// All but softmax without renormalisation, where only the chosen experts have a
+// gradient: eight lanes a token, the row put together in shared memory in the logits' type
+// and written 16 bytes at a time. S: slots a lane.
+template <typename L, int S>
+__global__ void __launch_bounds__(32 * kWarps)
+    route_grad_sparse_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int W = 8, kPer = 16 / static_cast<int>(sizeof(L));  // elements of a word
+  extern __shared__ __align__(16) uint8_t grad_rows[];           // [tokens of the CTA][ld]
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & (W - 1), words = static_cast<int>(p.ld) / kPer;
+  uint4* mine = reinterpret_cast<uint4*>(grad_rows) + (threadIdx.x / W) * words;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kWarps / W);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (32 * kWarps / W) + threadIdx.x / W;
+  for (int64_t token = first; token - threadIdx.x / W < p.tokens; token += step) {
+    const bool valid = token < p.tokens;
+    const L* row = static_cast<const L*>(p.logits) + token * p.ld;
+    // softmax: a logit that is no number, or infinite, and the largest of all
+    float of_all = -INFINITY;
+    bool number = true;
+    if (!p.sigmoid && valid) {
+      for (int w = lane; w * kPer < p.experts; w += W) {
+        const uint4 v = reinterpret_cast<const uint4*>(row)[w];
+        const L* e = reinterpret_cast<const L*>(&v);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const float x = w * kPer + j < p.experts ? as_float(e[j]) : -INFINITY;
+          of_all = fmaxf(of_all, x);
+          number = number && x < INFINITY;
+        }
+      }
+    }
+    int expert[S];
+    float x[S], g[S], s[S], rest[S];
+    float of_chosen = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const int j = lane + W * i;
+      expert[i] = -1;
+      g[i] = s[i] = rest[i] = 0.f;
+      x[i] = -INFINITY;
+      if (valid && j < p.topk) {
+        const int e = p.expert[token * p.topk + j];
+        const float d = p.d_weight[token * p.topk + j];
+        if (e >= 0 && e < p.experts) {
+          expert[i] = e;
+          g[i] = d;
+          x[i] = as_float(row[e]);
+          of_chosen = fmaxf(of_chosen, x[i]);
+        }
+      }
+    }
+    float top = 0.f;
+    bool none = false;
+    if (!p.sigmoid) {
+      of_all = lanes_max<W>(of_all);
+      top = lanes_max<W>(of_chosen);
+      none = top - of_all < kNoScore;
+      if (top == -INFINITY) top = 0.f;
+      number = lanes_max<W>(number ? 0 : 1) == 0;
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      if (expert[i] >= 0) {
+        s[i] = p.sigmoid ? logistic(x[i]) : expf(x[i] - top);
+        rest[i] = p.sigmoid ? logistic(-x[i]) : 1.f;
+      }
+    }
+    float factor = p.scale, dot = 0.f;
+    if (p.renorm) {
+      const float sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
+      const float part = sum == 0.f || none ? 0.f : 1.f / sum;
+      dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]) * part;
+      factor = p.scale * part;
+    }
+    const L fill = to_logit<L>(number ? 0.f : NAN);  // where nothing was chosen
+    uint4 fills;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) reinterpret_cast<L*>(&fills)[j] = fill;
+    for (int w = lane; w < words; w += W) {
+      uint4 v = fills;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (w * kPer + j >= p.experts) reinterpret_cast<L*>(&v)[j] = to_logit<L>(0.f);
+      mine[w] = v;
+    }
+    __syncwarp();
+    // an expert's slots in order, by the first of them
+    float v[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) v[i] = factor * s[i] * rest[i] * (g[i] - dot);
+    float total[S];
+    bool writes[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      total[i] = 0.f;
+      writes[i] = expert[i] >= 0;
+    }
+    for (int j = 0; j < p.topk; ++j) {
+      const int from = j & (W - 1);
+      const int e = __shfl_sync(kAll, S == 2 && j >= W ? expert[S - 1] : expert[0], from, W);
+      const float add = __shfl_sync(kAll, S == 2 && j >= W ? v[S - 1] : v[0], from, W);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        if (e == expert[i]) {
+          total[i] += add;
+          if (j < lane + W * i) writes[i] = false;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (writes[i]) reinterpret_cast<L*>(mine)[expert[i]] = to_logit<L>(number ? total[i] : NAN);
+    __syncwarp();
+    if (valid) {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<L*>(p.d_logits) + token * p.ld);
+      for (int w = lane; w < words; w += W) out[w] = mine[w];
+    }
+    __syncwarp();
+  }
+}
+
 template <typename L>
 __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ float rows[];  // [kWarps][experts]
@@ -916,6 +1038,17 @@ cudaError_t route(const RouteParams& args, cudaStream_t stream, int pdl) {
 
 template <typename L>
 cudaError_t route_grad(const RouteParams& p, cudaStream_t stream, int pdl) {
+  // rows of whole words, up to 2 KB
+  const size_t row_bytes = static_cast<size_t>(p.ld) * sizeof(L);
+  if ((p.sigmoid || p.renorm) && p.topk <= 16 && row_bytes % 16 == 0 && row_bytes <= 2048) {
+    constexpr int kTokens = 32 * kWarps / 8;
+    const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
+    const int64_t most = static_cast<int64_t>(p.sms) * 6;
+    const dim3 grid(static_cast<unsigned>(all < most ? all : most)), block(32 * kWarps);
+    return p.topk <= 8
+               ? launch_pdl(route_grad_sparse_kernel<L, 1>, grid, block, kTokens * row_bytes, stream, pdl, p)
+               : launch_pdl(route_grad_sparse_kernel<L, 2>, grid, block, kTokens * row_bytes, stream, pdl, p);
+  }
   const dim3 grid((p.tokens + kWarps - 1) / kWarps), block(32 * kWarps);
   return launch_pdl(route_grad_kernel<L>, grid, block,
                     static_cast<size_t>(kWarps) * p.experts * 4, stream, pdl, p);

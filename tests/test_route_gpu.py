@@ -114,7 +114,8 @@ def test_masked_and_without_a_number(score, biased, groups, topk_groups, best, t
 
 
 @pytest.mark.parametrize("tokens,experts,topk,pad", [(1, 1, 1, 0), (0, 8, 2, 0), (67, 8, 2, 4), (130, 60, 6, 0), (41, 128, 8, 8), (257, 256, 8, 0),
-                                                      (31, 512, 33, 1), (7, 1000, 64, 0), (9, 1024, 10, 0)])
+                                                      (31, 512, 33, 1), (7, 1000, 64, 0), (9, 1024, 10, 0),
+                                                      (20001, 64, 8, 0), (130, 60, 9, 4), (1000, 120, 16, 8), (77, 512, 12, 0)])
 @pytest.mark.parametrize("dtype,score,renorm,scale", [(gf.GF_F32, SIGMOID, True, 2.5), (gf.GF_F32, SOFTMAX, False, 1.0), (gf.GF_BF16, SOFTMAX, True, 1.0),
                                                       (gf.GF_F16, SIGMOID, False, -0.5)])
 def test_gradient(tokens, experts, topk, pad, dtype, score, renorm, scale):
