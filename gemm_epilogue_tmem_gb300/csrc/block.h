@@ -48,6 +48,7 @@ struct NormParams {
   int32_t stages;       // of a streaming kernel's ring
   int32_t* status;
   uint64_t wait_limit_ns;
+  int32_t drop_load;    // test hook: 1-based index of a CTA's stage load to skip (0: none)
   const void* x;        // backward: the rows that were normed
   const void* residual; // backward: the gradient that comes along the residual
   const void* weight;

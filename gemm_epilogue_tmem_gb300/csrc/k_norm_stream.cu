@@ -64,6 +64,7 @@ struct Ring {
   // a group's rows of each array into the stage; nothing past the last group
   __device__ __forceinline__ void issue(const NormParams& p, int stage, int64_t group) const {
     if (group >= groups) return;
+    if (p.drop_load != 0 && (group - blockIdx.x) / gridDim.x + 1 == p.drop_load) return;
     const int64_t row = group * blockDim.y, left = p.rows - row;
     const int rows = left < blockDim.y ? static_cast<int>(left) : static_cast<int>(blockDim.y);
     const uint32_t bytes = static_cast<uint32_t>(rows) * static_cast<uint32_t>(p.hidden) * 2u;

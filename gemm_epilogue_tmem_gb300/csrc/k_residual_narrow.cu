@@ -311,15 +311,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// (all of an SM's memory for shared memory: two CTAs need it)
-template <typename K>
-cudaError_t set_shared(K kernel, int smem) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                 cudaSharedmemCarveoutMaxShared);
-}
-
 cudaLaunchConfig_t config(int smem, int grid, int splits, int pdl, cudaStream_t stream,
                           cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
@@ -345,7 +336,7 @@ int clusters_of(int splits) {
   int n = 0;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = config(smem, splits, splits, 0, nullptr, attr);
-  if (set_shared(kernel, smem) != cudaSuccess ||
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -357,7 +348,8 @@ template <typename T, int TR, bool B_MN>
 cudaError_t launch_instance_of(const LaunchArgs& a) {
   auto kernel = residual_narrow_kernel<T, TR, B_MN>;
   constexpr int smem = NarrowCfg<TR>::kSmemBytes;
-  const cudaError_t e = set_shared(kernel, smem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = config(smem, a.grid, a.params->k_splits, a.pdl, a.stream, attr);

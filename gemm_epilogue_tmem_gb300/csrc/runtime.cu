@@ -890,6 +890,9 @@ static gf_status epi_option_check(const gf_plan* p, gf_option option) {
   if (gf::epi_fp8(p->epi) && (option == GF_OPT_KERNEL || option == GF_OPT_WAIT_LIMIT_US ||
                               option == GF_OPT_FAULT_DROP_LOAD))
     return GF_OK;
+  if (p->epi == gf::EPI_NORM &&
+      (option == GF_OPT_WAIT_LIMIT_US || option == GF_OPT_FAULT_DROP_LOAD))
+    return GF_OK;
   return option >= GF_OPT_BGRAD_MODE && option <= GF_OPT_RASTER ? GF_ERR_UNSUPPORTED
                                                                 : GF_ERR_INVALID_VALUE;
 }

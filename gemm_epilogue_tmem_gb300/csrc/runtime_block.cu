@@ -144,6 +144,7 @@ static gf::NormParams norm_params(const gf_plan* p) {
   n.sms = p->num_sms;
   n.status = p->d_status;
   n.wait_limit_ns = p->wait_limit_ns;
+  n.drop_load = p->drop_load;
   return n;
 }
 

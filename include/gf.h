@@ -222,7 +222,10 @@ GF_API gf_status gf_dswiglu_execute(const gf_plan* plan, const void* dout, const
  * if z_out asks for it).
  *
  * m, n, k, dtype, b_layout: as gf_matmul_plan_ex. Options: as its plans, and
- * GF_OPT_KERNEL 4, the kernel for few rows; gf_matmul_autotune does not take it.
+ * GF_OPT_KERNEL 4, the kernel for few rows (tiles of 16, 32 or 64 rows and 128 columns; it
+ * reads B once and joins the parts of a tile's k in a cluster's shared memory: no
+ * workspace). It is the plan's choice up to 64 rows, and up to 128 where its tiles are
+ * few. gf_matmul_autotune does not take these plans.
  */
 typedef enum gf_activation {
   GF_ACT_NONE = 0, /* act(z) = z                                             */
@@ -272,7 +275,8 @@ GF_API gf_status gf_dact_bgrad_execute(const gf_plan* plan, const void* d_out, c
  * its range), rounded once.
  *
  * rows >= 0, 1 <= hidden <= 32768 (more: GF_ERR_UNSUPPORTED), eps >= 0 and finite.
- * Options: GF_OPT_PDL.
+ * Options: GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US, GF_OPT_FAULT_DROP_LOAD. gf_plan_status
+ * reports a copy that never came (GF_ERR_DEVICE_TIMEOUT).
  */
 GF_API gf_plan* gf_rmsnorm_plan(int64_t rows, int64_t hidden, gf_dtype dtype, float eps);
 
@@ -537,7 +541,10 @@ GF_API gf_status gf_plan_status(const gf_plan* plan, struct CUstream_st* stream)
  *                          taking a column of both weights: 3/4 of the
  *                          operand traffic per flop, one accumulator whose
  *                          halves are released as soon as the epilogue has
- *                          them in registers).
+ *                          them in registers). Plans of
+ *                          gf_matmul_residual_plan: 4 the kernel for few
+ *                          rows, which of the options below takes
+ *                          GF_OPT_SPLIT_K and GF_OPT_PDL alone.
  * Returns GF_ERR_INVALID_VALUE for an unknown option or value.
  */
 typedef enum gf_option {
@@ -587,7 +594,9 @@ typedef enum gf_option {
  * take more than 256 MB). The workspace grows to tiles x splits x 128 x tile_n
  * fp32 plus one counter per tile; GF_ERR_OUT_OF_MEMORY (and no split) when it
  * cannot be allocated. Set options only while no launch of the plan is in
- * flight. */
+ * flight. Plans of gf_matmul_residual_plan split as GF_EPILOG_NONE plans do; their kernel
+ * for few rows shares a tile among a cluster of up to 8 CTAs, by default as many as
+ * can be resident for all tiles at once. */
 /* GF_OPT_RASTER: the order of the output tiles. 1: raster groups of
  * GF_OPT_GROUP_M row blocks, column by column within a group (the group's
  * A panels stay in L2 while B streams through); 2: groups of GF_OPT_GROUP_M
@@ -635,7 +644,9 @@ GF_API gf_status gf_plan_k_splits(const gf_plan* plan, int32_t* k_splits);
 /* The number of kernels one execute of the plan enqueues in its current
  * configuration: 0 for an empty output, else 1, plus 1 for the bias-gradient
  * epilogs in GF_BGRAD_TWO_PASS mode (the finalize kernel that adds the
- * partials; GF_BGRAD_ATOMIC enqueues a memset of bgrad instead).
+ * partials; GF_BGRAD_ATOMIC enqueues a memset of bgrad instead). For a plan of
+ * gf_route_plan or gf_rmsnorm_plan 1 (a gradient of the norm's weight adds one), of
+ * gf_dact_bgrad_plan 2 (without bgrad 1).
  * GF_ERR_INVALID_VALUE for a NULL argument. */
 GF_API gf_status gf_plan_launches(const gf_plan* plan, int32_t* launches);
 

@@ -213,6 +213,25 @@ def test_backward_against_differences():
     plan.free()
 
 
+def test_times_out_and_recovers():
+    """A copy that is never asked for: the waits run out, the status says so, and the plan works again."""
+    rows, hidden = 4000, 1024
+    x, res, w = inputs(rows, hidden, gf.GF_BF16)
+    plan = gf.gf_rmsnorm_plan(rows, hidden, gf.GF_BF16, EPS)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_WAIT_LIMIT_US, 20000)
+    gf.gf_plan_set_option(plan, gf.GF_OPT_FAULT_DROP_LOAD, 2)
+    out, d_w = torch.empty_like(x), torch.empty(hidden, device="cuda")
+    for call in (lambda: gf.gf_rmsnorm_execute(plan, x, w, residual=res, out=out), lambda: gf.gf_rmsnorm_grad_execute(plan, res, x, w, out, d_weight=d_w)):
+        call()
+        assert gf.gf_plan_status(plan) == gf.GF_ERR_DEVICE_TIMEOUT
+        assert gf.gf_plan_status(plan) == gf.GF_OK
+    gf.gf_plan_set_option(plan, gf.GF_OPT_FAULT_DROP_LOAD, 0)
+    gf.gf_rmsnorm_execute(plan, x, w, out=out)
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    near(out, exact(x, w)[0], gf.GF_BF16)
+    plan.free()
+
+
 def test_no_rows():
     plan = gf.gf_rmsnorm_plan(0, 64, gf.GF_BF16)
     none = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
