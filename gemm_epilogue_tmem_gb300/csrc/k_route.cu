@@ -15,9 +15,10 @@
 // Experts are whole numbers, and scores may lie closer together than fp32, less the
 // bits of the place, tells them apart. The comparisons that decide something are
 // therefore looked at again: where two differ by no more than their error bounds, and
-// not for equal inputs, those in question are compared in two fp32, and where that leaves it open in 64
-// bits (a few in a thousand tokens of 256 experts with a bias, and hardly any). Without a bias experts are compared by their
-// logits; those of 16 bits leave the place's bits free and are exact at once.
+// not for equal inputs, those in question are compared in two fp32, and where that
+// leaves it open in 64 bits (a few in a thousand tokens of 256 experts with a bias, and
+// hardly any). Without a bias experts are compared by their logits; those of 16 bits
+// leave the place's bits free and are exact at once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -434,7 +435,7 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, const L* row, 
   for (int i = 0; i < VPL; ++i) l[i] = i < count ? as_float(row[first + i]) : -INFINITY;
 }
 
-// CTAs of an SM (the grid is as large: warps loop over the tokens)
+// CTAs of an SM (a warp a token: the grid is as large, warps loop over the tokens)
 constexpr int resident(int vpl) { return vpl <= 8 ? 6 : vpl <= 16 ? 5 : 2; }
 
 // over the W lanes of a token
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(VPL))
     __syncwarp();
     // the next token's logits come meanwhile
     const int64_t next = token + step;
-    const bool valid = token < p.tokens, more = next - part < p.tokens;
+    const bool valid = token < p.tokens, more = W == 32 && next < p.tokens;
     if (more) {
       count = next < p.tokens ? experts_here : 0;
       load_logits<L, VPL>(p, row + step * p.ld, base, count, l);
@@ -765,7 +766,8 @@ __device__ __forceinline__ float to_logit<float>(float v) { return v; }
 
 // All but softmax without renormalisation, where only the chosen experts have a
 // gradient: eight lanes a token, the row put together in shared memory in the logits' type
-// and written 16 bytes at a time. S: slots a lane.
+// and written 16 bytes at a time (16384 tokens of 128 experts 3.6 us; CTAs that loop 5.1).
+// S: slots a lane.
 template <typename L, int S>
 __global__ void __launch_bounds__(32 * kWarps)
     route_grad_sparse_kernel(const __grid_constant__ RouteParams p) {
@@ -775,113 +777,109 @@ __global__ void __launch_bounds__(32 * kWarps)
   grid_dep_launch();
   const int lane = threadIdx.x & (W - 1), words = static_cast<int>(p.ld) / kPer;
   uint4* mine = reinterpret_cast<uint4*>(grad_rows) + (threadIdx.x / W) * words;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kWarps / W);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (32 * kWarps / W) + threadIdx.x / W;
-  for (int64_t token = first; token - threadIdx.x / W < p.tokens; token += step) {
-    const bool valid = token < p.tokens;
-    const L* row = static_cast<const L*>(p.logits) + token * p.ld;
-    // softmax: a logit that is no number, or infinite, and the largest of all
-    float of_all = -INFINITY;
-    bool number = true;
-    if (!p.sigmoid && valid) {
-      for (int w = lane; w * kPer < p.experts; w += W) {
-        const uint4 v = reinterpret_cast<const uint4*>(row)[w];
-        const L* e = reinterpret_cast<const L*>(&v);
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * (32 * kWarps / W) + threadIdx.x / W;
+  const bool valid = token < p.tokens;
+  const L* row = static_cast<const L*>(p.logits) + token * p.ld;
+  // softmax: a logit that is no number, or infinite, and the largest of all
+  float of_all = -INFINITY;
+  bool number = true;
+  if (!p.sigmoid && valid) {
+    for (int w = lane; w * kPer < p.experts; w += W) {
+      const uint4 v = reinterpret_cast<const uint4*>(row)[w];
+      const L* e = reinterpret_cast<const L*>(&v);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const float x = w * kPer + j < p.experts ? as_float(e[j]) : -INFINITY;
-          of_all = fmaxf(of_all, x);
-          number = number && x < INFINITY;
-        }
+      for (int j = 0; j < kPer; ++j) {
+        const float x = w * kPer + j < p.experts ? as_float(e[j]) : -INFINITY;
+        of_all = fmaxf(of_all, x);
+        number = number && x < INFINITY;
       }
     }
-    int expert[S];
-    float x[S], g[S], s[S], rest[S];
-    float of_chosen = -INFINITY;
+  }
+  int expert[S];
+  float x[S], g[S], s[S], rest[S];
+  float of_chosen = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int j = lane + W * i;
+    expert[i] = -1;
+    g[i] = s[i] = rest[i] = 0.f;
+    x[i] = -INFINITY;
+    if (valid && j < p.topk) {
+      const int e = p.expert[token * p.topk + j];
+      const float d = p.d_weight[token * p.topk + j];
+      if (e >= 0 && e < p.experts) {
+        expert[i] = e;
+        g[i] = d;
+        x[i] = as_float(row[e]);
+        of_chosen = fmaxf(of_chosen, x[i]);
+      }
+    }
+  }
+  float top = 0.f;
+  bool none = false;
+  if (!p.sigmoid) {
+    of_all = lanes_max<W>(of_all);
+    top = lanes_max<W>(of_chosen);
+    none = top - of_all < kNoScore;
+    if (top == -INFINITY) top = 0.f;
+    number = lanes_max<W>(number ? 0 : 1) == 0;
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    if (expert[i] >= 0) {
+      s[i] = p.sigmoid ? logistic(x[i]) : expf(x[i] - top);
+      rest[i] = p.sigmoid ? logistic(-x[i]) : 1.f;
+    }
+  }
+  float factor = p.scale, dot = 0.f;
+  if (p.renorm) {
+    const float sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
+    const float part = sum == 0.f || none ? 0.f : 1.f / sum;
+    dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]) * part;
+    factor = p.scale * part;
+  }
+  const L fill = to_logit<L>(number ? 0.f : NAN);  // where nothing was chosen
+  uint4 fills;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) reinterpret_cast<L*>(&fills)[j] = fill;
+  for (int w = lane; w < words; w += W) {
+    uint4 v = fills;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (w * kPer + j >= p.experts) reinterpret_cast<L*>(&v)[j] = to_logit<L>(0.f);
+    mine[w] = v;
+  }
+  __syncwarp();
+  // an expert's slots in order, by the first of them
+  float v[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) v[i] = factor * s[i] * rest[i] * (g[i] - dot);
+  float total[S];
+  bool writes[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    total[i] = 0.f;
+    writes[i] = expert[i] >= 0;
+  }
+  for (int j = 0; j < p.topk; ++j) {
+    const int from = j & (W - 1);
+    const int e = __shfl_sync(kAll, S == 2 && j >= W ? expert[S - 1] : expert[0], from, W);
+    const float add = __shfl_sync(kAll, S == 2 && j >= W ? v[S - 1] : v[0], from, W);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int j = lane + W * i;
-      expert[i] = -1;
-      g[i] = s[i] = rest[i] = 0.f;
-      x[i] = -INFINITY;
-      if (valid && j < p.topk) {
-        const int e = p.expert[token * p.topk + j];
-        const float d = p.d_weight[token * p.topk + j];
-        if (e >= 0 && e < p.experts) {
-          expert[i] = e;
-          g[i] = d;
-          x[i] = as_float(row[e]);
-          of_chosen = fmaxf(of_chosen, x[i]);
-        }
+      if (e == expert[i]) {
+        total[i] += add;
+        if (j < lane + W * i) writes[i] = false;
       }
     }
-    float top = 0.f;
-    bool none = false;
-    if (!p.sigmoid) {
-      of_all = lanes_max<W>(of_all);
-      top = lanes_max<W>(of_chosen);
-      none = top - of_all < kNoScore;
-      if (top == -INFINITY) top = 0.f;
-      number = lanes_max<W>(number ? 0 : 1) == 0;
-    }
+  }
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      if (expert[i] >= 0) {
-        s[i] = p.sigmoid ? logistic(x[i]) : expf(x[i] - top);
-        rest[i] = p.sigmoid ? logistic(-x[i]) : 1.f;
-      }
-    }
-    float factor = p.scale, dot = 0.f;
-    if (p.renorm) {
-      const float sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
-      const float part = sum == 0.f || none ? 0.f : 1.f / sum;
-      dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]) * part;
-      factor = p.scale * part;
-    }
-    const L fill = to_logit<L>(number ? 0.f : NAN);  // where nothing was chosen
-    uint4 fills;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) reinterpret_cast<L*>(&fills)[j] = fill;
-    for (int w = lane; w < words; w += W) {
-      uint4 v = fills;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (w * kPer + j >= p.experts) reinterpret_cast<L*>(&v)[j] = to_logit<L>(0.f);
-      mine[w] = v;
-    }
-    __syncwarp();
-    // an expert's slots in order, by the first of them
-    float v[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) v[i] = factor * s[i] * rest[i] * (g[i] - dot);
-    float total[S];
-    bool writes[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      total[i] = 0.f;
-      writes[i] = expert[i] >= 0;
-    }
-    for (int j = 0; j < p.topk; ++j) {
-      const int from = j & (W - 1);
-      const int e = __shfl_sync(kAll, S == 2 && j >= W ? expert[S - 1] : expert[0], from, W);
-      const float add = __shfl_sync(kAll, S == 2 && j >= W ? v[S - 1] : v[0], from, W);
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        if (e == expert[i]) {
-          total[i] += add;
-          if (j < lane + W * i) writes[i] = false;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (writes[i]) reinterpret_cast<L*>(mine)[expert[i]] = to_logit<L>(number ? total[i] : NAN);
-    __syncwarp();
-    if (valid) {
-      uint4* out = reinterpret_cast<uint4*>(static_cast<L*>(p.d_logits) + token * p.ld);
-      for (int w = lane; w < words; w += W) out[w] = mine[w];
-    }
-    __syncwarp();
+  for (int i = 0; i < S; ++i)
+    if (writes[i]) reinterpret_cast<L*>(mine)[expert[i]] = to_logit<L>(number ? total[i] : NAN);
+  __syncwarp();
+  if (valid) {
+    uint4* out = reinterpret_cast<uint4*>(static_cast<L*>(p.d_logits) + token * p.ld);
+    for (int w = lane; w < words; w += W) out[w] = mine[w];
   }
 }
 
@@ -987,11 +985,15 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
 
 template <typename L, int W, int VPL>
 cudaError_t route_of(const RouteParams& p, cudaStream_t stream, int pdl) {
-  // as many CTAs as are resident at once; more tokens follow in their loop
+  // A warp a token: as many CTAs as are resident at once, more tokens follow in their loop,
+  // each loaded ahead (16384 tokens, 256 experts in groups with a bias 23.4 us; a CTA for
+  // every four tokens 26.1). Four tokens a warp: a CTA for every 16, as the loop's last
+  // turn would leave many idle (128 experts, 16384 / 65536 tokens 7.1 / 16.1 us; in a
+  // loop 9.3 / 25.1).
   constexpr int kTokens = kWarps * (32 / W);
   const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
   const int64_t most = static_cast<int64_t>(p.sms) * resident(VPL);
-  const dim3 grid(static_cast<unsigned>(all < most ? all : most)), block(32 * kWarps);
+  const dim3 grid(static_cast<unsigned>(W < 32 || all < most ? all : most)), block(32 * kWarps);
   if constexpr (W == 32) {
     if (p.bias != nullptr)
       return launch_pdl(route_kernel<L, W, VPL, true>, grid, block, 0, stream, pdl, p);
@@ -1043,8 +1045,7 @@ cudaError_t route_grad(const RouteParams& p, cudaStream_t stream, int pdl) {
   if ((p.sigmoid || p.renorm) && p.topk <= 16 && row_bytes % 16 == 0 && row_bytes <= 2048) {
     constexpr int kTokens = 32 * kWarps / 8;
     const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
-    const int64_t most = static_cast<int64_t>(p.sms) * 6;
-    const dim3 grid(static_cast<unsigned>(all < most ? all : most)), block(32 * kWarps);
+    const dim3 grid(static_cast<unsigned>(all)), block(32 * kWarps);
     return p.topk <= 8
                ? launch_pdl(route_grad_sparse_kernel<L, 1>, grid, block, kTokens * row_bytes, stream, pdl, p)
                : launch_pdl(route_grad_sparse_kernel<L, 2>, grid, block, kTokens * row_bytes, stream, pdl, p);
