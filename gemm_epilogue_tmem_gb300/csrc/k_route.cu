@@ -435,8 +435,13 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, const L* row, 
   for (int i = 0; i < VPL; ++i) l[i] = i < count ? as_float(row[first + i]) : -INFINITY;
 }
 
-// CTAs of an SM (a warp a token: the grid is as large, warps loop over the tokens)
-constexpr int resident(int vpl) { return vpl <= 8 ? 6 : vpl <= 16 ? 5 : 2; }
+// CTAs of an SM (a warp a token: the grid is as large, warps loop over the tokens). With a
+// warp a token fewer registers cost more than more warps gain: 60000 tokens, 256 experts
+// in groups with a bias 66 us with 4, 75 with 6, 79 with 3; 128 experts in fp32 41 with 8,
+// 48 with 6; 16384 tokens of 512 29.5 with 4, 31.5 with 3, 36 with 6.
+constexpr int resident(int w, int vpl) {
+  return w < 32 ? (vpl <= 8 ? 6 : 5) : vpl <= 4 ? 8 : vpl <= 16 ? 4 : 2;
+}
 
 // over the W lanes of a token
 template <int W>
@@ -465,7 +470,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // W lanes a token, VPL experts a lane. BIAS: scores are compared, else logits. Eight lanes
 // a token: 16-bit logits that are compared as they are, of which nothing is ever in doubt.
 template <typename L, int W, int VPL, bool BIAS>
-__global__ void __launch_bounds__(32 * kWarps, resident(VPL))
+__global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
     route_kernel(const __grid_constant__ RouteParams p) {
   constexpr int MASK = VPL - 1;
   constexpr int T = 32 / W;  // tokens of a warp
@@ -986,13 +991,13 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
 template <typename L, int W, int VPL>
 cudaError_t route_of(const RouteParams& p, cudaStream_t stream, int pdl) {
   // A warp a token: as many CTAs as are resident at once, more tokens follow in their loop,
-  // each loaded ahead (16384 tokens, 256 experts in groups with a bias 23.4 us; a CTA for
-  // every four tokens 26.1). Four tokens a warp: a CTA for every 16, as the loop's last
+  // each loaded ahead (16384 tokens, 256 experts in groups with a bias, with six CTAs an
+  // SM: 23.4 us; a CTA for every four tokens 26.1). Four tokens a warp: a CTA for every 16, as the loop's last
   // turn would leave many idle (128 experts, 16384 / 65536 tokens 7.1 / 16.1 us; in a
   // loop 9.3 / 25.1).
   constexpr int kTokens = kWarps * (32 / W);
   const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
-  const int64_t most = static_cast<int64_t>(p.sms) * resident(VPL);
+  const int64_t most = static_cast<int64_t>(p.sms) * resident(W, VPL);
   const dim3 grid(static_cast<unsigned>(W < 32 || all < most ? all : most)), block(32 * kWarps);
   if constexpr (W == 32) {
     if (p.bias != nullptr)
