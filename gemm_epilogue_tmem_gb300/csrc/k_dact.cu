@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256, kPerSm) dact_kernel(const DactParams p) {
 
 template <typename T>
 cudaError_t dact(const DactParams& p, int chunks, cudaStream_t stream, int pdl) {
-  const dim3 grid((p.cols + 255) / 256, chunks), block(256);
+  const dim3 grid((static_cast<unsigned>(p.cols) + 255) / 256, chunks), block(256);
   switch (p.act) {
     case kActNone: return launch_pdl(dact_kernel<T, kActNone>, grid, block, 0, stream, pdl, p);
     case kActRelu: return launch_pdl(dact_kernel<T, kActRelu>, grid, block, 0, stream, pdl, p);

@@ -321,7 +321,8 @@ Shape norm_shape(int64_t hidden) {
 template <typename T, bool ALIGNED, bool FP8>
 cudaError_t forward(const NormParams& p, cudaStream_t stream, int pdl) {
   const Shape s = norm_shape(p.hidden);
-  const dim3 grid((p.rows + s.rows - 1) / s.rows), block(s.threads, s.rows);
+  const int64_t ctas = (static_cast<int64_t>(p.rows) + s.rows - 1) / s.rows;
+  const dim3 grid(static_cast<unsigned>(ctas)), block(s.threads, s.rows);
   switch (s.v) {
     case 1: return launch_pdl(norm_kernel<T, 1, ALIGNED, FP8>, grid, block, 0, stream, pdl, p);
     case 2: return launch_pdl(norm_kernel<T, 2, ALIGNED, FP8>, grid, block, 0, stream, pdl, p);
@@ -419,7 +420,7 @@ cudaError_t launch_norm_grad(const NormParams& p, int bf16, int ctas, cudaStream
 
 cudaError_t launch_column_sums(const float* partials, int rows, int cols, float* out,
                                cudaStream_t stream, int pdl) {
-  return launch_pdl(column_sums_kernel, dim3((cols + 31) / 32), dim3(32 * kSlices), 0, stream, pdl,
+  return launch_pdl(column_sums_kernel, dim3((static_cast<unsigned>(cols) + 31) / 32), dim3(32 * kSlices), 0, stream, pdl,
                     partials, rows, cols, out);
 }
 

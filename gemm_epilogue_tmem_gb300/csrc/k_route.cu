@@ -1055,7 +1055,7 @@ cudaError_t route_grad(const RouteParams& p, cudaStream_t stream, int pdl) {
                ? launch_pdl(route_grad_sparse_kernel<L, 1>, grid, block, kTokens * row_bytes, stream, pdl, p)
                : launch_pdl(route_grad_sparse_kernel<L, 2>, grid, block, kTokens * row_bytes, stream, pdl, p);
   }
-  const dim3 grid((p.tokens + kWarps - 1) / kWarps), block(32 * kWarps);
+  const dim3 grid((static_cast<unsigned>(p.tokens) + kWarps - 1) / kWarps), block(32 * kWarps);
   return launch_pdl(route_grad_kernel<L>, grid, block,
                     static_cast<size_t>(kWarps) * p.experts * 4, stream, pdl, p);
 }
