@@ -405,8 +405,9 @@ bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, bool pairs, int
   s->threads = (words + s->v * 32 - 1) / (s->v * 32) * 32;
   s->rows = s->threads >= 192 ? 1 : 256 / s->threads;
   const size_t stage = static_cast<size_t>(s->rows) * words * 16 * arrays;
-  // (16384 x 5120 to e4m3, two CTAs an SM 94 us, three 104; 16384 x 4096 backward 90 and 85)
-  int per_sm = s->v == 2 && s->threads <= 320 && !pairs ? 3 : stream_per_sm(s->v);
+  // (two CTAs an SM and three: 16384 x 5120 to e4m3 with a residual 94 and 104 us, without
+  // one 77 and 75, 16384 x 4096 81 and 59; backward 90 and 85)
+  int per_sm = s->v == 2 && s->threads <= 320 && (!pairs || arrays == 1) ? 3 : stream_per_sm(s->v);
   while (per_sm > 1 && per_sm * 2 * stage > kStreamSmem) --per_sm;
   s->stages = static_cast<int>(kStreamSmem / per_sm / stage);
   if (s->stages > kMaxStages) s->stages = kMaxStages;

@@ -836,12 +836,13 @@ __global__ void __launch_bounds__(32 * kWarps)
       rest[i] = p.sigmoid ? logistic(-x[i]) : 1.f;
     }
   }
-  float factor = p.scale, dot = 0.f;
+  float dot = 0.f;
   if (p.renorm) {
+    // (divided before they are summed: an expert alone has 1, and no gradient)
     const float sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
-    const float part = sum == 0.f || none ? 0.f : 1.f / sum;
-    dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]) * part;
-    factor = p.scale * part;
+#pragma unroll
+    for (int i = 0; i < S; ++i) s[i] = sum == 0.f || none ? 0.f : s[i] / sum;
+    dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]);
   }
   const L fill = to_logit<L>(number ? 0.f : NAN);  // where nothing was chosen
   uint4 fills;
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   // an expert's slots in order, by the first of them
   float v[S];
 #pragma unroll
-  for (int i = 0; i < S; ++i) v[i] = factor * s[i] * rest[i] * (g[i] - dot);
+  for (int i = 0; i < S; ++i) v[i] = p.scale * s[i] * rest[i] * (g[i] - dot);
   float total[S];
   bool writes[S];
 #pragma unroll
@@ -951,12 +952,13 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
       }
     }
   }
-  float factor = p.scale, dot = 0.f;
+  float dot = 0.f;
   if (p.renorm) {
+    // (divided before they are summed: an expert alone has 1, and no gradient)
     const float sum = warp_sum(s[0] + s[1]);
-    const float part = sum == 0.f || none ? 0.f : 1.f / sum;
-    dot = warp_sum(g[0] * s[0] + g[1] * s[1]) * part;
-    factor = p.scale * part;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s[i] = sum == 0.f || none ? 0.f : s[i] / sum;
+    dot = warp_sum(g[0] * s[0] + g[1] * s[1]);
   } else if (all) {
     dot = warp_sum(g[0] * s[0] + g[1] * s[1]);
     __syncwarp();
@@ -967,7 +969,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
   // the slots' own terms; the same expert may be there twice: slot after slot, then
   float v[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) v[i] = factor * s[i] * rest[i] * (g[i] - dot);
+  for (int i = 0; i < 2; ++i) v[i] = p.scale * s[i] * rest[i] * (g[i] - dot);
   bool twice = false;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

@@ -180,3 +180,20 @@ def test_refusals():
         with pytest.raises(gf.GfError):
             bad()
     plan.free()
+
+
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("pad", [0, 1])  # rows of whole 16-byte words or not
+@pytest.mark.parametrize("topk", [1, 3])
+def test_an_expert_alone_has_no_gradient(score, pad, topk):
+    """Renormalised, the weight of a token's only expert is the scale whatever its logit is."""
+    tokens, experts = 5000, 16
+    logits = logits_of(tokens, experts + pad, 5, gf.GF_F32)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    expert = torch.full((tokens, topk), -1, dtype=torch.int32, device="cuda")
+    expert[:, topk // 2] = torch.randint(experts, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    d_weight, d_logits = torch.randn(tokens, topk, generator=g, device="cuda"), torch.empty_like(logits)
+    plan = gf.gf_route_plan(tokens, experts, topk, gf.GF_F32, score, True, 2.5, 1, 1, 1, experts + pad)
+    gf.gf_route_grad_execute(plan, logits, expert, d_weight, d_logits)
+    assert torch.count_nonzero(d_logits) == 0
+    plan.free()
