@@ -180,7 +180,12 @@ __global__ void __launch_bounds__(stream_threads(V), stream_per_sm(V))
     if (ring.leader() && group != blockIdx.x)
       ring.issue(p, stage == 0 ? ring.stages - 1 : stage - 1,
                  group + static_cast<int64_t>(ring.stages - 1) * gridDim.x);
-    const float rstd = rsqrtf(fmaf(s.hi, inv_n, p.eps));
+    const float var = fmaf(s.hi, inv_n, p.eps);
+    float rstd = rsqrtf(var);
+    if constexpr (FP8) {  // one step of Newton's method: an error moves values over e4m3's borders
+      const float e = fmaf(-var * rstd, rstd, 1.f);
+      if (fabsf(e) < 1e-3f) rstd = fmaf(0.5f * rstd, e, rstd);  // (not of 0 or infinity)
+    }
     if constexpr (!FP8) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
