@@ -2,7 +2,7 @@
 // tile is 128 columns times TR rows, with B on the tensor core's 128-row side (D =
 // B^T A^T), so that few rows cost no more tensor work than they need and a CTA streams
 // one operand, B, from HBM, whose rate bounds the product (one row, 5120 columns, k =
-// 17408: 30.9 us, 5.8 TB/s; by the single-CTA kernel 47).
+// 17408: 29.8 us, 6.0 TB/s; by the single-CTA kernel 47).
 //
 // Tiles that leave SMs idle are shared by a cluster of CTAs, each with a run of their
 // k-blocks: each CTA puts its fp32 partial sums into its shared memory (the idle ring),

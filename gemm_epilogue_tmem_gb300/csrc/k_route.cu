@@ -10,7 +10,9 @@
 // last bits are the place within the lane, so that a lane sorts its experts by
 // minimum and maximum alone, a pick is one warp-wide integer maximum and the lowest
 // lane that has it, and the lane that loses its best moves up the others. What bounds
-// it is instructions (some 400 a token of 256 experts) and, for a token, latency.
+// it is instructions (some 950 a token of 256 experts in groups with a bias: 16384 tokens
+// 21 us; eight lanes a token, 128 experts of 16-bit logits: 250 and 7.1 us) and, for a
+// token, latency (3 us).
 //
 // Experts are whole numbers, and scores may lie closer together than fp32, less the
 // bits of the place, tells them apart. The comparisons that decide something are
