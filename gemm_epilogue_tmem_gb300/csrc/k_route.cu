@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 #include <limits.h>
 #include <math.h>
+#include <string.h>
 
 #include <type_traits>
 
@@ -773,17 +774,17 @@ __device__ __forceinline__ float to_logit<float>(float v) { return v; }
 
 // All but softmax without renormalisation, where only the chosen experts have a
 // gradient: eight lanes a token, the row put together in shared memory in the logits' type
-// and written 16 bytes at a time (16384 tokens of 128 experts 3.6 us; CTAs that loop 5.1).
-// S: slots a lane.
-template <typename L, int S>
+// and written a word at a time, of 16 bytes or what divides a row's (16384 tokens of 128
+// experts 3.5 us; CTAs that loop 5.1). S: slots a lane.
+template <typename L, int S, typename Word>
 __global__ void __launch_bounds__(32 * kWarps)
     route_grad_sparse_kernel(const __grid_constant__ RouteParams p) {
-  constexpr int W = 8, kPer = 16 / static_cast<int>(sizeof(L));  // elements of a word
-  extern __shared__ __align__(16) uint8_t grad_rows[];           // [tokens of the CTA][ld]
+  constexpr int W = 8, kPer = static_cast<int>(sizeof(Word) / sizeof(L));  // elements of a word
+  extern __shared__ __align__(16) uint8_t grad_rows[];  // [tokens of the CTA][ld]
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & (W - 1), words = static_cast<int>(p.ld) / kPer;
-  uint4* mine = reinterpret_cast<uint4*>(grad_rows) + (threadIdx.x / W) * words;
+  Word* mine = reinterpret_cast<Word*>(grad_rows) + (threadIdx.x / W) * words;
   const int64_t token = static_cast<int64_t>(blockIdx.x) * (32 * kWarps / W) + threadIdx.x / W;
   const bool valid = token < p.tokens;
   const L* row = static_cast<const L*>(p.logits) + token * p.ld;
@@ -792,8 +793,9 @@ __global__ void __launch_bounds__(32 * kWarps)
   bool number = true;
   if (!p.sigmoid && valid) {
     for (int w = lane; w * kPer < p.experts; w += W) {
-      const uint4 v = reinterpret_cast<const uint4*>(row)[w];
-      const L* e = reinterpret_cast<const L*>(&v);
+      const Word v = reinterpret_cast<const Word*>(row)[w];
+      L e[kPer];
+      memcpy(e, &v, sizeof(Word));
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const float x = w * kPer + j < p.experts ? as_float(e[j]) : -INFINITY;
@@ -847,14 +849,12 @@ __global__ void __launch_bounds__(32 * kWarps)
     dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]);
   }
   const L fill = to_logit<L>(number ? 0.f : NAN);  // where nothing was chosen
-  uint4 fills;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) reinterpret_cast<L*>(&fills)[j] = fill;
   for (int w = lane; w < words; w += W) {
-    uint4 v = fills;
+    L e[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (w * kPer + j >= p.experts) reinterpret_cast<L*>(&v)[j] = to_logit<L>(0.f);
+    for (int j = 0; j < kPer; ++j) e[j] = w * kPer + j < p.experts ? fill : to_logit<L>(0.f);
+    Word v;
+    memcpy(&v, e, sizeof(Word));
     mine[w] = v;
   }
   __syncwarp();
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (writes[i]) reinterpret_cast<L*>(mine)[expert[i]] = to_logit<L>(number ? total[i] : NAN);
   __syncwarp();
   if (valid) {
-    uint4* out = reinterpret_cast<uint4*>(static_cast<L*>(p.d_logits) + token * p.ld);
+    Word* out = reinterpret_cast<Word*>(static_cast<L*>(p.d_logits) + token * p.ld);
     for (int w = lane; w < words; w += W) out[w] = mine[w];
   }
 }
@@ -1047,17 +1047,25 @@ cudaError_t route(const RouteParams& args, cudaStream_t stream, int pdl) {
   return route_of<L, 32, 64>(p, stream, pdl);
 }
 
+template <typename L, typename Word>
+cudaError_t route_grad_sparse(const RouteParams& p, size_t row_bytes, cudaStream_t stream, int pdl) {
+  constexpr int kTokens = 32 * kWarps / 8;
+  const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
+  const dim3 grid(static_cast<unsigned>(all)), block(32 * kWarps);
+  return p.topk <= 8 ? launch_pdl(route_grad_sparse_kernel<L, 1, Word>, grid, block,
+                                  kTokens * row_bytes, stream, pdl, p)
+                     : launch_pdl(route_grad_sparse_kernel<L, 2, Word>, grid, block,
+                                  kTokens * row_bytes, stream, pdl, p);
+}
+
 template <typename L>
 cudaError_t route_grad(const RouteParams& p, cudaStream_t stream, int pdl) {
   // rows of whole words, up to 2 KB
   const size_t row_bytes = static_cast<size_t>(p.ld) * sizeof(L);
-  if ((p.sigmoid || p.renorm) && p.topk <= 16 && row_bytes % 16 == 0 && row_bytes <= 2048) {
-    constexpr int kTokens = 32 * kWarps / 8;
-    const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
-    const dim3 grid(static_cast<unsigned>(all)), block(32 * kWarps);
-    return p.topk <= 8
-               ? launch_pdl(route_grad_sparse_kernel<L, 1>, grid, block, kTokens * row_bytes, stream, pdl, p)
-               : launch_pdl(route_grad_sparse_kernel<L, 2>, grid, block, kTokens * row_bytes, stream, pdl, p);
+  if ((p.sigmoid || p.renorm) && p.topk <= 16 && row_bytes % 4 == 0 && row_bytes <= 2048) {
+    if (row_bytes % 16 == 0) return route_grad_sparse<L, uint4>(p, row_bytes, stream, pdl);
+    if (row_bytes % 8 == 0) return route_grad_sparse<L, uint2>(p, row_bytes, stream, pdl);
+    return route_grad_sparse<L, uint32_t>(p, row_bytes, stream, pdl);
   }
   const dim3 grid((static_cast<unsigned>(p.tokens) + kWarps - 1) / kWarps), block(32 * kWarps);
   return launch_pdl(route_grad_kernel<L>, grid, block,

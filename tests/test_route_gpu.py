@@ -197,3 +197,11 @@ def test_an_expert_alone_has_no_gradient(score, pad, topk):
     gf.gf_route_grad_execute(plan, logits, expert, d_weight, d_logits)
     assert torch.count_nonzero(d_logits) == 0
     plan.free()
+
+
+# rows of words of 8, 4 and 2 bytes, with and without columns behind the experts
+@pytest.mark.parametrize("tokens,experts,topk,pad", [(1001, 60, 6, 0), (999, 54, 8, 0), (500, 61, 9, 0), (333, 62, 16, 4), (77, 6, 3, 0), (18, 2, 1, 0),
+                                                     (40, 505, 8, 3)])
+@pytest.mark.parametrize("dtype,score", [(gf.GF_F32, SIGMOID), (gf.GF_BF16, SOFTMAX), (gf.GF_F16, SIGMOID)])
+def test_gradient_of_ragged_rows(tokens, experts, topk, pad, dtype, score):
+    test_gradient(tokens, experts, topk, pad, dtype, score, True, 1.5)
