@@ -932,7 +932,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
       d[e] = expf(as_float(row[e]) - top);
       sum += d[e];
     }
-    inv = 1.f / warp_sum(sum);
+    sum = warp_sum(sum);
+    inv = sum == 0.f ? 0.f : 1.f / sum;  // (no logit above -inf: no scores)
   } else {
     for (int e = lane; e < p.experts; e += 32) d[e] = rest_of;
   }

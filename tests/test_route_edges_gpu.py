@@ -1,0 +1,71 @@
+"""The router and its gradient where a token's scores vanish, or its logits lie far from 0: against the definition in 64 bits."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import gemm_epilogue_tmem_gb300 as gf  # noqa: E402
+from route_reference import route, route_grad  # noqa: E402
+
+TDT = {gf.GF_F16: torch.float16, gf.GF_BF16: torch.bfloat16, gf.GF_F32: torch.float32}
+ROUND = {gf.GF_F16: (2.0 ** -11, 2.0 ** -25), gf.GF_BF16: (2.0 ** -8, 0.0), gf.GF_F32: (2.0 ** -24, 2.0 ** -149)}
+SOFTMAX, SIGMOID = gf.GF_SCORE_SOFTMAX, gf.GF_SCORE_SIGMOID
+NAN, INF = float("nan"), float("inf")
+
+
+def randn(*shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def choose(logits, experts, topk, dtype, score, renorm, scale, bias=None, groups=1, topk_groups=1, best=1):
+    tokens, ld = logits.shape
+    plan = gf.gf_route_plan(tokens, experts, topk, dtype, score, renorm, scale, groups, topk_groups, best, ld)
+    expert = torch.full((tokens, topk), 77, dtype=torch.int32, device="cuda")
+    weight = torch.full((tokens, topk), NAN, device="cuda")
+    gf.gf_route_execute(plan, logits, expert, weight, bias=bias)
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    plan.free()
+    return expert, weight
+
+
+def check_choice(logits, experts, topk, dtype, score, renorm, scale, bias=None, groups=1, topk_groups=1, best=1):
+    expert, weight = choose(logits, experts, topk, dtype, score, renorm, scale, bias, groups, topk_groups, best)
+    want, w = route(logits[:, :experts].double().cpu().numpy(), topk, score == SIGMOID, renorm, scale,
+                    None if bias is None else bias.double().cpu().numpy(), groups, topk_groups, best)
+    expert, weight = expert.cpu().numpy(), weight.double().cpu().numpy()
+    assert np.array_equal(expert, want), (np.argwhere(expert != want)[:4], expert[expert != want][:4], want[expert != want][:4])
+    # exponentials, at most 1024 terms in 32 sums, divisions
+    assert np.all((np.isnan(weight) & np.isnan(w)) | (np.abs(weight - w) <= 2.0 ** -18 * np.abs(w)))
+    return expert
+
+
+def check_grad(logits, experts, expert, d_weight, dtype, score, renorm, scale):
+    tokens, ld = logits.shape
+    plan = gf.gf_route_plan(tokens, experts, expert.shape[1], dtype, score, renorm, scale, ld=ld)
+    d = torch.full_like(logits, NAN)
+    gf.gf_route_grad_execute(plan, logits, torch.from_numpy(expert.astype(np.int32)).cuda(), torch.from_numpy(d_weight).cuda(), d)
+    assert gf.gf_plan_status(plan) == gf.GF_OK
+    plan.free()
+    want, size = route_grad(logits[:, :experts].double().cpu().numpy(), expert, d_weight.astype(np.float64), score == SIGMOID, renorm, scale)
+    got, (u, tiny) = d.double().cpu().numpy(), ROUND[dtype]
+    assert np.all(np.abs(got[:, :experts] - want) <= u * np.abs(want) + 2.0 ** -18 * size + tiny)
+    assert np.all(got[:, experts:] == 0)
+
+
+# rows of 16-byte words, of words of 4 bytes and of single elements; more slots than the kernel of eight lanes has
+@pytest.mark.parametrize("experts,topk,pad", [(32, 4, 0), (20, 20, 0), (30, 3, 0), (33, 5, 0), (64, 8, 3), (700, 8, 0)])
+@pytest.mark.parametrize("dtype", [gf.GF_F32, gf.GF_BF16])
+@pytest.mark.parametrize("score,renorm", [(SOFTMAX, True), (SOFTMAX, False), (SIGMOID, True), (SIGMOID, False)])
+def test_gradient_of_tokens_without_experts(experts, topk, pad, dtype, score, renorm):
+    """A token whose logits are all -inf has no gradient, with no slot filled and with masked experts in its slots."""
+    tokens = 37
+    logits = randn(tokens, experts + pad, seed=1).to(TDT[dtype])
+    logits[::3] = -INF
+    rng = np.random.default_rng(2)
+    expert = np.argsort(rng.random((tokens, experts)), 1)[:, :topk].astype(np.int32)
+    expert[0::6] = -1
+    check_grad(logits, experts, expert, rng.standard_normal((tokens, topk)).astype(np.float32), dtype, score, renorm, 1.5)
