@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
       const int j = lane + W * s;
       if (valid && j < p.topk) {
         p.expert[token * p.topk + j] = expert[s];
-        p.weight[token * p.topk + j] = w[s] * factor;
+        p.weight[token * p.topk + j] = expert[s] >= 0 ? w[s] * factor : 0.f;
       }
     }
     if (!more) return;

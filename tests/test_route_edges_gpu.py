@@ -69,3 +69,13 @@ def test_gradient_of_tokens_without_experts(experts, topk, pad, dtype, score, re
     expert = np.argsort(rng.random((tokens, experts)), 1)[:, :topk].astype(np.int32)
     expert[0::6] = -1
     check_grad(logits, experts, expert, rng.standard_normal((tokens, topk)).astype(np.float32), dtype, score, renorm, 1.5)
+
+
+@pytest.mark.parametrize("dtype,tokens", [(gf.GF_F32, 9), (gf.GF_BF16, 9), (gf.GF_F16, 2100)])
+@pytest.mark.parametrize("score,renorm", [(SOFTMAX, True), (SOFTMAX, False), (SIGMOID, True), (SIGMOID, False)])
+def test_slots_without_an_expert_beside_a_nan(dtype, tokens, score, renorm):
+    """The weights of the experts chosen are NaN, those of the slots that find none 0."""
+    experts, topk = 64, 8
+    logits = torch.full((tokens, experts), -INF, device="cuda", dtype=TDT[dtype])
+    logits[:, 11], logits[:, 30] = NAN, 0.5
+    check_choice(logits, experts, topk, dtype, score, renorm, 1.0)
