@@ -534,7 +534,8 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) sum += exp_fast(l[i] - top);
-        inv = 1.f / lanes_sum<W>(sum);
+        sum = lanes_sum<W>(sum);
+        inv = sum == 0.f ? 0.f : 1.f / sum;  // (no logit above -inf: no scores)
       }
     }
     // the error of fast_score: of the exponential (2^-22 of it and 2^-23 |x|), the sum
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
       }
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        key[i] = key_of<MASK>(c[i] + (l[i] == -INFINITY ? -INFINITY : bias[i]), i);
+        key[i] = key_of<MASK>(l[i] == -INFINITY ? -INFINITY : c[i] + bias[i], i);  // (c may be NaN)
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = key_of<MASK>(l[i], i);

@@ -79,3 +79,21 @@ def test_slots_without_an_expert_beside_a_nan(dtype, tokens, score, renorm):
     logits = torch.full((tokens, experts), -INF, device="cuda", dtype=TDT[dtype])
     logits[:, 11], logits[:, 30] = NAN, 0.5
     check_choice(logits, experts, topk, dtype, score, renorm, 1.0)
+
+
+# every expert is wanted: as many as lanes, fewer, groups that do not fill their lanes, two slots a lane
+@pytest.mark.parametrize("experts,groups,best", [(32, 1, 1), (20, 1, 1), (15, 5, 2), (12, 4, 1), (7, 7, 2), (33, 1, 1), (45, 3, 2), (60, 1, 1)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_masked_tokens_that_want_every_expert(experts, groups, best, score, renorm):
+    """Biases that are all equal leave nothing to compare but the masks: masked experts are left out, and those past the
+    last expert are not looked at."""
+    tokens = 70
+    logits = randn(tokens, experts, seed=3)
+    logits[::5] = -INF
+    logits[1::5, ::2] = -INF
+    logits[2::5] = NAN
+    logits[3::5, experts // 2] = NAN
+    logits[3::5, ::3] = -INF
+    logits[4::10, experts - 1] = INF
+    check_choice(logits, experts, experts, gf.GF_F32, score, renorm, 1.0, torch.zeros(experts, device="cuda"), groups, groups, best)
