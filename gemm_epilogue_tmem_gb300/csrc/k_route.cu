@@ -559,16 +559,31 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = key_of<MASK>(l[i], i);
     }
+    // the two largest logits with all their bits: e^l takes a cut of l, which may be far from
+    // 0, as a factor
+    int first = INT_MIN, second = INT_MIN;
+    if constexpr (!BIAS && !kExact) {
+      if (sums) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int k = ordered(__float_as_int(l[i] + 0.f));
+          second = max(second, min(first, k));
+          first = max(first, k);
+        }
+      }
+    }
     sort_keys<VPL>(key);
     bool out = false, unsure = false;  // this lane's group goes; the choice needs 64 bits
     if (grouped) {
       // the group's two best, over this lane's experts and then its lanes
       float a, b;
       if (!BIAS && sums) {  // sums are of scores, in which the experts are in the same order
-        a = fast_score(p, value_of<MASK>(key[0]), top, inv);
-        b = VPL > 1 ? fast_score(p, value_of<MASK>(key[VPL > 1 ? 1 : 0]), top, inv) : 0.f;
-        if (key[0] < kNone) a = -INFINITY;
-        if (VPL == 1 || key[VPL > 1 ? 1 : 0] < kNone) b = -INFINITY;
+        if constexpr (kExact) {
+          first = key[0] & ~MASK;
+          second = VPL > 1 ? key[VPL > 1 ? 1 : 0] & ~MASK : INT_MIN;
+        }
+        a = first < kNone ? -INFINITY : fast_score(p, __int_as_float(ordered(first)), top, inv);
+        b = second < kNone ? -INFINITY : fast_score(p, __int_as_float(ordered(second)), top, inv);
       } else {
         a = value_of<MASK>(key[0]);
         b = VPL > 1 ? value_of<MASK>(key[VPL > 1 ? 1 : 0]) : -INFINITY;

@@ -97,3 +97,20 @@ def test_masked_tokens_that_want_every_expert(experts, groups, best, score, reno
     logits[3::5, ::3] = -INF
     logits[4::10, experts - 1] = INF
     check_choice(logits, experts, experts, gf.GF_F32, score, renorm, 1.0, torch.zeros(experts, device="cuda"), groups, groups, best)
+
+
+@pytest.mark.parametrize("experts,groups,kept", [(1024, 8, 4), (1024, 4, 2), (512, 8, 3), (256, 8, 4), (60, 5, 2)])
+@pytest.mark.parametrize("offset", [-100.0, -50.0, 0.0, 50.0, 100.0, 1000.0])
+def test_groups_of_logits_far_from_zero(experts, groups, kept, offset):
+    """Softmax does not see what is added to all logits of a token; the groups' sums of two scores are compared as closely."""
+    tokens, topk = 200000, 8
+    logits = randn(tokens, experts, seed=int(offset) + 2000) + offset
+    expert, _ = choose(logits, experts, topk, gf.GF_F32, SOFTMAX, True, 1.0, None, groups, kept, 2)
+    for part in torch.arange(tokens, device="cuda").split(50000):
+        l = logits[part].double()
+        s = l.softmax(1).view(len(part), groups, -1)
+        order = s.topk(2, 2).values.sum(2).sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        stays = torch.zeros(len(part), groups, dtype=torch.bool, device="cuda").scatter_(1, order, True)
+        left = torch.where(stays.repeat_interleave(experts // groups, 1), l, -INF)
+        want = left.sort(dim=1, descending=True, stable=True).indices[:, :topk]
+        assert torch.equal(expert[part].long(), want), int((expert[part] != want).any(1).sum())
