@@ -91,6 +91,14 @@ __device__ __forceinline__ double logistic(double l) {
   return (l >= 0. ? 1. : e) / (1. + e);
 }
 
+// A chosen score over one factor of them all, where their sum divides it: softmax's is
+// e^(l - top) with the largest chosen logit, and so is, over 1 + e^l, sigmoid's where top is
+// negative, as e^l itself may have few bits in fp32, or none.
+__device__ __forceinline__ float part_of_chosen(const RouteParams& p, float l, float top) {
+  if (!p.sigmoid) return expf(l - top);
+  return top < 0.f ? expf(l - top) / (1.f + expf(l)) : logistic(l);
+}
+
 // a score as it is compared in fp32: e^x by the hardware exponential and the
 // hardware reciprocal, small results flushed
 __device__ __forceinline__ float exp_fast(float x) {
@@ -732,40 +740,38 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
     for (int s = 0; s < S; ++s)
       if (lane + W * s >= p.topk) expert[s] = -1;
 
-    // the weights; softmax over the chosen alone where they are renormalised, unless
-    // their scores are 0 in 64 bits too
+    // the weights; renormalised they are ratios of the chosen scores alone, unless these are 0
+    // in 64 bits too. (Divided, then scaled: scale over a small sum may be infinite.)
     float x[S], w[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) x[s] = expert[s] >= 0 ? as_float(row[expert[s]]) : -INFINITY;
-    bool none = false;
-    if (!p.sigmoid && p.renorm) {
-      const float of_all = top;
-      top = lanes_max<W>(fmaxf(x[0], x[S - 1]));
-      none = top - of_all < kNoScore;
-      if (top == -INFINITY) top = 0.f;
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      w[s] = 0.f;
-      if (expert[s] >= 0) {
-        w[s] = p.sigmoid ? logistic(x[s]) : expf(x[s] - top);
-        if (!p.sigmoid && !p.renorm) w[s] *= inv;
-      }
-    }
-    float factor = p.scale;
     if (p.renorm) {
-      const float sum = lanes_sum<W>(S == 2 ? w[0] + w[S - 1] : w[0]);
-      // (chosen scores that are all 0 stay 0)
-      factor = sum == 0.f || none ? 0.f : __fdividef(p.scale, sum);
-      // a logit without a number (or infinite) makes every score NaN, chosen or not
-      if (inv != inv) factor = inv;
+      const float chosen = lanes_max<W>(fmaxf(x[0], x[S - 1]));
+      const bool none = (p.sigmoid ? chosen : chosen - top) < kNoScore;
+      float sum = 0.f;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        w[s] = expert[s] >= 0 && !(none && x[s] == x[s]) ? part_of_chosen(p, x[s], chosen) : 0.f;
+        sum += w[s];
+      }
+      sum = lanes_sum<W>(sum);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        w[s] = sum == 0.f ? 0.f : w[s] / sum * p.scale;
+        // a logit without a number (or infinite) makes every score NaN, chosen or not
+        if (inv != inv) w[s] = inv;
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        w[s] = (p.sigmoid ? logistic(x[s]) : expf(x[s] - top) * inv) * p.scale;
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const int j = lane + W * s;
       if (valid && j < p.topk) {
         p.expert[token * p.topk + j] = expert[s];
-        p.weight[token * p.topk + j] = expert[s] >= 0 ? w[s] * factor : 0.f;
+        p.weight[token * p.topk + j] = expert[s] >= 0 ? w[s] : 0.f;
       }
     }
     if (!more) return;

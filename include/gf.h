@@ -324,9 +324,10 @@ GF_API gf_status gf_rmsnorm_grad_execute(const gf_plan* plan, const void* d_out,
  * Of equal ones the lowest index goes first, experts and groups. Slots that find no
  * expert left get -1 and weight 0 (gf_moe_dispatch drops them). NaN ranks above every
  * number, and is in the weights what the formulas make of it. Scores that fp32 does not tell
- * apart are compared in 64 bits. Chosen scores that sum to 0 have the weights 0 and
- * pass no gradient.
- * Logits and scores are fp32 whatever dtype is.
+ * apart are compared in 64 bits. Renormalised weights are the ratios of the scores, also
+ * where fp32 does not hold these; chosen scores that sum to 0 in 64 bits (logits of less than
+ * -745, under softmax below the largest) have the weights 0 and pass no gradient. Else
+ * logits and scores are fp32 whatever dtype is.
  *
  * tokens >= 0, 1 <= experts <= 1024, 1 <= topk <= 64, tokens * topk < 2^31, topk at most the
  * experts of topk_groups groups, groups a divisor of experts, else GF_ERR_INVALID_VALUE; at most 32

@@ -114,3 +114,29 @@ def test_groups_of_logits_far_from_zero(experts, groups, kept, offset):
         left = torch.where(stays.repeat_interleave(experts // groups, 1), l, -INF)
         want = left.sort(dim=1, descending=True, stable=True).indices[:, :topk]
         assert torch.equal(expert[part].long(), want), int((expert[part] != want).any(1).sum())
+
+
+LOW = [-80.0, -86.0, -87.5, -90.0, -100.0, -103.5, -104.0, -120.0, -300.0, -600.0, -800.0, -1e5]
+
+
+# a warp a token and eight lanes; an expert alone
+@pytest.mark.parametrize("tokens,dtype", [(60, gf.GF_F32), (60, gf.GF_BF16), (2100, gf.GF_F16)])
+@pytest.mark.parametrize("topk", [1, 8])
+@pytest.mark.parametrize("renorm,scale", [(True, 2.5), (True, 1e6), (False, 2.5)])
+def test_weights_of_low_sigmoid_scores(tokens, dtype, topk, renorm, scale):
+    """Renormalised weights are ratios of scores, also where fp32 holds few of the scores' bits or none: e^l / (1 + e^l) of
+    l down to -600, 0 in 64 bits from -745 on."""
+    experts = 64
+    base = torch.tensor(LOW, device="cuda").repeat(tokens // len(LOW) + 1)[:tokens, None]
+    logits = (base + randn(tokens, experts, seed=7)).to(TDT[dtype])
+    logits[:, 40] = base[:, 0].to(TDT[dtype]) - 40  # hardly any part in the sum
+    logits[11, 9] = NAN
+    if renorm:
+        check_choice(logits, experts, topk, dtype, SIGMOID, renorm, scale)
+    else:
+        # as they are, scores are fp32's: of subnormal ones a step is 2^-149
+        expert, weight = choose(logits, experts, topk, dtype, SIGMOID, renorm, scale)
+        want, w = route(logits.double().cpu().numpy(), topk, True, renorm, scale)
+        assert np.array_equal(expert.cpu().numpy(), want)
+        weight = weight.double().cpu().numpy()
+        assert np.all((np.isnan(weight) & np.isnan(w)) | (np.abs(weight - w) <= 2.0 ** -18 * w + 4 * scale * 2.0 ** -149))
