@@ -846,19 +846,19 @@ __global__ void __launch_bounds__(32 * kWarps)
       }
     }
   }
-  float top = 0.f;
-  bool none = false;
+  const float top = lanes_max<W>(of_chosen);
+  bool none = top < kNoScore;
   if (!p.sigmoid) {
-    of_all = lanes_max<W>(of_all);
-    top = lanes_max<W>(of_chosen);
-    none = top - of_all < kNoScore;
-    if (top == -INFINITY) top = 0.f;
+    none = !(top - lanes_max<W>(of_all) >= kNoScore);  // (and where all are -inf)
     number = lanes_max<W>(number ? 0 : 1) == 0;
   }
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     if (expert[i] >= 0) {
-      s[i] = p.sigmoid ? logistic(x[i]) : expf(x[i] - top);
+      if (!p.renorm)
+        s[i] = logistic(x[i]);
+      else if (!(none && x[i] == x[i]))
+        s[i] = part_of_chosen(p, x[i], top);
       rest[i] = p.sigmoid ? logistic(-x[i]) : 1.f;
     }
   }
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     // (divided before they are summed: an expert alone has 1, and no gradient)
     const float sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
 #pragma unroll
-    for (int i = 0; i < S; ++i) s[i] = sum == 0.f || none ? 0.f : s[i] / sum;
+    for (int i = 0; i < S; ++i) s[i] = sum == 0.f ? 0.f : s[i] / sum;
     dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]);
   }
   const L fill = to_logit<L>(number ? 0.f : NAN);  // where nothing was chosen
@@ -924,11 +924,20 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
   const L* row = static_cast<const L*>(p.logits) + token * p.ld;
   float* d = rows + warp * p.experts;
   const bool all = !p.sigmoid && !p.renorm;  // every expert's logit takes part
-  float top = 0.f, inv = 1.f;
+  float top = 0.f, inv = 1.f;  // renormalised: top is of the chosen
   bool none = false;  // the chosen scores are 0
   float rest_of = 0.f;  // the gradient where nothing was chosen: NaN with a score of NaN
+  if (p.renorm) {
+    float of_chosen = -INFINITY;
+    for (int j = lane; j < p.topk; j += 32) {
+      const int e = p.expert[token * p.topk + j];
+      if (e >= 0 && e < p.experts) of_chosen = fmaxf(of_chosen, as_float(row[e]));
+    }
+    top = warp_max(of_chosen);
+    none = top < kNoScore;
+  }
   if (!p.sigmoid) {
-    float of_all = -INFINITY, of_chosen = -INFINITY;
+    float of_all = -INFINITY;
     bool number = true;
     for (int e = lane; e < p.experts; e += 32) {
       const float x = as_float(row[e]);
@@ -937,16 +946,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
     }
     of_all = warp_max(of_all);
     if (!__all_sync(kAll, number)) rest_of = NAN;
-    top = of_all;
-    if (p.renorm) {
-      for (int j = lane; j < p.topk; j += 32) {
-        const int e = p.expert[token * p.topk + j];
-        if (e >= 0 && e < p.experts) of_chosen = fmaxf(of_chosen, as_float(row[e]));
-      }
-      top = warp_max(of_chosen);
-      none = top - of_all < kNoScore;
-    }
-    if (top == -INFINITY) top = 0.f;
+    if (p.renorm)
+      none = !(top - of_all >= kNoScore);  // (and where all are -inf)
+    else
+      top = of_all == -INFINITY ? 0.f : of_all;
   }
   if (all) {
     float sum = 0.f;
@@ -972,7 +975,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
         expert[i] = e;
         g[i] = p.d_weight[token * p.topk + j];
         const float x = as_float(row[e]);
-        s[i] = p.sigmoid ? logistic(x) : expf(x - top) * inv;
+        if (!p.renorm)
+          s[i] = p.sigmoid ? logistic(x) : expf(x - top) * inv;
+        else if (!(none && x == x))
+          s[i] = part_of_chosen(p, x, top);
         rest[i] = p.sigmoid ? logistic(-x) : 1.f;
       }
     }
@@ -982,7 +988,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
     // (divided before they are summed: an expert alone has 1, and no gradient)
     const float sum = warp_sum(s[0] + s[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) s[i] = sum == 0.f || none ? 0.f : s[i] / sum;
+    for (int i = 0; i < 2; ++i) s[i] = sum == 0.f ? 0.f : s[i] / sum;
     dot = warp_sum(g[0] * s[0] + g[1] * s[1]);
   } else if (all) {
     dot = warp_sum(g[0] * s[0] + g[1] * s[1]);

@@ -140,3 +140,14 @@ def test_weights_of_low_sigmoid_scores(tokens, dtype, topk, renorm, scale):
         assert np.array_equal(expert.cpu().numpy(), want)
         weight = weight.double().cpu().numpy()
         assert np.all((np.isnan(weight) & np.isnan(w)) | (np.abs(weight - w) <= 2.0 ** -18 * w + 4 * scale * 2.0 ** -149))
+
+
+@pytest.mark.parametrize("experts,topk,pad", [(64, 8, 0), (64, 1, 0), (61, 8, 0), (64, 20, 0), (64, 12, 2)])
+@pytest.mark.parametrize("dtype", [gf.GF_F32, gf.GF_F16])
+def test_gradient_of_low_sigmoid_scores(experts, topk, pad, dtype):
+    tokens = 60
+    base = torch.tensor(LOW, device="cuda").repeat(5)[:, None]
+    logits = (base + randn(tokens, experts + pad, seed=8)).to(TDT[dtype])
+    rng = np.random.default_rng(9)
+    expert = np.argsort(rng.random((tokens, experts)), 1)[:, :topk]
+    check_grad(logits, experts, expert, rng.standard_normal((tokens, topk)).astype(np.float32), dtype, SIGMOID, True, 2.5)
