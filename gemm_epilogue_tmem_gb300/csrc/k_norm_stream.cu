@@ -368,8 +368,10 @@ __global__ void __launch_bounds__(stream_threads(V), stream_per_sm(V))
 
 template <typename K>
 cudaError_t launch_ring(K kernel, const NormParams& p, const NormStream& s, cudaStream_t stream, int pdl) {
+  // (always the same amount: it belongs to the kernel, which another thread may be launching
+  // with the ring of other rows)
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(s.smem));
+                                             static_cast<int>(kStreamSmem));
   if (e != cudaSuccess) return e;
   NormParams q = p;
   q.stages = s.stages;
