@@ -15,13 +15,12 @@ namespace {
 
 constexpr int kPerSm = 4;  // CTAs of an SM
 
-// act'(z): with s = 1 / (1 + e^-u) and act = z s, s + z u' s (1 - s); u = z (SiLU) or
+// act'(z) of SiLU and GELU: with s = 1 / (1 + e^-u) and act = z s, s + z u' s (1 - s); u = z (SiLU) or
 // 2 c (z + k z^3) (GELU's tanh form). e^-u by the hardware's exponential of base 2, the
 // base in the constants, and its reciprocal, small results flushed. Where s has reached
 // its end the second term is 0, also for an infinite z.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
   constexpr float kLog2e = 1.4426950408889634f;
   const float z2 = z * z;
   const float t = ACT == kActGelu ? z * fmaf(-2.f * kGeluCK * kLog2e, z2, -2.f * kGeluC * kLog2e)
@@ -69,7 +68,12 @@ __global__ void __launch_bounds__(256, kPerSm) dact_kernel(const DactParams p) {
           if constexpr (ACT != kActNone) {
             unpack8<T>(z[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(f[j]);
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (ACT == kActRelu)
+                d[j] = f[j] > 0.f ? d[j] : 0.f;  // (an infinite gradient too)
+              else
+                d[j] *= act_slope<ACT>(f[j]);
+            }
             static_cast<uint4*>(p.d_z)[((row0 + 8 * i) * p.cols + col) >> 3] =
                 make_uint4(pack2<T>(d[0], d[1]), pack2<T>(d[2], d[3]), pack2<T>(d[4], d[5]),
                            pack2<T>(d[6], d[7]));

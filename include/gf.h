@@ -253,8 +253,8 @@ GF_API gf_status gf_matmul_residual_execute(const gf_plan* plan, const void* A, 
  * The gradients of that call up to its product: with d_out the gradient of out,
  * which is the residual's as well,
  *   d_z = d_out * act'(z),   bgrad[j] = sum_i d_z[i][j]  (fp32, before rounding)
- * d_z goes on into the products of the gradients of A and B. act'(z) of ReLU is 1 for
- * z > 0, else 0. Sums run in an order that the plan fixes: the same bits every time.
+ * d_z goes on into the products of the gradients of A and B. d_z of ReLU is d_out for
+ * z > 0, else 0 whatever d_out is. Sums run in an order that the plan fixes: the same bits every time.
  *
  * m, n: 0 <= m, n < 2^31, n % 8 == 0 (else GF_ERR_UNSUPPORTED). d_out, z, d_z: device
  * [m, n] of dtype; d_z may be d_out or z. bgrad: device fp32 [n], or NULL: not

@@ -68,3 +68,22 @@ def test_two_threads_with_their_own_plans():
     finally:
         sys.setswitchinterval(interval)
     assert not failed and not wrong, (failed, wrong)
+
+
+@pytest.mark.parametrize("dtype", [gf.GF_F16, gf.GF_BF16])
+def test_relu_gradient_of_closed_units(dtype):
+    """Where z > 0 does not hold, d_z and its part of the bias gradient are 0 whatever d_out is."""
+    rows, cols = 300, 264
+    d, z = randn(rows, cols, seed=1, dtype=TDT[dtype]), randn(rows, cols, seed=2, dtype=TDT[dtype])
+    z[:, 0], z[:, 1] = 0.0, NAN
+    closed = ~(z > 0)
+    odd = torch.tensor([INF, -INF, NAN], device="cuda", dtype=TDT[dtype])[torch.arange(rows * cols, device="cuda").view(rows, cols) % 3]
+    d = torch.where(closed, odd, d)
+    plan = gf.gf_dact_bgrad_plan(rows, cols, dtype, gf.GF_ACT_RELU)
+    d_z, bgrad = torch.empty_like(d), torch.empty(cols, device="cuda")
+    gf.gf_dact_bgrad_execute(plan, d, z, d_z, bgrad)
+    plan.free()
+    want = torch.where(closed, 0.0, d.double())
+    assert torch.equal(d_z.double(), want)
+    # fp32 sums of at most 300 terms
+    assert bool(((bgrad.double() - want.sum(0)).abs() <= want.abs().sum(0) * 300 * 2.0 ** -24).all())
