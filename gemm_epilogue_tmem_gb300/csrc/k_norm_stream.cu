@@ -243,8 +243,9 @@ __global__ void __launch_bounds__(stream_threads(V), stream_per_sm(V))
         float inv;
         const float scale = e4m3_scale(bits, inv);
         uint4 q;
-        if (finite) {
-          q = quant16<true>(f, rstd * inv);  // (inv a power of two: rounded as f * rstd is)
+        const float both = rstd * inv;  // (inv a power of two: rounded as f * rstd is)
+        if (finite && both < INFINITY) {
+          q = quant16<true>(f, both);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) f[j] *= rstd;

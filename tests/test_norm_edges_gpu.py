@@ -87,3 +87,25 @@ def test_relu_gradient_of_closed_units(dtype):
     assert torch.equal(d_z.double(), want)
     # fp32 sums of at most 300 terms
     assert bool(((bgrad.double() - want.sum(0)).abs() <= want.abs().sum(0) * 300 * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("rows", [7, 6000])  # loaded by their CTA, and streamed
+def test_e4m3_of_small_products(rows):
+    """y of an ordinary size beside products r * weight near fp32's smallest: the factor of the row and the reciprocal of
+    the scale are each within fp32, their product is not."""
+    hidden = 256
+    x = (randn(rows, hidden, seed=3) * 2.0 ** -55).bfloat16()
+    w = ((1 + 0.3 * randn(hidden, seed=4)) * 2.0 ** -69).bfloat16()
+    x[:, 5] = 0
+    plan = gf.gf_rmsnorm_plan(rows, hidden, gf.GF_BF16, 0.0)
+    q, scale = torch.empty(rows, hidden, dtype=torch.uint8, device="cuda"), torch.empty(rows, 2, device="cuda")
+    gf.gf_rmsnorm_execute(plan, x, w, out8=q, out_scale=scale)
+    plan.free()
+    y = x.double() * w.double() / x.double().square().mean(1, keepdim=True).sqrt()
+    top = y.abs().view(rows, 2, 128).amax(2)
+    assert torch.equal(scale.double(), torch.exp2(torch.ceil(torch.log2(top / 448))))
+    v, got = y / scale.double().repeat_interleave(128, 1), q.view(torch.float8_e4m3fn).double()
+    # e4m3's rounding; and products of some 2^-124 are off by up to 2^-150, in steps of the scale (2^-76) and the
+    # row's factor (2^55) 2^-19
+    bound = torch.maximum(v.abs() * (2.0 ** -4 + 2.0 ** -17), torch.full_like(v, 2.0 ** -10 * (1 + 2.0 ** -17))) + 2.0 ** -18
+    assert bool(((got - v).abs() <= bound).all())
