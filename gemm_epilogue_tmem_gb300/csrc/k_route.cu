@@ -40,6 +40,7 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kManyTokens = 2048;  // from which on a token may have eight lanes
 constexpr int kWarps = 4;      // tokens of a CTA
 constexpr float kNoScore = -745.f;  // e to this is 0 in 64 bits
+constexpr float kLowSum = 0x1p-100f;    // a sum of sigmoid's scores that are not taken as they are
 
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -590,8 +591,10 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
           first = key[0] & ~MASK;
           second = VPL > 1 ? key[VPL > 1 ? 1 : 0] & ~MASK : INT_MIN;
         }
-        a = first < kNone ? -INFINITY : fast_score(p, __int_as_float(ordered(first)), top, inv);
-        b = second < kNone ? -INFINITY : fast_score(p, __int_as_float(ordered(second)), top, inv);
+        a = fast_score(p, __int_as_float(ordered(first)), top, inv);
+        b = fast_score(p, __int_as_float(ordered(second)), top, inv);
+        if (first < kNone) a = -INFINITY;
+        if (second < kNone) b = -INFINITY;
       } else {
         a = value_of<MASK>(key[0]);
         b = VPL > 1 ? value_of<MASK>(key[VPL > 1 ? 1 : 0]) : -INFINITY;
@@ -746,18 +749,31 @@ __global__ void __launch_bounds__(32 * kWarps, resident(W, VPL))
 #pragma unroll
     for (int s = 0; s < S; ++s) x[s] = expert[s] >= 0 ? as_float(row[expert[s]]) : -INFINITY;
     if (p.renorm) {
-      const float chosen = lanes_max<W>(fmaxf(x[0], x[S - 1]));
-      const bool none = (p.sigmoid ? chosen : chosen - top) < kNoScore;
-      float sum = 0.f;
+      float most = 0.f, sum = 0.f;
+      bool none = false, low = p.sigmoid;
+      auto add_parts = [&] {
+        sum = 0.f;
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        w[s] = expert[s] >= 0 && !(none && x[s] == x[s]) ? part_of_chosen(p, x[s], chosen) : 0.f;
-        sum += w[s];
+        for (int s = 0; s < S; ++s) {
+          w[s] = expert[s] >= 0 && !(none && x[s] == x[s]) ? part_of_chosen(p, x[s], most) : 0.f;
+          sum += w[s];
+        }
+        sum = lanes_sum<W>(sum);
+      };
+      if (p.sigmoid) {  // as they are, unless they are small
+        add_parts();
+        low = __any_sync(kAll, sum < kLowSum);
       }
-      sum = lanes_sum<W>(sum);
+      if (!p.sigmoid || low) {
+        most = lanes_max<W>(fmaxf(x[0], x[S - 1]));
+        // (a token's weights do not depend on those of its warp's others)
+        if (p.sigmoid && !(sum < kLowSum)) most = 0.f;
+        none = (p.sigmoid ? most : most - top) < kNoScore;
+        add_parts();
+      }
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        w[s] = sum == 0.f ? 0.f : w[s] / sum * p.scale;
+        w[s] = sum == 0.f ? 0.f : __fdividef(w[s], sum) * p.scale;
         // a logit without a number (or infinite) makes every score NaN, chosen or not
         if (inv != inv) w[s] = inv;
       }
@@ -846,26 +862,30 @@ __global__ void __launch_bounds__(32 * kWarps)
       }
     }
   }
-  const float top = lanes_max<W>(of_chosen);
-  bool none = top < kNoScore;
-  if (!p.sigmoid) {
-    none = !(top - lanes_max<W>(of_all) >= kNoScore);  // (and where all are -inf)
-    number = lanes_max<W>(number ? 0 : 1) == 0;
-  }
+  if (!p.sigmoid) number = lanes_max<W>(number ? 0 : 1) == 0;
 #pragma unroll
   for (int i = 0; i < S; ++i) {
-    if (expert[i] >= 0) {
-      if (!p.renorm)
-        s[i] = logistic(x[i]);
-      else if (!(none && x[i] == x[i]))
-        s[i] = part_of_chosen(p, x[i], top);
-      rest[i] = p.sigmoid ? logistic(-x[i]) : 1.f;
+    if (p.sigmoid && expert[i] >= 0) {
+      s[i] = logistic(x[i]);
+      rest[i] = logistic(-x[i]);
+    } else {
+      rest[i] = 1.f;
     }
   }
   float dot = 0.f;
   if (p.renorm) {
+    float sum = 0.f;
+    if (p.sigmoid) sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
+    if (!p.sigmoid || __any_sync(kAll, sum < kLowSum)) {
+      float top = lanes_max<W>(of_chosen);
+      if (p.sigmoid && !(sum < kLowSum)) top = 0.f;  // (whatever the warp's other tokens are)
+      const bool none = p.sigmoid ? top < kNoScore : !(top - lanes_max<W>(of_all) >= kNoScore);  // (and where all are -inf)
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        s[i] = expert[i] >= 0 && !(none && x[i] == x[i]) ? part_of_chosen(p, x[i], top) : 0.f;
+      sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
+    }
     // (divided before they are summed: an expert alone has 1, and no gradient)
-    const float sum = lanes_sum<W>(S == 2 ? s[0] + s[S - 1] : s[0]);
 #pragma unroll
     for (int i = 0; i < S; ++i) s[i] = sum == 0.f ? 0.f : s[i] / sum;
     dot = lanes_sum<W>(S == 2 ? g[0] * s[0] + g[S - 1] * s[S - 1] : g[0] * s[0]);

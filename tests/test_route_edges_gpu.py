@@ -151,3 +151,22 @@ def test_gradient_of_low_sigmoid_scores(experts, topk, pad, dtype):
     rng = np.random.default_rng(9)
     expert = np.argsort(rng.random((tokens, experts)), 1)[:, :topk]
     check_grad(logits, experts, expert, rng.standard_normal((tokens, topk)).astype(np.float32), dtype, SIGMOID, True, 2.5)
+
+
+def test_a_token_does_not_depend_on_its_neighbours():
+    """The same token among tokens of ordinary and of low scores, whose sums are formed otherwise: the same bits."""
+    tokens, experts, topk = 4096, 64, 8
+    logits = (randn(tokens, experts, seed=11) - 30).half()
+    low = logits.clone()
+    low[::2] -= 200
+    for score in (SIGMOID, SOFTMAX):
+        plan = gf.gf_route_plan(tokens, experts, topk, gf.GF_F16, score, True, 2.5)
+        expert = torch.empty(tokens, topk, dtype=torch.int32, device="cuda")
+        d_weight, got = randn(tokens, topk, seed=12), []
+        for l in (logits, low):
+            weight, d = torch.empty(tokens, topk, device="cuda"), torch.empty_like(l)
+            gf.gf_route_execute(plan, l, expert, weight)
+            gf.gf_route_grad_execute(plan, l, expert, d_weight, d)
+            got.append((expert[1::2].clone(), weight[1::2], d[1::2]))
+        plan.free()
+        assert all(torch.equal(a, b) for a, b in zip(*got))
