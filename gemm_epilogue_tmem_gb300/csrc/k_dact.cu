@@ -14,6 +14,9 @@ namespace gf {
 namespace {
 
 constexpr int kPerSm = 4;  // CTAs of an SM
+// rows of a chunk at most, an eighth of which fp32 adds up in a row: beside the sum of 2^18 of its
+// size a term has 6 bits left
+constexpr int64_t kMostRows = 65536;
 
 // act'(z) of SiLU and GELU: with s = 1 / (1 + e^-u) and act = z s, s + z u' s (1 - s); u = z (SiLU) or
 // 2 c (z + k z^3) (GELU's tanh form). e^-u by the hardware's exponential of base 2, the
@@ -114,7 +117,8 @@ cudaError_t dact(const DactParams& p, int chunks, cudaStream_t stream, int pdl) 
 int dact_chunks(int64_t rows, int64_t cols, int sms) {
   const int64_t blocks = (cols + 255) / 256;
   int64_t chunks = static_cast<int64_t>(sms) * kPerSm / blocks;  // one wave of CTAs
-  const int64_t most = (rows + 31) / 32;
+  const int64_t least = (rows + kMostRows - 1) / kMostRows, most = (rows + 31) / 32;
+  if (chunks < least) chunks = least;
   if (chunks > most) chunks = most;
   return static_cast<int>(chunks < 1 ? 1 : chunks);
 }

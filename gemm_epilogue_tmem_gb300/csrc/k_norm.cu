@@ -366,7 +366,9 @@ cudaError_t grad_ctas(int64_t rows, int64_t hidden, int sms, int* ctas) {
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     int64_t n = (rows + s.rows - 1) / s.rows;
-    if (n > static_cast<int64_t>(per_sm) * sms) n = static_cast<int64_t>(per_sm) * sms;
+    const int64_t resident = static_cast<int64_t>(per_sm) * sms;
+    const int64_t least = (n + kMostTurns - 1) / kMostTurns;
+    if (n > resident) n = resident > least ? resident : least;
     if (hidden % 8 != 0) n = (n + 7) / 8 * 8;  // thread rows in whole periods
     *ctas = static_cast<int>(n < 1 ? 1 : n);
     return cudaSuccess;

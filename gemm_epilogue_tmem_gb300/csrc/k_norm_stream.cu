@@ -425,7 +425,8 @@ bool norm_stream_shape(int64_t rows, int64_t hidden, int arrays, bool pairs, int
   s->smem = s->stages * stage;
   const int64_t groups = (rows + s->rows - 1) / s->rows, most = static_cast<int64_t>(per_sm) * sms;
   // as many turns for every CTA, but for one
-  const int64_t turns = (groups + most - 1) / most;
+  int64_t turns = (groups + most - 1) / most;
+  if (turns > kMostTurns) turns = kMostTurns;
   s->ctas = static_cast<int>(turns > 0 ? (groups + turns - 1) / turns : 0);
   return turns >= kLeastTurns;
 }

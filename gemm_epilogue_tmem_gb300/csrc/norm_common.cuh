@@ -136,6 +136,11 @@ __device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
 }
 
 // Many rows of whole 16-byte words: the streaming kernels take them, see k_norm_stream.cu.
+// Rows that a thread goes through at most, so that fp32 adds up no more terms of the weight's
+// gradient in a row: beside the sum of 2^18 of its size a term has 6 bits left. More rows take more
+// CTAs than are resident, each with sums of its own.
+constexpr int64_t kMostTurns = 4096;
+
 struct NormStream {
   int v, threads, rows;  // words a thread, threads a row, rows of a group
   int stages, ctas;

@@ -241,7 +241,8 @@ GF_API gf_plan* gf_dact_bgrad_plan(int64_t m, int64_t n, gf_dtype dtype, gf_acti
   p->num_chunks = m == 0 || n == 0 ? 0 : gf::dact_chunks(m, n, p->num_sms);
   p->tile_rows = p->num_chunks == 0 ? 0 : static_cast<int>((m + p->num_chunks - 1) / p->num_chunks);
   p->tile_n = 256;
-  p->grid = static_cast<int>((n + 255) / 256) * p->num_chunks;
+  const int64_t ctas = (n + 255) / 256 * p->num_chunks;
+  p->grid = static_cast<int>(ctas < kMaxDim ? ctas : kMaxDim);
   const gf_status st = add_partials(p, p->num_chunks, n);
   if (st != GF_OK) {
     gf_plan_free(p);
