@@ -35,6 +35,8 @@ constexpr int kRouteMaxGroups = 32;
 
 // logits: 0 fp16, 1 bf16, 2 fp32
 cudaError_t launch_route(const RouteParams& p, int type, cudaStream_t stream, int pdl);
+// the CTAs of that launch, and the tokens that each has at a time
+int64_t route_ctas(const RouteParams& p, int type, int* tokens);
 cudaError_t launch_route_grad(const RouteParams& p, int type, cudaStream_t stream, int pdl);
 
 // --------------------------------------------------------------------- norm
@@ -61,6 +63,8 @@ struct NormParams {
 };
 
 cudaError_t launch_norm(const NormParams& p, int bf16, cudaStream_t stream, int pdl);
+// the CTAs of that launch, the rows that each has at a time, and its ring's stages (0: no ring)
+int64_t norm_ctas(const NormParams& p, int* rows, int* stages);
 // The CTAs of the backward kernel that loads its rows itself, for so many (0 with an
 // error in *err), and the most rows of partial sums of either backward kernel.
 int norm_grad_ctas(int64_t rows, int64_t hidden, int bf16, int sms, cudaError_t* err);

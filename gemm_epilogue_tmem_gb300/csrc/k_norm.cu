@@ -388,10 +388,25 @@ cudaError_t backward(const NormParams& p, int ctas, cudaStream_t stream, int pdl
 
 }  // namespace
 
+static bool streams(const NormParams& p, NormStream* s) {
+  return norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 2 : 1, p.out8 != nullptr, p.sms, s);
+}
+
+int64_t norm_ctas(const NormParams& p, int* rows, int* stages) {
+  NormStream s;
+  if (streams(p, &s)) {
+    *rows = s.rows;
+    *stages = s.stages;
+    return s.ctas;
+  }
+  *rows = norm_shape(p.hidden).rows;
+  *stages = 0;
+  return (static_cast<int64_t>(p.rows) + *rows - 1) / *rows;
+}
+
 cudaError_t launch_norm(const NormParams& p, int bf16, cudaStream_t stream, int pdl) {
   NormStream s;
-  if (norm_stream_shape(p.rows, p.hidden, p.residual != nullptr ? 2 : 1, p.out8 != nullptr, p.sms, &s))
-    return launch_norm_stream(p, s, bf16, stream, pdl);
+  if (streams(p, &s)) return launch_norm_stream(p, s, bf16, stream, pdl);
   return bf16 ? forward_type<__nv_bfloat16>(p, stream, pdl) : forward_type<__half>(p, stream, pdl);
 }
 

@@ -1041,30 +1041,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_co
   for (int64_t e = lane; e < p.ld; e += 32) out[e] = to_logit<L>(e < p.experts ? d[e] : 0.f);
 }
 
-template <typename L, int W, int VPL>
-cudaError_t route_of(const RouteParams& p, cudaStream_t stream, int pdl) {
-  // A warp a token: as many CTAs as are resident at once, more tokens follow in their loop,
-  // each loaded ahead (16384 tokens, 256 experts in groups with a bias, with six CTAs an
-  // SM: 23.4 us; a CTA for every four tokens 26.1). Four tokens a warp: a CTA for every 16, as the loop's last
-  // turn would leave many idle (128 experts, 16384 / 65536 tokens 7.1 / 16.1 us; in a
-  // loop 9.3 / 25.1).
-  constexpr int kTokens = kWarps * (32 / W);
-  const int64_t all = (static_cast<int64_t>(p.tokens) + kTokens - 1) / kTokens;
-  const int64_t most = static_cast<int64_t>(p.sms) * resident(W, VPL);
-  const dim3 grid(static_cast<unsigned>(W < 32 || all < most ? all : most)), block(32 * kWarps);
-  if constexpr (W == 32) {
-    if (p.bias != nullptr)
-      return launch_pdl(route_kernel<L, W, VPL, true>, grid, block, 0, stream, pdl, p);
-  }
-  return launch_pdl(route_kernel<L, W, VPL, false>, grid, block, 0, stream, pdl, p);
-}
-
 // The lanes of w that share a group, a power of two, and the experts of each.
-template <typename L>
-RouteParams map_lanes(RouteParams p, int w) {
+RouteParams map_lanes(RouteParams p, int w, int size) {
   p.lane_shift = 0;
   while (p.groups << (p.lane_shift + 1) <= w) ++p.lane_shift;
-  const int lanes = 1 << p.lane_shift, size = static_cast<int>(sizeof(L));
+  const int lanes = 1 << p.lane_shift;
   p.per_lane = (p.group_size + lanes - 1) / lanes;
   const int bytes = p.per_lane * size, word = bytes < 16 ? bytes : 16;
   p.vector = (p.per_lane & (p.per_lane - 1)) == 0 && p.group_size == lanes * p.per_lane &&
@@ -1074,26 +1055,67 @@ RouteParams map_lanes(RouteParams p, int w) {
   return p;
 }
 
+// The instance for a call, logits of `size` bytes: lanes a token, experts a lane; its CTAs and
+// the tokens that each has at a time.
+struct RouteShape {
+  int w, vpl, tokens;
+  int64_t ctas;
+};
+
+RouteShape route_shape(const RouteParams& args, int size) {
+  RouteShape s = {32, 0, kWarps, 0};
+  if (size == 2 && args.tokens >= kManyTokens && args.bias == nullptr && args.groups <= 8 && args.topk <= 16 &&
+      (args.groups == 1 || args.group_best == 1) && map_lanes(args, 8, size).per_lane <= 16)
+    s.w = 8;
+  const int per_lane = map_lanes(args, s.w, size).per_lane;
+  const int n = s.w == 32 && args.topk > 32 && per_lane < 32 ? 32 : per_lane;  // two slots a lane
+  for (s.vpl = s.w == 32 ? 1 : 4; s.vpl < n;) s.vpl *= 2;
+  s.tokens = kWarps * (32 / s.w);
+  // A warp a token: as many CTAs as are resident at once, more tokens follow in their loop,
+  // each loaded ahead (16384 tokens, 256 experts in groups with a bias, with six CTAs an
+  // SM: 23.4 us; a CTA for every four tokens 26.1). Four tokens a warp: a CTA for every 16, as the loop's last
+  // turn would leave many idle (128 experts, 16384 / 65536 tokens 7.1 / 16.1 us; in a
+  // loop 9.3 / 25.1).
+  const int64_t all = (static_cast<int64_t>(args.tokens) + s.tokens - 1) / s.tokens;
+  const int64_t most = static_cast<int64_t>(args.sms) * resident(s.w, s.vpl);
+  s.ctas = s.w < 32 || all < most ? all : most;
+  return s;
+}
+
+template <typename L, int W, int VPL>
+cudaError_t route_of(const RouteParams& p, int64_t ctas, cudaStream_t stream, int pdl) {
+  const dim3 grid(static_cast<unsigned>(ctas)), block(32 * kWarps);
+  if constexpr (W == 32) {
+    if (p.bias != nullptr)
+      return launch_pdl(route_kernel<L, W, VPL, true>, grid, block, 0, stream, pdl, p);
+  }
+  return launch_pdl(route_kernel<L, W, VPL, false>, grid, block, 0, stream, pdl, p);
+}
+
 template <typename L>
 cudaError_t route(const RouteParams& args, cudaStream_t stream, int pdl) {
+  const RouteShape s = route_shape(args, static_cast<int>(sizeof(L)));
+  const RouteParams p = map_lanes(args, s.w, static_cast<int>(sizeof(L)));
   if constexpr (sizeof(L) == 2) {
-    if (args.tokens >= kManyTokens && args.bias == nullptr && args.groups <= 8 && args.topk <= 16 &&
-        (args.groups == 1 || args.group_best == 1)) {
-      const RouteParams p = map_lanes<L>(args, 8);
-      if (p.per_lane <= 4) return route_of<L, 8, 4>(p, stream, pdl);
-      if (p.per_lane <= 8) return route_of<L, 8, 8>(p, stream, pdl);
-      if (p.per_lane <= 16) return route_of<L, 8, 16>(p, stream, pdl);
+    if (s.w == 8) {
+      switch (s.vpl) {
+        case 4: return route_of<L, 8, 4>(p, s.ctas, stream, pdl);
+        case 8: return route_of<L, 8, 8>(p, s.ctas, stream, pdl);
+        case 16: return route_of<L, 8, 16>(p, s.ctas, stream, pdl);
+      }
+      return cudaErrorInvalidValue;
     }
   }
-  const RouteParams p = map_lanes<L>(args, 32);
-  const int n = p.topk > 32 && p.per_lane < 32 ? 32 : p.per_lane;  // two slots a lane
-  if (n <= 1) return route_of<L, 32, 1>(p, stream, pdl);
-  if (n <= 2) return route_of<L, 32, 2>(p, stream, pdl);
-  if (n <= 4) return route_of<L, 32, 4>(p, stream, pdl);
-  if (n <= 8) return route_of<L, 32, 8>(p, stream, pdl);
-  if (n <= 16) return route_of<L, 32, 16>(p, stream, pdl);
-  if (n <= 32) return route_of<L, 32, 32>(p, stream, pdl);
-  return route_of<L, 32, 64>(p, stream, pdl);
+  switch (s.vpl) {
+    case 1: return route_of<L, 32, 1>(p, s.ctas, stream, pdl);
+    case 2: return route_of<L, 32, 2>(p, s.ctas, stream, pdl);
+    case 4: return route_of<L, 32, 4>(p, s.ctas, stream, pdl);
+    case 8: return route_of<L, 32, 8>(p, s.ctas, stream, pdl);
+    case 16: return route_of<L, 32, 16>(p, s.ctas, stream, pdl);
+    case 32: return route_of<L, 32, 32>(p, s.ctas, stream, pdl);
+    case 64: return route_of<L, 32, 64>(p, s.ctas, stream, pdl);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <typename L, typename Word>
@@ -1122,6 +1144,12 @@ cudaError_t route_grad(const RouteParams& p, cudaStream_t stream, int pdl) {
 }
 
 }  // namespace
+
+int64_t route_ctas(const RouteParams& p, int type, int* tokens) {
+  const RouteShape s = route_shape(p, type == 2 ? 4 : 2);
+  *tokens = s.tokens;
+  return s.ctas;
+}
 
 cudaError_t launch_route(const RouteParams& p, int type, cudaStream_t stream, int pdl) {
   switch (type) {

@@ -73,7 +73,7 @@ struct gf_plan {
   // gf_moe_plan: m = tokens, k = hidden
   int64_t topk, experts;
   int chunk_tokens;      // tokens per CTA of the sort
-  int num_chunks;
+  int num_chunks;        // gf_dact_bgrad_plan: of its rows; gf_rmsnorm_plan: the gradient's CTAs
   int fused;             // little to copy: the sort kernel does that too
   void* d_work;          // e4m3 products: counters and partial sums of split tiles;
                          // gradients of a norm's weight, a bias: the CTAs' column sums

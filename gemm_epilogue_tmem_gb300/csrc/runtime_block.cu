@@ -53,6 +53,28 @@ gf_status add_partials(gf_plan* p, int64_t rows, int64_t cols) {
 extern "C" {
 
 // ------------------------------------------------------------------- router
+static gf::RouteParams route_params(const gf_plan* p, const void* logits) {
+  gf::RouteParams r = {};
+  r.tokens = static_cast<int32_t>(p->m);
+  r.experts = static_cast<int32_t>(p->experts);
+  r.topk = static_cast<int32_t>(p->topk);
+  r.groups = static_cast<int32_t>(p->groups);
+  r.group_size = static_cast<int32_t>(p->experts / p->groups);
+  r.topk_groups = static_cast<int32_t>(p->topk_groups);
+  r.group_best = p->group_best;
+  r.sigmoid = p->score == GF_SCORE_SIGMOID ? 1 : 0;
+  r.renorm = p->renorm;
+  r.scale = p->scale;
+  r.ld = p->ld;
+  r.logits = logits;
+  r.sms = p->num_sms;
+  return r;
+}
+
+static int logits_type(const gf_plan* p) {
+  return p->dtype == GF_F32 ? 2 : p->dtype == GF_BF16 ? 1 : 0;
+}
+
 GF_API gf_plan* gf_route_plan(int64_t tokens, int64_t experts, int64_t topk, gf_dtype dtype,
                               gf_score score, int32_t renorm, float scale, int64_t groups,
                               int64_t topk_groups, int32_t group_best, int64_t ld) {
@@ -78,32 +100,9 @@ GF_API gf_plan* gf_route_plan(int64_t tokens, int64_t experts, int64_t topk, gf_
   p->score = score;
   p->renorm = renorm;
   p->scale = scale;
-  p->tile_rows = 4;
   p->tile_n = static_cast<int>(experts);
-  p->grid = static_cast<int>((tokens + 3) / 4);
+  p->grid = static_cast<int>(gf::route_ctas(route_params(p, nullptr), logits_type(p), &p->tile_rows));
   return p;
-}
-
-static gf::RouteParams route_params(const gf_plan* p, const void* logits) {
-  gf::RouteParams r = {};
-  r.tokens = static_cast<int32_t>(p->m);
-  r.experts = static_cast<int32_t>(p->experts);
-  r.topk = static_cast<int32_t>(p->topk);
-  r.groups = static_cast<int32_t>(p->groups);
-  r.group_size = static_cast<int32_t>(p->experts / p->groups);
-  r.topk_groups = static_cast<int32_t>(p->topk_groups);
-  r.group_best = p->group_best;
-  r.sigmoid = p->score == GF_SCORE_SIGMOID ? 1 : 0;
-  r.renorm = p->renorm;
-  r.scale = p->scale;
-  r.ld = p->ld;
-  r.logits = logits;
-  r.sms = p->num_sms;
-  return r;
-}
-
-static int logits_type(const gf_plan* p) {
-  return p->dtype == GF_F32 ? 2 : p->dtype == GF_BF16 ? 1 : 0;
 }
 
 GF_API gf_status gf_route_execute(const gf_plan* p, const void* logits, const float* bias,
@@ -158,14 +157,14 @@ GF_API gf_plan* gf_rmsnorm_plan(int64_t rows, int64_t hidden, gf_dtype dtype, fl
   p->m = rows;
   p->n = p->k = hidden;
   p->scale = eps;
-  p->tile_rows = 1;
   p->tile_n = static_cast<int>(hidden);
+  p->grid = static_cast<int>(gf::norm_ctas(norm_params(p), &p->tile_rows, &p->stages));
   cudaError_t e = cudaSuccess;
-  p->grid = rows == 0 ? 0
-                      : gf::norm_grad_ctas(rows, hidden, dtype == GF_BF16, p->num_sms, &e);
+  p->num_chunks = rows == 0 ? 0
+                            : gf::norm_grad_ctas(rows, hidden, dtype == GF_BF16, p->num_sms, &e);
   gf_status st = e != cudaSuccess ? GF_ERR_CUDA
                  : rows == 0      ? GF_OK
-                                  : add_partials(p, gf::norm_grad_partials(rows, hidden, p->num_sms, p->grid), hidden);
+                                  : add_partials(p, gf::norm_grad_partials(rows, hidden, p->num_sms, p->num_chunks), hidden);
   if (st != GF_OK) {
     cudaGetLastError();
     gf_plan_free(p);
@@ -221,7 +220,7 @@ GF_API gf_status gf_rmsnorm_grad_execute(const gf_plan* p, const void* d_out, co
   n.d_out = d_out;
   n.partials = d_weight != nullptr ? static_cast<float*>(p->d_work) : nullptr;
   int partial_rows = 0;
-  cudaError_t e = gf::launch_norm_grad(n, p->dtype == GF_BF16, p->grid, st, p->pdl, &partial_rows);
+  cudaError_t e = gf::launch_norm_grad(n, p->dtype == GF_BF16, p->num_chunks, st, p->pdl, &partial_rows);
   if (e == cudaSuccess && d_weight != nullptr)
     e = gf::launch_column_sums(n.partials, partial_rows, n.hidden, d_weight, st, p->pdl);
   return launched(e);

@@ -631,7 +631,11 @@ GF_API gf_status gf_matmul_autotune(gf_plan* plan, const void* A, const void* B,
                                     int32_t reps);
 
 /* Read back the plan's choices: tile_m, tile_n, stages, grid size (CTAs per
- * launch), workspace bytes. Any out-pointer may be NULL. */
+ * launch), workspace bytes. Any out-pointer may be NULL. Of gf_route_plan: the call without
+ * a bias, tile_m the tokens of a CTA at a time. Of gf_rmsnorm_plan: the norm in 16 bits
+ * without a residual, tile_m the rows of a CTA at a time, stages those of the ring that its
+ * rows come through (0: none). Of gf_dact_bgrad_plan: the first launch, tile_m the rows of
+ * a CTA. */
 GF_API gf_status gf_plan_describe(const gf_plan* plan, int32_t* tile_m, int32_t* tile_n,
                                   int32_t* stages, int32_t* grid, int64_t* workspace_bytes);
 

@@ -109,3 +109,27 @@ def test_e4m3_of_small_products(rows):
     # row's factor (2^55) 2^-19
     bound = torch.maximum(v.abs() * (2.0 ** -4 + 2.0 ** -17), torch.full_like(v, 2.0 ** -10 * (1 + 2.0 ** -17))) + 2.0 ** -18
     assert bool(((got - v).abs() <= bound).all())
+
+
+def test_describe_is_what_runs():
+    """The plans' grids, tiles and stages are those of the launches: tokens and rows of a CTA times CTAs that cover them,
+    or a resident grid."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+
+    def of(plan):
+        d = gf.gf_plan_describe(plan)
+        plan.free()
+        return d
+
+    # eight lanes a token: 16 tokens a CTA; a warp a token: 4, in a resident grid
+    assert [of(gf.gf_route_plan(16384, 128, 8, gf.GF_BF16))[k] for k in ("tile_m", "grid")] == [16, 1024]
+    d = of(gf.gf_route_plan(16384, 256, 8, gf.GF_F32, gf.GF_SCORE_SIGMOID, groups=8, topk_groups=4))
+    assert d["tile_m"] == 4 and d["grid"] % sms == 0 and d["grid"] < 4096
+    assert [of(gf.gf_route_plan(9, 256, 8, gf.GF_F32))[k] for k in ("tile_m", "grid")] == [4, 3]
+    assert of(gf.gf_route_plan(0, 256, 8, gf.GF_F32))["grid"] == 0
+    # few rows: one CTA each; many: a ring of several stages, all CTAs resident; rows that are not whole words: no ring
+    assert [of(gf.gf_rmsnorm_plan(5, 5120, gf.GF_BF16))[k] for k in ("tile_m", "stages", "grid")] == [1, 0, 5]
+    d = of(gf.gf_rmsnorm_plan(16384, 5120, gf.GF_BF16))
+    assert d["tile_m"] == 1 and d["stages"] >= 2 and d["grid"] <= 5 * sms
+    assert [of(gf.gf_rmsnorm_plan(5003, 2047, gf.GF_F16))[k] for k in ("tile_m", "stages", "grid")] == [1, 0, 5003]
+    assert [of(gf.gf_rmsnorm_plan(7, 64, gf.GF_F16))[k] for k in ("tile_m", "grid")] == [4, 2]
