@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "block.h"
 #include "gf.h"
 #include "moe.h"
@@ -38,13 +40,14 @@ bool known_act(int act) { return act >= GF_ACT_NONE && act <= GF_ACT_SILU; }
 
 // The fp32 column sums of a backward pass, one row for each CTA or chunk.
 gf_status add_partials(gf_plan* p, int64_t rows, int64_t cols) {
-  p->work_bytes = static_cast<size_t>(rows) * static_cast<size_t>(cols) * 4;
-  if (p->work_bytes == 0) return GF_OK;
-  if (cudaMalloc(&p->d_work, p->work_bytes) != cudaSuccess) {
+  const size_t bytes = static_cast<size_t>(rows) * static_cast<size_t>(cols) * 4;
+  if (bytes == 0) return GF_OK;
+  if (cudaMalloc(&p->d_work, bytes) != cudaSuccess) {
     cudaGetLastError();
     p->d_work = nullptr;
     return GF_ERR_OUT_OF_MEMORY;
   }
+  p->work_bytes = bytes;
   return GF_OK;
 }
 
@@ -159,18 +162,30 @@ GF_API gf_plan* gf_rmsnorm_plan(int64_t rows, int64_t hidden, gf_dtype dtype, fl
   p->scale = eps;
   p->tile_n = static_cast<int>(hidden);
   p->grid = static_cast<int>(gf::norm_ctas(norm_params(p), &p->tile_rows, &p->stages));
-  cudaError_t e = cudaSuccess;
-  p->num_chunks = rows == 0 ? 0
-                            : gf::norm_grad_ctas(rows, hidden, dtype == GF_BF16, p->num_sms, &e);
-  gf_status st = e != cudaSuccess ? GF_ERR_CUDA
-                 : rows == 0      ? GF_OK
-                                  : add_partials(p, gf::norm_grad_partials(rows, hidden, p->num_sms, p->num_chunks), hidden);
-  if (st != GF_OK) {
-    cudaGetLastError();
-    gf_plan_free(p);
-    return refuse(st);
-  }
   return p;
+}
+
+// What the gradient alone needs, made by the first call that does: the CTAs of the kernel that
+// loads its rows itself and, for d_weight, the workspace. That call may be captured into a graph:
+// the relaxed mode lets this thread allocate meanwhile.
+static gf_status norm_grad_ready(gf_plan* p, bool sums) {
+  std::lock_guard<std::mutex> lock(p->cache_mu);
+  if (p->num_chunks == 0) {
+    cudaError_t e = cudaSuccess;
+    p->num_chunks = gf::norm_grad_ctas(p->m, p->n, p->dtype == GF_BF16, p->num_sms, &e);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      p->num_chunks = 0;
+      return GF_ERR_CUDA;
+    }
+  }
+  if (!sums || p->d_work != nullptr) return GF_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GF_ERR_CUDA;
+  const gf_status st =
+      add_partials(p, gf::norm_grad_partials(p->m, p->n, p->num_sms, p->num_chunks), p->n);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return st;
 }
 
 GF_API gf_status gf_rmsnorm_execute(const gf_plan* p, const void* x, const void* residual,
@@ -212,6 +227,8 @@ GF_API gf_status gf_rmsnorm_grad_execute(const gf_plan* p, const void* d_out, co
   if (!given(d_out) || !given(r) || !given(weight) || !aligned(d_residual) || !given(d_x))
     return runtime_fail(GF_ERR_INVALID_VALUE);
   if (cudaSetDevice(p->device) != cudaSuccess) return runtime_fail(GF_ERR_CUDA);
+  const gf_status ready = norm_grad_ready(const_cast<gf_plan*>(p), d_weight != nullptr);
+  if (ready != GF_OK) return runtime_fail(ready);
   gf::NormParams n = norm_params(p);
   n.x = r;
   n.residual = d_residual;

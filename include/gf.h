@@ -304,8 +304,9 @@ GF_API gf_status gf_rmsnorm_execute(const gf_plan* plan, const void* x, const vo
  * forward (x, without a residual); nothing else of the forward is needed. d_x: device [rows,
  * hidden] of dtype, may be d_out or d_residual. d_weight: device fp32 [hidden], or NULL: not
  * wanted; its sums run in an order that the plan fixes. One launch, two with d_weight;
- * asynchronous on stream. The plan's workspace is shared by its calls: one stream
- * at a time.
+ * asynchronous on stream. The plan's workspace, the partial sums of d_weight, is allocated by
+ * the first call that wants them (GF_ERR_OUT_OF_MEMORY; that call may be captured into a
+ * graph) and shared by its calls: one stream at a time.
  */
 GF_API gf_status gf_rmsnorm_grad_execute(const gf_plan* plan, const void* d_out, const void* r,
                                          const void* weight, const void* d_residual, void* d_x,

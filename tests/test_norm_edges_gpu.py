@@ -133,3 +133,38 @@ def test_describe_is_what_runs():
     assert d["tile_m"] == 1 and d["stages"] >= 2 and d["grid"] <= 5 * sms
     assert [of(gf.gf_rmsnorm_plan(5003, 2047, gf.GF_F16))[k] for k in ("tile_m", "stages", "grid")] == [1, 0, 5003]
     assert [of(gf.gf_rmsnorm_plan(7, 64, gf.GF_F16))[k] for k in ("tile_m", "grid")] == [4, 2]
+
+
+def test_plans_of_the_forward_alone_hold_no_workspace():
+    """A server keeps a plan for each number of tokens: without a gradient's call none holds memory for one."""
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    plans = [gf.gf_rmsnorm_plan(16384 + i, 5120, gf.GF_BF16) for i in range(64)]
+    assert before - torch.cuda.mem_get_info()[0] < 16 << 20
+    assert gf.gf_plan_describe(plans[0])["workspace_bytes"] <= 256
+    for plan in plans:
+        plan.free()
+
+
+@pytest.mark.parametrize("rows,hidden", [(1000, 2048), (70, 999)])
+def test_first_gradient_is_captured(rows, hidden):
+    """The call that makes the workspace, in a graph: replayed, and the same bits as an ordinary one's."""
+    x, d, w = randn(rows, hidden, seed=1).bfloat16(), randn(rows, hidden, seed=2).bfloat16(), randn(hidden, seed=3).bfloat16()
+    plans = [gf.gf_rmsnorm_plan(rows, hidden, gf.GF_BF16) for _ in range(2)]
+    outs = [(torch.zeros_like(x), torch.zeros(hidden, device="cuda")) for _ in plans]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gf.gf_rmsnorm_grad_execute(plans[0], d, x, w, outs[0][0], d_weight=outs[0][1])
+    gf.gf_rmsnorm_grad_execute(plans[1], d, x, w, outs[1][0], d_weight=outs[1][1])
+    for _ in range(2):
+        outs[0][0].zero_(), outs[0][1].zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert gf.gf_plan_describe(plans[0])["workspace_bytes"] > 256
+    # an eager call of the plan whose graph lives, without the weight's gradient, and with it
+    gf.gf_rmsnorm_grad_execute(plans[0], d, x, w, outs[0][0])
+    gf.gf_rmsnorm_grad_execute(plans[0], d, x, w, outs[0][0], d_weight=outs[0][1])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    del graph
+    for plan in plans:
+        plan.free()
