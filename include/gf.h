@@ -271,8 +271,8 @@ GF_API gf_status gf_dact_bgrad_execute(const gf_plan* plan, const void* d_out, c
  * bits or as the e4m3 operand of gf_fp8_matmul:
  *   r = x + residual rounded to dtype (x, without a residual)
  *   y = r * weight / sqrt(mean(r^2) + eps)
- * y is of r as it is stored. Sums and y are fp32 (the mean of r^2 has to be within
- * its range), rounded once.
+ * y is of r as it is stored. Sums and y are fp32 (the sum of r^2 over a row and the products
+ * r * weight have to be within its range), rounded once.
  *
  * rows >= 0, 1 <= hidden <= 32768 (more: GF_ERR_UNSUPPORTED), eps >= 0 and finite.
  * Options: GF_OPT_PDL, GF_OPT_WAIT_LIMIT_US, GF_OPT_FAULT_DROP_LOAD. gf_plan_status
