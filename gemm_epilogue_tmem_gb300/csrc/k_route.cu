@@ -43,7 +43,9 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kManyTokens = 2048;
 constexpr int kWarps = 4;      // tokens of a CTA
 constexpr float kNoScore = -745.f;  // e to this is 0 in 64 bits
-constexpr float kLowSum = 0x1p-100f;    // a sum of sigmoid's scores that are not taken as they are
+// Sum of the chosen sigmoid scores from which on they are taken as they are: scores with parts of
+// more than 2^-106 in it are then normal numbers.
+constexpr float kLowSum = 0x1p-20f;
 
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -100,7 +102,10 @@ __device__ __forceinline__ double logistic(double l) {
 // negative, as e^l itself may have few bits in fp32, or none.
 __device__ __forceinline__ float part_of_chosen(const RouteParams& p, float l, float top) {
   if (!p.sigmoid) return expf(l - top);
-  return top < 0.f ? expf(l - top) / (1.f + expf(l)) : logistic(l);
+  if (!(top < 0.f) || l == -INFINITY) return logistic(l);
+  const Two x = two_of(l, -top);  // (70, rounded, moves e^70 by 2^-18)
+  const float e = expf(x.h);
+  return fmaf(e, x.l, e) / (1.f + expf(l));
 }
 
 // a score as it is compared in fp32: e^x by the hardware exponential and the

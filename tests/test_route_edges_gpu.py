@@ -170,3 +170,16 @@ def test_a_token_does_not_depend_on_its_neighbours():
             got.append((expert[1::2].clone(), weight[1::2], d[1::2]))
         plan.free()
         assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("tokens,dtype", [(60, gf.GF_F32), (2100, gf.GF_BF16)])
+@pytest.mark.parametrize("base", [0.0, -8.0, -14.0, -20.0, -60.0, -80.0, -300.0])
+def test_small_parts_of_low_sigmoid_sums(tokens, dtype, base):
+    """Parts in the sum down to e^-70, of scores that fp32 holds in full, in part or not at all."""
+    experts, topk = 64, 8
+    logits = torch.full((tokens, experts), -INF, device="cuda")
+    logits[:, 3::8] = base - torch.tensor([0.0, 5.0, 10.0, 20.0, 30.0, 40.0, 60.0, 70.0], device="cuda") - 0.5 * randn(tokens, 8, seed=13).abs()
+    logits = logits.to(TDT[dtype])
+    expert = check_choice(logits, experts, topk, dtype, SIGMOID, True, 2.5)
+    rng = np.random.default_rng(14)
+    check_grad(logits, experts, expert, rng.standard_normal((tokens, topk)).astype(np.float32), dtype, SIGMOID, True, 2.5)
