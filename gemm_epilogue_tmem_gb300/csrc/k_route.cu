@@ -11,7 +11,7 @@
 // minimum and maximum alone, a pick is one warp-wide integer maximum and the lowest
 // lane that has it, and the lane that loses its best moves up the others. What bounds
 // it is instructions (some 950 a token of 256 experts in groups with a bias: 16384 tokens
-// 21 us; eight lanes a token, 128 experts of 16-bit logits: 250 and 7.1 us) and, for a
+// 22 us; eight lanes a token, 128 experts of 16-bit logits: 250 and 7.2 us) and, for a
 // token, latency (3 us).
 //
 // Experts are whole numbers, and scores may lie closer together than fp32, less the
